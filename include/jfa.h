@@ -6,7 +6,7 @@
  * backward, a broadcast-Q variant whose dQ is summed over the batch, a varlen
  * form with separate query / key lengths and grouped KV heads, and a split-KV
  * decode (one or a few query tokens per sequence) over a paged, grouped-query
- * KV cache.
+ * KV cache in bf16, or in 8 bits with the calls that fill and shorten it.
  *
  * Sources of the operations (web pages; cited by title and section):
  *  [JFA]  "Optimizing Jagged Flash Attention with TLX: The Road Toward SOTA FA4
@@ -356,6 +356,112 @@ typedef struct {
   void* main_kernel_events;   /* optional cudaEvent_t[2] around the split kernel */
 } jfa_decode_smallq_args;
 
+/* ------------------------------------------------------------------ 8-bit paged cache
+ * A paged KV cache held in 8 bits ([INF] PR 1999/2104, PR 2109: paging and FP8
+ * for inference; the pages give no format, the one here is this library's).
+ * k_cache and v_cache hold e4m3 codes, each block of `block_size` consecutive
+ * slots of a page and KV head with one fp32 scale; the value of a code is
+ *   e4m3(code) * scale[page][slot / block_size][head].
+ * block_size is 1, 2, 4, ..., 128 and divides page_size (1 = a scale per token);
+ * num_pages * page_size < 2^31. Token t of sequence b lives in page
+ * page_table[b][t / page_size], slot t % page_size. Scales must be positive;
+ * those that jfa_cache_append_fp8 and jfa_cache_evict_fp8 write are powers of
+ * two. head_dim is 64 or 128. Slots of a page past a sequence's length are never
+ * read and, but for codes of a block whose scale changes, never written.
+ *
+ * jfa_cache_append_fp8: the new tokens' K and V, packed by offsets, become the
+ * last tokens of their sequences: seqlens_k counts them already, so sequence b's
+ * n_b = new_offsets[b+1] - new_offsets[b] rows go to positions L_b - n_b ..
+ * L_b - 1 (n_b may be 0). For each block and head that receives tokens
+ *   need = the smallest power of two >= 2^-126 with max|x| / need <= 448,
+ * the maximum over the finite new values; the block's scale becomes need, or, if
+ * it holds older tokens, s' = max(its scale s, need), their codes being rewritten
+ * as e4m3(e4m3(code) * s / s') where s' > s. New codes are e4m3(x / scale),
+ * rounded to nearest even; infinities and NaN become NaN. Sequences of one call
+ * must not share a block that receives tokens. If weights is set, the entries
+ * at the new positions become 0. */
+typedef struct {
+  const void* k;              /* bf16 [total_new, kv_heads, head_dim] */
+  const void* v;              /* bf16 [total_new, kv_heads, head_dim] */
+  const int32_t* new_offsets; /* int32 [batch+1], device */
+  void* k_cache;              /* in/out: e4m3 [num_pages, page_size, kv_heads, head_dim] */
+  void* v_cache;              /* in/out: as k_cache */
+  float* k_scale;             /* in/out: fp32 [num_pages, page_size / block_size, kv_heads] */
+  float* v_scale;             /* in/out: as k_scale */
+  const int32_t* page_table;  /* int32 [batch, max_pages]; entries past ceil(L_b/page_size) are not read */
+  const int32_t* seqlens_k;   /* int32 [batch], new tokens included, <= max_pages*page_size */
+  int32_t batch, kv_heads, head_dim;
+  int32_t page_size, block_size, num_pages, max_pages;
+  int32_t total_new;          /* host: new_offsets[batch] */
+  int32_t max_new;            /* host: >= every n_b */
+  float* weights;             /* optional in/out: fp32 [batch, kv_heads, max_pages * page_size] */
+} jfa_cache_append_fp8_args;
+
+/* Decode over the 8-bit cache: the last q_len >= 1 tokens of each sequence
+ * attend to it as in jfa_decode_smallq (query token i sees keys
+ * j <= L_b - q_len + i; a row that sees no key gets O = 0, LSE = -inf), over the
+ * values that the codes and scales stand for. q_len x (q_heads / kv_heads) must
+ * be <= 16; the group may be any number up to that. The work is split evenly over
+ * the device whatever the lengths; there is no split count to choose.
+ * Attention weights: with weights_out set, for every t < L_b and KV head g
+ *   weights_out[b][g][t] = decay * weights[b][g][t] + sum of P over the group's
+ *   query heads and the q_len query tokens
+ * (the first term is left out if weights is NULL); entries past L_b are not
+ * written. weights and weights_out may be the same array. Codes that are NaN
+ * make NaN of the rows that see them, and of no others. */
+typedef struct {
+  const void* q;              /* bf16 [batch, q_len, q_heads, head_dim] */
+  const void* k_cache;        /* e4m3 [num_pages, page_size, kv_heads, head_dim] */
+  const void* v_cache;        /* as k_cache */
+  const float* k_scale;       /* fp32 [num_pages, page_size / block_size, kv_heads] */
+  const float* v_scale;       /* as k_scale */
+  const int32_t* page_table;  /* int32 [batch, max_pages] */
+  const int32_t* seqlens_k;   /* int32 [batch], 0 <= L_b <= max_pages*page_size, new tokens included */
+  int32_t batch, q_len, q_heads, kv_heads, head_dim;
+  int32_t page_size, block_size, num_pages, max_pages;
+  float scale;
+  void* o;                    /* out: bf16 [batch, q_len, q_heads, head_dim] */
+  float* lse;                 /* out: fp32 [batch, q_len, q_heads] */
+  const float* weights;       /* optional: fp32 [batch, kv_heads, max_pages * page_size] */
+  float* weights_out;         /* optional out: as weights */
+  float decay;                /* >= 0 (used with weights) */
+  void* main_kernel_events;   /* optional cudaEvent_t[2] around the main kernel */
+} jfa_decode_fp8_args;
+
+/* Eviction by accumulated attention weight: every sequence is cut to
+ *   new_seqlens[b] = min(L_b, keep) tokens.
+ * Each KV head keeps, in their old order, its first `first` and last `recent`
+ * tokens and, of the rest, those of the largest weights (equal weights: the lower
+ * position first; NaN counts as -infinity); a sequence of at most `keep` tokens
+ * keeps them all. Kept tokens go to the pages of new_page_table, as positions
+ * 0 .. new_seqlens[b] - 1, with the block scales that jfa_cache_append_fp8 gives
+ * values entering an empty block; their weights go along and the rest of
+ * new_weights becomes 0. kept lists the old positions (-1 past the end).
+ * The new pages in use (the first ceil(new_seqlens[b] / page_size) of a row) must
+ * not be pages that a sequence of the call still holds, and no page may be given
+ * out twice: such pages are not written, and the call reports JFA_ERR_BAD_INPUT.
+ * The old pages are left as they are. Heads may keep different tokens, so
+ * positions no longer agree between heads; attention does not depend on the order
+ * of the keys but for the q_len newest. */
+typedef struct {
+  void* k_cache;              /* in/out: e4m3 [num_pages, page_size, kv_heads, head_dim] */
+  void* v_cache;              /* in/out: as k_cache */
+  float* k_scale;             /* in/out: fp32 [num_pages, page_size / block_size, kv_heads] */
+  float* v_scale;             /* in/out: as k_scale */
+  const int32_t* page_table;  /* int32 [batch, max_pages] */
+  const int32_t* seqlens_k;   /* int32 [batch], 0 <= L_b <= max_pages*page_size */
+  const float* weights;       /* fp32 [batch, kv_heads, max_pages * page_size] */
+  const int32_t* new_page_table; /* int32 [batch, new_max_pages]; entries past the kept tokens are not read */
+  int32_t batch, kv_heads, head_dim;
+  int32_t page_size, block_size, num_pages, max_pages;
+  int32_t new_max_pages;      /* new_max_pages * page_size >= keep */
+  int32_t keep;               /* >= 1 */
+  int32_t first, recent;      /* >= 0, first + recent <= keep */
+  int32_t* kept;              /* out: int32 [batch, kv_heads, keep] */
+  int32_t* new_seqlens;       /* out: int32 [batch] (not seqlens_k itself) */
+  float* new_weights;         /* out: fp32 [batch, kv_heads, new_max_pages * page_size] (not weights itself) */
+} jfa_cache_evict_fp8_args;
+
 /* Workspace sizes in bytes (0 only when args is NULL). */
 JFA_API size_t jfa_fwd_workspace_size(const jfa_fwd_args* args);
 JFA_API size_t jfa_bwd_workspace_size(const jfa_bwd_args* args);
@@ -367,6 +473,9 @@ JFA_API size_t jfa_varlen_bwd_workspace_size(const jfa_varlen_bwd_args* args);
 JFA_API size_t jfa_decode_smallq_workspace_size(const jfa_decode_smallq_args* args);
 JFA_API size_t jfa_fwd_fp8_workspace_size(const jfa_fwd_fp8_args* args);
 JFA_API size_t jfa_fp8_quantize_v_workspace_size(const jfa_fp8_quantize_v_args* args);
+JFA_API size_t jfa_cache_append_fp8_workspace_size(const jfa_cache_append_fp8_args* args);
+JFA_API size_t jfa_decode_fp8_workspace_size(const jfa_decode_fp8_args* args);
+JFA_API size_t jfa_cache_evict_fp8_workspace_size(const jfa_cache_evict_fp8_args* args);
 /* Bytes of the V blocks for a batch (an upper bound: (ceil(total/128) + batch) x heads x 16384). */
 JFA_API size_t jfa_fp8_vt_bytes(int32_t batch, int32_t heads, int32_t total);
 
@@ -390,6 +499,13 @@ JFA_API jfa_status jfa_fwd_fp8(const jfa_fwd_fp8_args* args, void* workspace, si
                        cudaStream_t stream);
 JFA_API jfa_status jfa_fp8_quantize_v(const jfa_fp8_quantize_v_args* args, void* workspace, size_t workspace_bytes,
                               cudaStream_t stream);
+
+JFA_API jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* args, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+JFA_API jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* args, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+JFA_API jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* args, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
 
 /* Paged split-KV decode that allocates nothing. The pages have no
  * counterpart for this entry point; it exists for callers that cannot

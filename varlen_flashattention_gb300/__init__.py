@@ -16,6 +16,9 @@ kernels; there is no CPU or PyTorch fallback.
     jfa_decode_smallq     paged split-KV decode of a few query tokens per sequence -> (O, LSE)
     jfa_fwd_fp8           jagged forward over FP8 (e4m3) inputs with per-tensor descales -> (O, LSE)
     jfa_fp8_quantize_v    bf16 V -> e4m3 V in the layout jfa_fwd_fp8 reads (its vt argument)
+    jfa_cache_append_fp8  new tokens' K and V quantized into an 8-bit paged cache (block scales)
+    jfa_decode_fp8        decode over the 8-bit paged cache, with accumulated attention weights -> (O, LSE)
+    jfa_cache_evict_fp8   the tokens of the largest accumulated weights moved to new pages
     jfa_trace_enable      registers a per-role event trace buffer (JFA_TRACE builds; see trace.py)
     jfa_trace_compiled    1 if the loaded library records traces
     jagged_attention      autograd wrapper of jfa_fwd / jfa_bwd
@@ -36,6 +39,7 @@ __all__ = [
     "jfa_read_device_status", "jagged_attention", "library", "jfa_fwd_varlen", "jfa_bwd_varlen",
     "varlen_attention", "jfa_decode_smallq", "jfa_selftest_wait_timeout", "jfa_fwd_fp8",
     "jfa_trace_enable", "jfa_trace_compiled", "jfa_fp8_quantize_v",
+    "jfa_cache_append_fp8", "jfa_decode_fp8", "jfa_cache_evict_fp8",
 ]
 
 
@@ -504,6 +508,134 @@ def jfa_decode_smallq(q, k_cache, v_cache, page_table, seqlens_k, num_splits, mi
     a.main_kernel_events = ev
     _run("jfa_decode_smallq", "jfa_decode_smallq_workspace_size", a, dev, workspace, stream, check)
     return o, lse
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+
+def _codes(t, name, shape):
+    """The uint8 view of an e4m3 cache (torch.uint8 or torch.float8_e4m3fn)."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    _need(t, name, torch.uint8, shape)
+    return t
+
+
+def _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k):
+    """Shapes of an 8-bit cache and of the batch that reads it; the scales' second
+    dimension gives the block size."""
+    k_cache = _codes(k_cache, "k_cache", 4)
+    num_pages, P, Hkv, d = k_cache.shape
+    v_cache = _codes(v_cache, "v_cache", k_cache.shape)
+    _need(k_scale, "k_scale", torch.float32, 3)
+    blocks = k_scale.shape[1]
+    _need(k_scale, "k_scale", torch.float32, (num_pages, blocks, Hkv))
+    _need(v_scale, "v_scale", torch.float32, k_scale.shape)
+    if blocks < 1 or P % blocks != 0:
+        raise ValueError(f"k_scale must hold a divisor of the page size {P} in dimension 1, got {blocks}")
+    _need(seqlens_k, "seqlens_k", torch.int32, 1)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(page_table, "page_table", torch.int32, (seqlens_k.numel(), page_table.shape[1]))
+    return k_cache, v_cache, num_pages, P, P // blocks, Hkv, d
+
+
+def jfa_cache_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k, new_offsets, max_new,
+                         weights=None, workspace=None, stream=None, check=False):
+    """Quantizes the K and V rows of new tokens into an 8-bit paged cache, in place (see include/jfa.h).
+    k, v: bf16 [total_new, Hkv, d], sequence b's rows new_offsets[b] .. new_offsets[b+1]-1 becoming its
+    last tokens (seqlens_k counts them already); caches: e4m3 codes [num_pages, page_size, Hkv, d]
+    (torch.uint8 or torch.float8_e4m3fn); k_scale, v_scale: fp32 [num_pages, page_size / block, Hkv];
+    page_table int32 [B, max_pages]; seqlens_k int32 [B]; new_offsets int32 [B+1]; max_new >= every
+    sequence's count. weights (optional, fp32 [B, Hkv, max_pages * page_size]) is set to 0 at the new
+    positions. Returns (k_cache, v_cache, k_scale, v_scale)."""
+    kc, vc, num_pages, P, block, Hkv, d = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
+    B, mp = page_table.shape
+    _need(k, "k", torch.bfloat16, 3)
+    _need(k, "k", torch.bfloat16, (k.shape[0], Hkv, d))
+    _need(v, "v", torch.bfloat16, k.shape)
+    _need(new_offsets, "new_offsets", torch.int32, (B + 1,))
+    if weights is not None:
+        _need(weights, "weights", torch.float32, (B, Hkv, mp * P))
+    dev = _device(k=k, v=v, k_cache=kc, v_cache=vc, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+                  seqlens_k=seqlens_k, new_offsets=new_offsets, weights=weights)
+    a = _abi.CacheAppendFp8Args(_ptr(k), _ptr(v), _ptr(new_offsets), _ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale),
+                                _ptr(page_table), _ptr(seqlens_k), B, Hkv, d, P, block, num_pages, mp, k.shape[0],
+                                int(max_new), _ptr(weights))
+    _run("jfa_cache_append_fp8", "jfa_cache_append_fp8_workspace_size", a, dev, workspace, stream, check)
+    return k_cache, v_cache, k_scale, v_scale
+
+
+def jfa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k, scale=None, weights=None, decay=1.0,
+                   weights_out=None, o=None, lse=None, workspace=None, stream=None, events=None, check=False):
+    """Decode of the last q_len tokens of each sequence over an 8-bit paged cache. q: bf16
+    [B, q_len, Hq, d], q_len * Hq / Hkv <= 16; the cache as in jfa_cache_append_fp8; seqlens_k
+    counts the query tokens (token i sits at key position L - q_len + i and sees keys up to it).
+    weights (optional, fp32 [B, Hkv, max_pages * page_size]): weights_out = decay * weights + each
+    cached token's attention weight, summed over the group's query heads and the query tokens, for
+    the tokens of each sequence; weights is updated in place if weights_out is not given, and
+    weights_out alone receives the sums. Returns O bf16 [B, q_len, Hq, d], LSE fp32 [B, q_len, Hq]."""
+    _need(q, "q", torch.bfloat16, 4)
+    B, ql, Hq, _ = q.shape
+    kc, vc, num_pages, P, block, Hkv, d = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
+    _need(q, "q", torch.bfloat16, (seqlens_k.numel(), ql, Hq, d))
+    mp = page_table.shape[1]
+    if weights_out is None:
+        weights_out = weights
+    for n, t in (("weights", weights), ("weights_out", weights_out)):
+        if t is not None:
+            _need(t, n, torch.float32, (B, Hkv, mp * P))
+    if o is not None:
+        _need(o, "o", torch.bfloat16, q.shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, ql, Hq))
+    dev = _device(q=q, k_cache=kc, v_cache=vc, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+                  seqlens_k=seqlens_k, weights=weights, weights_out=weights_out, o=o, lse=lse)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((B, ql, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    a = _abi.DecodeFp8Args(_ptr(q), _ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                           _ptr(seqlens_k), B, ql, Hq, Hkv, d, P, block, num_pages, mp, scale, _ptr(o), _ptr(lse),
+                           _ptr(weights), _ptr(weights_out), float(decay), None)
+    ev, _keep = _events(events)
+    a.main_kernel_events = ev
+    _run("jfa_decode_fp8", "jfa_decode_fp8_workspace_size", a, dev, workspace, stream, check)
+    return o, lse
+
+
+def jfa_cache_evict_fp8(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k, weights, keep, new_page_table,
+                        first=0, recent=0, kept=None, new_seqlens=None, new_weights=None, workspace=None, stream=None,
+                        check=False):
+    """Cuts every sequence of an 8-bit paged cache to at most `keep` tokens: each KV head keeps its
+    first `first` and last `recent` tokens and the largest weights of the rest (ties: the lower
+    position), in order, in the pages of new_page_table (int32 [B, new_max_pages], room for `keep`
+    tokens a row, pages that no sequence of the call holds). weights: fp32 [B, Hkv, max_pages *
+    page_size], as jfa_decode_fp8 accumulates them. Returns kept int32 [B, Hkv, keep] (old positions,
+    -1 past the end), new_seqlens int32 [B] and new_weights fp32 [B, Hkv, new_max_pages * page_size]."""
+    kc, vc, num_pages, P, block, Hkv, d = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
+    B, mp = page_table.shape
+    keep = int(keep)
+    _need(weights, "weights", torch.float32, (B, Hkv, mp * P))
+    _need(new_page_table, "new_page_table", torch.int32, 2)
+    nmp = new_page_table.shape[1]
+    _need(new_page_table, "new_page_table", torch.int32, (B, nmp))
+    if keep < 1 or first < 0 or recent < 0 or first + recent > keep:
+        raise ValueError(f"keep must be >= 1 and first + recent at most keep, got {keep}, {first}, {recent}")
+    if nmp * P < keep:
+        raise ValueError(f"new_page_table holds {nmp * P} tokens a sequence, keep is {keep}")
+    shapes = (("kept", kept, torch.int32, (B, Hkv, keep)), ("new_seqlens", new_seqlens, torch.int32, (B,)),
+              ("new_weights", new_weights, torch.float32, (B, Hkv, nmp * P)))
+    for n, t, dtype, shape in shapes:
+        if t is not None:
+            _need(t, n, dtype, shape)
+    dev = _device(k_cache=kc, v_cache=vc, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+                  seqlens_k=seqlens_k, weights=weights, new_page_table=new_page_table, kept=kept,
+                  new_seqlens=new_seqlens, new_weights=new_weights)
+    kept, new_seqlens, new_weights = (torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+                                      for _, t, dtype, shape in shapes)
+    a = _abi.CacheEvictFp8Args(_ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(seqlens_k),
+                               _ptr(weights), _ptr(new_page_table), B, Hkv, d, P, block, num_pages, mp, nmp, keep,
+                               int(first), int(recent), _ptr(kept), _ptr(new_seqlens), _ptr(new_weights))
+    _run("jfa_cache_evict_fp8", "jfa_cache_evict_fp8_workspace_size", a, dev, workspace, stream, check)
+    return kept, new_seqlens, new_weights
 
 
 # ---------------------------------------------------------------- autograd

@@ -108,6 +108,34 @@ class Fp8QuantizeVArgs(ctypes.Structure):
                 ("max_seqlen", c_i32), ("total", c_i32), ("v_descale", c_f32), ("vt", c_void_p)]
 
 
+class CacheAppendFp8Args(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("new_offsets", c_void_p), ("k_cache", c_void_p),
+                ("v_cache", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("page_table", c_void_p),
+                ("seqlens_k", c_void_p),
+                ("batch", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("page_size", c_i32), ("block_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32),
+                ("total_new", c_i32), ("max_new", c_i32), ("weights", c_void_p)]
+
+
+class DecodeFp8Args(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("k_scale", c_void_p),
+                ("v_scale", c_void_p), ("page_table", c_void_p), ("seqlens_k", c_void_p),
+                ("batch", c_i32), ("q_len", c_i32), ("q_heads", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("page_size", c_i32), ("block_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32),
+                ("scale", c_f32), ("o", c_void_p), ("lse", c_void_p), ("weights", c_void_p),
+                ("weights_out", c_void_p), ("decay", c_f32), ("main_kernel_events", c_void_p)]
+
+
+class CacheEvictFp8Args(ctypes.Structure):
+    _fields_ = [("k_cache", c_void_p), ("v_cache", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("page_table", c_void_p), ("seqlens_k", c_void_p), ("weights", c_void_p),
+                ("new_page_table", c_void_p),
+                ("batch", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("page_size", c_i32), ("block_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32),
+                ("new_max_pages", c_i32), ("keep", c_i32), ("first", c_i32), ("recent", c_i32),
+                ("kept", c_void_p), ("new_seqlens", c_void_p), ("new_weights", c_void_p)]
+
+
 # (name, argtypes, restype) of every exported symbol declared in include/jfa.h
 SIGNATURES = [
     ("jfa_fwd_workspace_size", [ctypes.POINTER(FwdArgs)], ctypes.c_size_t),
@@ -120,6 +148,9 @@ SIGNATURES = [
     ("jfa_decode_smallq_workspace_size", [ctypes.POINTER(DecodeSmallqArgs)], ctypes.c_size_t),
     ("jfa_fwd_fp8_workspace_size", [ctypes.POINTER(FwdFp8Args)], ctypes.c_size_t),
     ("jfa_fp8_quantize_v_workspace_size", [ctypes.POINTER(Fp8QuantizeVArgs)], ctypes.c_size_t),
+    ("jfa_cache_append_fp8_workspace_size", [ctypes.POINTER(CacheAppendFp8Args)], ctypes.c_size_t),
+    ("jfa_decode_fp8_workspace_size", [ctypes.POINTER(DecodeFp8Args)], ctypes.c_size_t),
+    ("jfa_cache_evict_fp8_workspace_size", [ctypes.POINTER(CacheEvictFp8Args)], ctypes.c_size_t),
     ("jfa_fp8_vt_bytes", [c_i32, c_i32, c_i32], ctypes.c_size_t),
     ("jfa_fwd", [ctypes.POINTER(FwdArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_bwd", [ctypes.POINTER(BwdArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
@@ -131,6 +162,9 @@ SIGNATURES = [
     ("jfa_decode_smallq", [ctypes.POINTER(DecodeSmallqArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_fwd_fp8", [ctypes.POINTER(FwdFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_fp8_quantize_v", [ctypes.POINTER(Fp8QuantizeVArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
+    ("jfa_cache_append_fp8", [ctypes.POINTER(CacheAppendFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
+    ("jfa_decode_fp8", [ctypes.POINTER(DecodeFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
+    ("jfa_cache_evict_fp8", [ctypes.POINTER(CacheEvictFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_decode_splitkv_noalloc", [ctypes.POINTER(DecodeArgs), c_void_p], c_i32),
     ("jfa_decode_noalloc_status", [c_void_p, ctypes.POINTER(c_i32)], c_i32),
     ("jfa_read_device_status", [c_void_p, c_void_p, ctypes.POINTER(c_i32)], c_i32),

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -247,7 +248,80 @@ Layout decode_layout(int64_t batch, int64_t q_heads, int64_t splits) {
   return L;
 }
 
+// 8-bit cache decode: lengths, tile numbers, the parts' partial results and,
+// for the attention weights, the scores of every tile.
+struct Fp8DecodeLayout {
+  size_t lens = 0, tile_base = 0, part_o = 0, part_lse2 = 0, lse2 = 0, scores = 0, bytes = 0;
+};
+int64_t fp8_seq_tiles(int64_t max_pages, int64_t page_size) { return (max_pages * page_size + 15) / 16; }
+Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
+  Fp8DecodeLayout L;
+  const int64_t rows = a.kv_heads > 0 ? static_cast<int64_t>(a.q_heads / a.kv_heads) * a.q_len : 0;
+  const int64_t segs = static_cast<int64_t>(a.batch) * a.kv_heads;
+  const int64_t tiles = segs * fp8_seq_tiles(a.max_pages, a.page_size);
+  const int64_t parts = std::min<int64_t>(kFp8MaxParts, tiles) + segs;
+  size_t off = kStatusBytes;
+  L.lens = off;
+  off = align_up(off + 4 * static_cast<size_t>(a.batch), 256);
+  L.tile_base = off;
+  off = align_up(off + 4 * (static_cast<size_t>(a.batch) + 1), 256);
+  L.part_o = off;
+  off = align_up(off + 4 * parts * rows * a.head_dim, 256);
+  L.part_lse2 = off;
+  off = align_up(off + 4 * parts * rows, 256);
+  if (a.weights_out) {
+    L.lse2 = off;
+    off = align_up(off + 4 * segs * rows, 256);
+    L.scores = off;
+    off = align_up(off + 4 * tiles * rows * 16, 256);
+  }
+  L.bytes = off;
+  return L;
+}
+
+size_t fp8_evict_bytes(int64_t num_pages) { return align_up(kStatusBytes + 4 * static_cast<size_t>(num_pages), 256); }
+
 // ------------------------------------------------------------------ validation
+
+// What the three calls on the 8-bit cache have in common: the cache's own sizes and pointers.
+jfa_status check_fp8_cache(const void* kc, const void* vc, const float* ks, const float* vs, const int32_t* table,
+                           const int32_t* seqlens, int32_t batch, int32_t kv_heads, int32_t head_dim,
+                           int32_t page_size, int32_t block_size, int32_t num_pages, int32_t max_pages) {
+  if (batch < 0 || kv_heads < 1 || page_size < 1 || block_size < 1 || num_pages < 0 || max_pages < 0)
+    return JFA_ERR_INVALID_ARG;
+  if (page_size % block_size != 0) return JFA_ERR_INVALID_ARG;
+  if (block_size > 128 || (block_size & (block_size - 1)) != 0) return JFA_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return JFA_ERR_UNSUPPORTED;
+  if (kv_heads > 32767) return JFA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * page_size >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_pages) * page_size >= (int64_t(1) << 31) - 256) return JFA_ERR_INVALID_ARG;
+  if (batch > 0 && num_pages > 0 && (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4)))
+    return JFA_ERR_INVALID_ARG;
+  if (batch > 0 && (!aligned(seqlens, 4) || (max_pages > 0 && !aligned(table, 4)))) return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
+
+jfa_status check_decode_fp8(const jfa_decode_fp8_args* a) {
+  if (!a) return JFA_ERR_INVALID_ARG;
+  const jfa_status st = check_fp8_cache(a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->page_table, a->seqlens_k,
+                                        a->batch, a->kv_heads, a->head_dim, a->page_size, a->block_size, a->num_pages,
+                                        a->max_pages);
+  if (st != JFA_OK) return st;
+  if (a->q_len < 1 || a->q_heads < 1 || a->q_heads % a->kv_heads != 0) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->q_heads / a->kv_heads) * a->q_len > 16) return JFA_ERR_UNSUPPORTED;  // rows of one tile
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return JFA_ERR_INVALID_ARG;
+  if (a->batch > 0 && (!aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4))) return JFA_ERR_INVALID_ARG;
+  if (a->weights && !a->weights_out) return JFA_ERR_INVALID_ARG;
+  const bool has_weights = a->batch > 0 && a->max_pages > 0;
+  if (has_weights && a->weights_out && !aligned(a->weights_out, 4)) return JFA_ERR_INVALID_ARG;
+  if (has_weights && a->weights && (!aligned(a->weights, 4) || !(a->decay >= 0.f) || !std::isfinite(a->decay)))
+    return JFA_ERR_INVALID_ARG;
+  // rows of O and 16-token tiles are numbered with 32 bits
+  if (static_cast<int64_t>(a->batch) * a->q_len * a->q_heads >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->batch) * fp8_seq_tiles(a->max_pages, a->page_size) >= (int64_t(1) << 31))
+    return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
 
 jfa_status check_fwd(const jfa_fwd_args* a) {
   if (!a) return JFA_ERR_INVALID_ARG;
@@ -921,6 +995,88 @@ jfa_status jfa_decode_smallq(const jfa_decode_smallq_args* a, void* ws, size_t w
   return cuda_status(launch_decode_general(d, reinterpret_cast<float*>(w + L.part_o),
                                            reinterpret_cast<float*>(w + L.part_lse), reinterpret_cast<int32_t*>(w),
                                            stream));
+}
+
+size_t jfa_cache_append_fp8_workspace_size(const jfa_cache_append_fp8_args* a) { return a ? kStatusBytes : 0; }
+
+jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!a) return JFA_ERR_INVALID_ARG;
+  const jfa_status st = check_fp8_cache(a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->page_table, a->seqlens_k,
+                                        a->batch, a->kv_heads, a->head_dim, a->page_size, a->block_size, a->num_pages,
+                                        a->max_pages);
+  if (st != JFA_OK) return st;
+  if (a->total_new < 0 || a->max_new < 0) return JFA_ERR_INVALID_ARG;
+  if (a->batch > 0 && !aligned(a->new_offsets, 4)) return JFA_ERR_INVALID_ARG;
+  if (a->batch > 0 && a->total_new > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return JFA_ERR_INVALID_ARG;
+  if (a->weights && !aligned(a->weights, 4)) return JFA_ERR_INVALID_ARG;
+  // blocks of the grid: batch x chunks of 128 positions
+  if (static_cast<int64_t>(a->batch) * ((static_cast<int64_t>(a->max_new) + 126) / 128 + 1) >= (int64_t(1) << 31))
+    return JFA_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  int32_t* status = static_cast<int32_t*>(ws);
+  if (launch_status_clear(status, stream) != cudaSuccess) return JFA_ERR_CUDA;
+  if (a->batch == 0) return JFA_OK;
+  return cuda_status(launch_cache_append_fp8(*a, status, stream));
+}
+
+size_t jfa_decode_fp8_workspace_size(const jfa_decode_fp8_args* a) {
+  if (!a) return 0;
+  return fp8_decode_layout(*a).bytes;
+}
+
+jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const jfa_status st = check_decode_fp8(a);
+  if (st != JFA_OK) return st;
+  const Fp8DecodeLayout L = fp8_decode_layout(*a);
+  if (!aligned(ws, 256) || !events_ok(a->main_kernel_events)) return JFA_ERR_INVALID_ARG;
+  if (ws_bytes < L.bytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  if (a->batch == 0) return cuda_status(launch_status_clear(reinterpret_cast<int32_t*>(w), stream));
+  const int sms = sm_count();
+  if (sms <= 0) return JFA_ERR_CUDA;
+  const int64_t tiles = static_cast<int64_t>(a->batch) * a->kv_heads * fp8_seq_tiles(a->max_pages, a->page_size);
+  Fp8DecodeBuffers buf{};
+  buf.status = reinterpret_cast<int32_t*>(w);
+  buf.lens = reinterpret_cast<int32_t*>(w + L.lens);
+  buf.tile_base = reinterpret_cast<int32_t*>(w + L.tile_base);
+  buf.part_o = reinterpret_cast<float*>(w + L.part_o);
+  buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);
+  buf.lse2 = reinterpret_cast<float*>(w + L.lse2);
+  buf.scores = reinterpret_cast<float*>(w + L.scores);
+  buf.parts = static_cast<int32_t>(
+      std::max<int64_t>(1, std::min<int64_t>({fp8_decode_parts(sms), kFp8MaxParts, tiles})));
+  return cuda_status(launch_decode_fp8(*a, buf, sms, stream));
+}
+
+size_t jfa_cache_evict_fp8_workspace_size(const jfa_cache_evict_fp8_args* a) {
+  return a ? fp8_evict_bytes(a->num_pages > 0 ? a->num_pages : 0) : 0;
+}
+
+jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!a) return JFA_ERR_INVALID_ARG;
+  const jfa_status st = check_fp8_cache(a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->page_table, a->seqlens_k,
+                                        a->batch, a->kv_heads, a->head_dim, a->page_size, a->block_size, a->num_pages,
+                                        a->max_pages);
+  if (st != JFA_OK) return st;
+  if (a->keep < 1 || a->first < 0 || a->recent < 0 || a->new_max_pages < 0) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->first) + a->recent > a->keep) return JFA_ERR_INVALID_ARG;
+  const int64_t new_cap = static_cast<int64_t>(a->new_max_pages) * a->page_size;
+  if (new_cap < a->keep || new_cap >= (int64_t(1) << 31) - 256) return JFA_ERR_INVALID_ARG;
+  if (a->batch > 0 && (!aligned(a->new_page_table, 4) || !aligned(a->kept, 4) || !aligned(a->new_seqlens, 4) ||
+                       !aligned(a->new_weights, 4) || (a->max_pages > 0 && !aligned(a->weights, 4))))
+    return JFA_ERR_INVALID_ARG;
+  // other blocks still read what these would overwrite
+  if (a->batch > 0 && (a->new_seqlens == a->seqlens_k || a->new_weights == a->weights)) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->batch) * a->kv_heads >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(a->batch) * ((static_cast<int64_t>(a->keep) + 127) / 128) >= (int64_t(1) << 31))
+    return JFA_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
+  if (ws_bytes < fp8_evict_bytes(a->num_pages)) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  int32_t* status = static_cast<int32_t*>(ws);
+  if (a->batch == 0) return cuda_status(launch_status_clear(status, stream));
+  uint32_t* page_state = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  return cuda_status(launch_cache_evict_fp8(*a, page_state, status, stream));
 }
 
 jfa_status jfa_selftest_wait_timeout(int32_t budget_us, void* ws, cudaStream_t stream) {

@@ -91,6 +91,9 @@ enum WaitSite : int32_t {
   kSiteCheckBwdQ = 262,
   kSiteQueueOffsets = 301,
   kSiteDecodeTable = 401,
+  kSiteFp8DecodeTable = 411,  // 8-bit cache decode: a length or page entry out of range
+  kSiteFp8Append = 421,       // append: offsets, a length or a page entry out of range
+  kSiteFp8Evict = 431,        // evict: a length or page entry out of range, or a new page that is in use
   kSiteSelftestInput = 901,  // the self-test's first stage (its input never arrives)
   kSiteSelftestChain = 902,  // the self-test's second stage (should leave through the abort flag)
 };
@@ -226,6 +229,23 @@ struct DecodeLaunch {
 };
 cudaError_t launch_decode_general(const DecodeLaunch& a, float* part_o, float* part_lse, int32_t* status,
                                   cudaStream_t stream);
+// 8-bit paged cache: decode, append, evict.
+constexpr int kFp8MaxParts = 640;  // most parts the decode cuts its line of tiles into
+struct Fp8DecodeBuffers {
+  int32_t* status;
+  int32_t* lens;       // [B]
+  int32_t* tile_base;  // [B + 1]
+  float* part_o;       // [parts + B * kv_heads][rows][D]
+  float* part_lse2;    // [parts + B * kv_heads][rows]
+  float* lse2;         // [B * kv_heads][rows] (weights only)
+  float* scores;       // [B * kv_heads * tiles per sequence][rows][16] (weights only)
+  int32_t parts;
+};
+int fp8_decode_parts(int sms);
+cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream);
+cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t* status, cudaStream_t stream);
+cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status,
+                                   cudaStream_t stream);
 // Clears a call's status block (a kernel, not a memset, so that the call's next
 // kernel can start as its programmatic dependent).
 cudaError_t launch_status_clear(int32_t* status, cudaStream_t stream);
