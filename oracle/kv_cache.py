@@ -72,19 +72,24 @@ def gather(c, sc, row, L):
 
 def decode(q, kc, vc, ks, vs, table, seqlens, scale, weights=None, decay=1.0):
     """jfa_decode_fp8. Returns O, LSE, the new weights (a list of [Hkv, L] per sequence) and, per
-    output row, sum_j P_j |v_j| and max_j sum_d |q_d k_jd| * scale, from which errors are bounded."""
+    output row, sum_j P_j |v_j|, max_j sum_d |q_d k_jd| * scale and keys * max_j P_j * (scale of
+    v_j's block), from which errors are bounded."""
     B, ql, Hq, d = q.shape
     Hkv = kc.shape[2]
     G = Hq // Hkv
     O = np.zeros((B, ql, Hq, d))
     absO = np.zeros((B, ql, Hq, d))
     size = np.zeros((B, ql, Hq))
+    top = np.zeros((B, ql, Hq))
+    P, block = vc.shape[1], vc.shape[1] // vs.shape[1]
     LSE = np.full((B, ql, Hq), -np.inf)
     W = []
     for b in range(B):
         L = int(seqlens[b])
         K, V = gather(kc, ks, table[b], L), gather(vc, vs, table[b], L)
         w = np.zeros((Hkv, L))
+        t = np.arange(L)
+        vscale = vs[np.asarray(table[b])[t // P].astype(np.int64), t % P // block].astype(np.float64)
         for i in range(ql):
             see = max(0, L - ql + i + 1)
             if not see:
@@ -99,12 +104,13 @@ def decode(q, kc, vc, ks, vs, table, seqlens, scale, weights=None, decay=1.0):
                 O[b, i, h] = p @ Vh
                 absO[b, i, h] = p @ np.abs(Vh)
                 size[b, i, h] = scale * np.max(np.abs(Kh) @ np.abs(q[b, i, h]))
+                top[b, i, h] = see * np.max(p * vscale[:see, h // G])
                 LSE[b, i, h] = m + np.log(z)
                 w[h // G, :see] += p
         if weights is not None:
             w = w + decay * weights[b, :, :L].astype(np.float64)
         W.append(w)
-    return O, LSE, W, absO, size
+    return O, LSE, W, absO, size, top
 
 
 def evict(kc, vc, ks, vs, table, seqlens, weights, keep, new_table, first=0, recent=0):

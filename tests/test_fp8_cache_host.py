@@ -50,7 +50,7 @@ def test_oracle_decode_is_attention_over_the_values():
     kc, vc, ks, vs = _cache(rng, 4, 8, 4, 1, 16)
     table, L = np.array([[2, 0, 3]]), 19
     q = rng.standard_normal((1, L, 1, 16))  # every token a query: causal self-attention
-    O, LSE, W, _, _ = kvo.decode(q, kc, vc, ks, vs, table, [L], 0.25, weights=np.ones((1, 1, 24)), decay=0.5)
+    O, LSE, W, _, _, _ = kvo.decode(q, kc, vc, ks, vs, table, [L], 0.25, weights=np.ones((1, 1, 24)), decay=0.5)
     K, V = kvo.gather(kc, ks, table[0], L), kvo.gather(vc, vs, table[0], L)
     Oa, La = attention_forward(q[0], K, V, [0, L], 0.25, True)
     assert np.allclose(O[0], Oa, atol=1e-12) and np.allclose(LSE[0].T, La, atol=1e-12)

@@ -12,7 +12,11 @@ are derived per output row from the arithmetic, with u = 2^-24:
   * O: weights carry the scores' error twice (numerator, denominator) and one
     rounding to fp16, half a step 2^-11; the sum and the joins of the parts add
     far less than 2^-13 together; the bf16 result rounds by half a step 2^-8:
-    |dO| <= (2^-11 + 2^-13 + 2 |ds|) sum_j P_j |v_j| + 2^-8 |O|;
+    |dO| <= (2^-11 + 2^-13 + 2 |ds|) sum_j P_j |v_j| + 2^-8 |O|. That half step is
+    relative down to fp16's smallest normal number; below it is 2^-25 absolute. A
+    weight is held as w_j = P_j vs_j / r with r at most 2^-7 of the largest P_j vs_j
+    (vs: the scale of the value's block), so a key adds at most 2^-25 * 448 * r <=
+    2^-32 * 448 * max_j P_j vs_j more, and all L keys L times that;
   * a token's weight, in fp32: (2 |ds| + 2^-20) of itself.
 """
 import numpy as np
@@ -75,11 +79,12 @@ def _same_codes(a, b):
 
 
 def check_decode(c, q, o, lse, scale, w_in=None, w_out=None, w_was=None, decay=1.0, what=""):
-    O, LSE, W, absO, A = kvo.decode(np64(q), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["lens"], scale,
+    O, LSE, W, absO, A, top = kvo.decode(np64(q), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], c["lens"], scale,
                                     w_in, decay)
     ds = (c["d"] + 8) * 2.0 ** -23 * A + 2.0 ** -20
     o, lse = np64(o), np64(lse)
-    bound = (2.0 ** -11 + 2.0 ** -13 + 2 * ds)[..., None] * absO + 2.0 ** -8 * np.abs(O)
+    bound = (2.0 ** -11 + 2.0 ** -13 + 2 * ds)[..., None] * absO + 2.0 ** -8 * np.abs(O) + \
+        (448 * 2.0 ** -32 * top)[..., None]
     assert (np.isnan(o) == np.isnan(O)).all(), what
     bad = ~(np.abs(o - O) <= bound) & ~np.isnan(O)
     assert not bad.any(), f"{what}: O off by {np.nanmax(np.abs(o - O) - bound):.3e} over its bound at {np.argwhere(bad)[:3]}"
