@@ -248,21 +248,21 @@ Layout decode_layout(int64_t batch, int64_t q_heads, int64_t splits) {
   return L;
 }
 
-// 8-bit cache decode: lengths, tile numbers, the parts' partial results and,
+// 8-bit cache decode: findings, tile numbers, the parts' partial results and,
 // for the attention weights, the scores of every tile.
 struct Fp8DecodeLayout {
-  size_t lens = 0, tile_base = 0, part_o = 0, part_lse2 = 0, lse2 = 0, scores = 0, bytes = 0;
+  size_t errors = 0, tile_base = 0, part_o = 0, part_lse2 = 0, lse2 = 0, scores = 0, bytes = 0;
 };
-int64_t fp8_seq_tiles(int64_t max_pages, int64_t page_size) { return (max_pages * page_size + 15) / 16; }
 Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
   Fp8DecodeLayout L;
   const int64_t rows = a.kv_heads > 0 ? static_cast<int64_t>(a.q_heads / a.kv_heads) * a.q_len : 0;
   const int64_t segs = static_cast<int64_t>(a.batch) * a.kv_heads;
-  const int64_t tiles = segs * fp8_seq_tiles(a.max_pages, a.page_size);
-  const int64_t parts = std::min<int64_t>(kFp8MaxParts, tiles) + segs;
+  const int64_t tiles = static_cast<int64_t>(a.batch) * fp8_seq_tiles(a.max_pages, a.page_size);
+  const int64_t most = a.kv_heads > 0 ? std::max(1, kFp8MaxWarps / a.kv_heads) : 0;
+  const int64_t parts = std::min(most, tiles) * a.kv_heads + segs;  // of one head each
   size_t off = kStatusBytes;
-  L.lens = off;
-  off = align_up(off + 4 * static_cast<size_t>(a.batch), 256);
+  L.errors = off;
+  off = align_up(off + 4 * (1 + kFp8MaxWarps), 256);
   L.tile_base = off;
   off = align_up(off + 4 * (static_cast<size_t>(a.batch) + 1), 256);
   L.part_o = off;
@@ -273,7 +273,7 @@ Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
     L.lse2 = off;
     off = align_up(off + 4 * segs * rows, 256);
     L.scores = off;
-    off = align_up(off + 4 * tiles * rows * 16, 256);
+    off = align_up(off + 4 * tiles * a.kv_heads * rows * 16, 256);
   }
   L.bytes = off;
   return L;
@@ -1035,17 +1035,14 @@ jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* a, void* ws, size_t ws_byte
   if (a->batch == 0) return cuda_status(launch_status_clear(reinterpret_cast<int32_t*>(w), stream));
   const int sms = sm_count();
   if (sms <= 0) return JFA_ERR_CUDA;
-  const int64_t tiles = static_cast<int64_t>(a->batch) * a->kv_heads * fp8_seq_tiles(a->max_pages, a->page_size);
   Fp8DecodeBuffers buf{};
   buf.status = reinterpret_cast<int32_t*>(w);
-  buf.lens = reinterpret_cast<int32_t*>(w + L.lens);
+  buf.errors = reinterpret_cast<int32_t*>(w + L.errors);
   buf.tile_base = reinterpret_cast<int32_t*>(w + L.tile_base);
   buf.part_o = reinterpret_cast<float*>(w + L.part_o);
   buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);
   buf.lse2 = reinterpret_cast<float*>(w + L.lse2);
   buf.scores = reinterpret_cast<float*>(w + L.scores);
-  buf.parts = static_cast<int32_t>(
-      std::max<int64_t>(1, std::min<int64_t>({fp8_decode_parts(sms), kFp8MaxParts, tiles})));
   return cuda_status(launch_decode_fp8(*a, buf, sms, stream));
 }
 

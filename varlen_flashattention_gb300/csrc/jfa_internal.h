@@ -230,18 +230,18 @@ struct DecodeLaunch {
 cudaError_t launch_decode_general(const DecodeLaunch& a, float* part_o, float* part_lse, int32_t* status,
                                   cudaStream_t stream);
 // 8-bit paged cache: decode, append, evict.
-constexpr int kFp8MaxParts = 640;  // most parts the decode cuts its line of tiles into
+constexpr int kFp8MaxWarps = 2560;  // most warps of the decode's main kernel
 struct Fp8DecodeBuffers {
   int32_t* status;
-  int32_t* lens;       // [B]
+  int32_t* errors;     // [1 + kFp8MaxWarps]
   int32_t* tile_base;  // [B + 1]
-  float* part_o;       // [parts + B * kv_heads][rows][D]
-  float* part_lse2;    // [parts + B * kv_heads][rows]
+  float* part_o;       // [parts + B][kv_heads][rows][D]
+  float* part_lse2;    // [parts + B][kv_heads][rows]
   float* lse2;         // [B * kv_heads][rows] (weights only)
-  float* scores;       // [B * kv_heads * tiles per sequence][rows][16] (weights only)
-  int32_t parts;
+  float* scores;       // [B * tiles per sequence][kv_heads][rows][16] (weights only)
 };
-int fp8_decode_parts(int sms);
+// 16-token tiles of a sequence that fills its row of the page table.
+inline int64_t fp8_seq_tiles(int64_t max_pages, int64_t page_size) { return (max_pages * page_size + 15) / 16; }
 cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t* status, cudaStream_t stream);
 cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status,
