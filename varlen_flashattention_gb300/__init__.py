@@ -26,7 +26,6 @@ kernels; there is no CPU or PyTorch fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -55,7 +54,7 @@ def library():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, dtype, shape):
@@ -63,6 +62,9 @@ def _need(t, name, dtype, shape):
     layout of one argument. The kernels address every tensor from the shapes
     of q (and k), so each buffer is checked against them here; the device is
     checked by _device once every tensor of the call is known."""
+    if type(t) is torch.Tensor and t.dtype is dtype and (t.dim() if type(shape) is int else t.shape) == shape and \
+            t.is_contiguous():
+        return  # the usual case; what follows names what is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -100,8 +102,11 @@ def _device(**tensors):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The cudaStream_t of a torch stream, by default the current one (asked for by its
+    handle: building torch's stream object costs several microseconds a call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _events(events):
@@ -130,17 +135,35 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+_entries = {}  # the library's functions by name
+
+
+def _entry(name):
+    f = _entries.get(name)
+    if f is None:
+        f = _entries[name] = getattr(library(), name)
+    return f
+
+
 def _run(entry, size_entry, a, device, workspace, stream, check):
     """Sizes the workspace, calls the entry point on `device` and its stream,
     and with check=True reads the device status back (a stream sync)."""
-    lib = library()
-    here = device.index == torch.cuda.current_device()
-    with contextlib.nullcontext() if here else torch.cuda.device(device):
-        if stream is not None and stream.device_index != device.index:
-            raise ValueError(f"stream belongs to {stream.device}, the call runs on {device}")
-        ws = _workspace(getattr(lib, size_entry)(ctypes.byref(a)), device, workspace)
-        _check(getattr(lib, entry)(ctypes.byref(a), _ptr(ws), _nbytes(ws), _stream(stream)), entry)
-        _finish(ws, check, stream, entry)
+    if device.index == torch.cuda.current_device():
+        _run_here(entry, size_entry, a, device, workspace, stream, check)
+    else:
+        with torch.cuda.device(device):
+            _run_here(entry, size_entry, a, device, workspace, stream, check)
+
+
+def _run_here(entry, size_entry, a, device, workspace, stream, check):
+    if stream is not None and stream.device_index != device.index:
+        raise ValueError(f"stream belongs to {stream.device}, the call runs on {device}")
+    ref = ctypes.byref(a)
+    ws = _workspace(_entry(size_entry)(ref), device, workspace)
+    if stream is not None and workspace is None:
+        ws.record_stream(stream)  # allocated on the current stream, used on this one
+    _check(_entry(entry)(ref, ws.data_ptr(), _nbytes(ws), _stream(stream)), entry)
+    _finish(ws, check, stream, entry)
 
 
 def _check(status, where):
