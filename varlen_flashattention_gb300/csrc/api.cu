@@ -1009,9 +1009,9 @@ jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* a, void* ws, si
   if (a->batch > 0 && !aligned(a->new_offsets, 4)) return JFA_ERR_INVALID_ARG;
   if (a->batch > 0 && a->total_new > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return JFA_ERR_INVALID_ARG;
   if (a->weights && !aligned(a->weights, 4)) return JFA_ERR_INVALID_ARG;
-  // blocks of the grid: batch x chunks of 128 positions
-  if (static_cast<int64_t>(a->batch) * ((static_cast<int64_t>(a->max_new) + 126) / 128 + 1) >= (int64_t(1) << 31))
-    return JFA_ERR_INVALID_ARG;
+  // blocks of the grid: batch x chunks of 128 positions x heads, K and V
+  const double blocks = static_cast<double>(a->batch) * ((static_cast<int64_t>(a->max_new) + 126) / 128 + 1) * 2 * a->kv_heads;
+  if (blocks >= 2147483648.0) return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
   if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
   int32_t* status = static_cast<int32_t*>(ws);
@@ -1065,8 +1065,9 @@ jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size
     return JFA_ERR_INVALID_ARG;
   // other blocks still read what these would overwrite
   if (a->batch > 0 && (a->new_seqlens == a->seqlens_k || a->new_weights == a->weights)) return JFA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(a->batch) * a->kv_heads >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(a->batch) * ((static_cast<int64_t>(a->keep) + 127) / 128) >= (int64_t(1) << 31))
+  // blocks of the grids: batch x heads x chunks of 128 kept tokens, or up to 8 of the selection
+  const double segs = static_cast<double>(a->batch) * a->kv_heads;
+  if (segs * std::max<int64_t>(8, (static_cast<int64_t>(a->keep) + 127) / 128) >= 2147483648.0)
     return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
   if (ws_bytes < fp8_evict_bytes(a->num_pages)) return JFA_ERR_WORKSPACE_TOO_SMALL;

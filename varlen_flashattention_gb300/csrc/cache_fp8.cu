@@ -80,7 +80,7 @@ __device__ __forceinline__ void decode8(uint2 codes, float s, float (&x)[8]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendParams p) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(const Fp8AppendParams p) {
   constexpr int kLanes = D / 8;              // threads of a row, 8 values each
   constexpr int kRowsPerPass = kThreads / kLanes;
   constexpr int kPasses = kChunk / kRowsPerPass;
@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(kThreads) fp8_append_kernel(const Fp8AppendPar
   __shared__ float s_new[kChunk], s_old[kChunk];
 
   wait_prior_grid();  // the cleared status block
-  const int b = blockIdx.x / p.chunks, ci = blockIdx.x % p.chunks;
-  const int h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
   const int hkv = p.c.hkv;
+  const int h = blockIdx.x % (2 * hkv) >> 1;  // heads first: their rows are neighbours in memory
+  const bool is_v = blockIdx.x & 1;
+  const int b = blockIdx.x / (2 * hkv) / p.chunks, ci = blockIdx.x / (2 * hkv) % p.chunks;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
   // offsets rise from 0 to total_new, and the new tokens are part of the length
@@ -214,8 +214,8 @@ cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t*
   p.chunks = static_cast<int32_t>((static_cast<int64_t>(a.max_new) + kChunk - 2) / kChunk + 1);
   p.weights = a.weights;
   p.status = status;
-  const dim3 grid(static_cast<uint32_t>(p.batch) * static_cast<uint32_t>(p.chunks),
-                  static_cast<uint32_t>(a.kv_heads) * 2);
+  const dim3 grid(static_cast<uint32_t>(p.batch) * static_cast<uint32_t>(p.chunks) *
+                  (2 * static_cast<uint32_t>(a.kv_heads)));
   return a.head_dim == 128 ? launch_after(fp8_append_kernel<128>, grid, dim3(kThreads), 0, stream, p)
                            : launch_after(fp8_append_kernel<64>, grid, dim3(kThreads), 0, stream, p);
 }
@@ -264,40 +264,87 @@ __device__ __forceinline__ int block_exclusive_sum(int x, int32_t* warp_sum, int
   __syncthreads();  // warp_sum may still be read from an earlier call
   if (lane == 31) warp_sum[warp] = y;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    const int s = warp_sum[w];
-    before += w < warp ? s : 0;
-    all += s;
+  int v = warp_sum[lane];  // kSelThreads / 32 = 32 warps, one sum a lane
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += z;
   }
-  *total = all;
-  return before + y - x;
+  *total = __shfl_sync(0xffffffffu, v, 31);
+  const int before = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+  return (warp > 0 ? before : 0) + y - x;
 }
 
-// One block per (sequence, KV head): what stays, in order.
-__global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const Fp8EvictParams p) {
-  __shared__ int32_t hist[2048];
-  __shared__ int32_t warp_sum[32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int32_t s_need;
+// What stays of one sequence and KV head, in order: a cluster of blocks, each with a run of the
+// candidates, whose keys it reads once and keeps in shared memory (the first
+// kSelKeys of a run; the rest is read again for every pass). The blocks'
+// digit counts are added through distributed shared memory, so each finds
+// the same digits; then they write their own survivors, placed by the numbers of survivors
+// before them. What the passes cost is latency, not bytes: about 16 keys a
+// thread is where more blocks stop paying (a sequence of 131,071 tokens:
+// 240 us with one block re-reading its keys, see the launcher for the cluster sizes).
+struct SelShared {
+  int32_t hist[3][2048];
+  int32_t warp_sum[32];
+  int32_t count[2];  // survivors above the threshold, candidates that equal it
+  uint32_t prefix;
+  int32_t need;
+};
+constexpr int kSelKeys = 40960;
+
+__global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  __shared__ SelShared sh;
   wait_prior_grid();
   allow_next_grid();
-  const int b = blockIdx.x / p.c.hkv, h = blockIdx.x % p.c.hkv;
+  const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0;
+  const int seg = blockIdx.x / cluster;
+  const int b = seg / p.c.hkv, h = seg % p.c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int64_t new_cap = static_cast<int64_t>(p.new_max_pages) * p.page_size;
+  const int64_t wide = static_cast<int64_t>(cluster) * kSelThreads;  // threads of the cluster
+  const int64_t wtid = static_cast<int64_t>(rank) * kSelThreads + tid;
   int L = p.seqlens[b];
   if (L < 0 || L > cap || (L > 0 && p.c.num_pages == 0)) {
     if (tid == 0) flag_bad_cache(p.status, kSiteFp8Evict);
     L = 0;
   }
   const int n = min(L, p.keep);
-  const float* w = p.weights + static_cast<int64_t>(blockIdx.x) * cap;
-  int32_t* kept = p.kept + static_cast<int64_t>(blockIdx.x) * p.keep;
-  float* nw = p.new_weights + static_cast<int64_t>(blockIdx.x) * new_cap;
-  if (h == 0) {
+  const float* w = p.weights + seg * cap;
+  int32_t* kept = p.kept + static_cast<int64_t>(seg) * p.keep;
+  float* nw = p.new_weights + seg * new_cap;
+
+  // the candidates: this block's run of them
+  const bool choose = L > p.keep && p.keep > p.first + p.recent;
+  const int c0 = p.first, c1 = max(L - p.recent, c0);
+  const int run = choose ? ((c1 - c0 + cluster - 1) / cluster + 31) / 32 * 32 : 0;
+  const int r0 = min(c0 + static_cast<int>(rank) * run, c1), r1 = min(r0 + run, c1);
+  const int nrun = choose ? r1 - r0 : 0, nkeys = min(nrun, kSelKeys);
+  for (int i = tid; i < 3 * 2048; i += kSelThreads) sh.hist[0][i] = 0;
+  __syncthreads();
+  // keys, and the counts of their first digits
+#pragma unroll 1
+  for (int i0 = 0; i0 < nrun; i0 += 8 * kSelThreads) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kSelThreads + tid;
+      x[k] = i < nrun ? __ldg(w + r0 + i) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kSelThreads + tid;
+      if (i < nrun) {
+        const uint32_t key = weight_key(x[k]);
+        if (i < kSelKeys) s_keys[i] = key;
+        atomicAdd(&sh.hist[0][key >> 21], 1);
+      }
+    }
+  }
+  // meanwhile: pages read by this sequence and pages it will write
+  if (h == 0 && rank == 0) {
     if (tid == 0) p.new_seqlens[b] = n;
-    // pages read by this sequence and pages it will write
     const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
     const int32_t* nt = p.new_table + static_cast<int64_t>(b) * p.new_max_pages;
     const int used = L > 0 ? fast_div(L - 1, p.c.page) + 1 : 0, fresh = n > 0 ? fast_div(n - 1, p.c.page) + 1 : 0;
@@ -310,110 +357,138 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
       if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicAdd(p.page_state + pg, 1u);
     }
   }
-  for (int64_t j = n + tid; j < p.keep; j += kSelThreads) kept[j] = -1;
-  for (int64_t j = n + tid; j < new_cap; j += kSelThreads) nw[j] = 0.f;
-  if (L <= p.keep) {
-    for (int j = tid; j < n; j += kSelThreads) {
-      kept[j] = j;
+  for (int64_t j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
+  for (int64_t j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
+  if (L <= p.keep) {  // the same in all blocks of the cluster
+    for (int64_t j = wtid; j < n; j += wide) {
+      kept[j] = static_cast<int32_t>(j);
       nw[j] = w[j];
     }
     return;
   }
-  const int c0 = p.first, c1 = L - p.recent;           // candidates
-  const int want = p.keep - p.first - p.recent;        // of which this many stay, 0 <= want < c1 - c0
-  // The want-th largest key, digit by digit (11, 11 and 10 bits from the top).
-  uint32_t prefix = 0;
-  int need = want;  // how many keys with the prefix found so far stay
-  if (want > 0) {
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);  // the prefix's bits end here
-      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int t0 = c0 + warp * 32; t0 < c1; t0 += kSelThreads) {
-        uint32_t d = 2048;  // no digit
-        if (t0 + lane < c1) {
-          const uint32_t k = weight_key(w[t0 + lane]);
-          if (pass == 0 || (k >> above) == prefix) d = (k >> shift) & mask;
-        }
-        // equal digits of a warp count once: caches of mostly equal weights are common
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        if (d < 2048 && lane == __ffs(same) - 1) atomicAdd(&hist[d], __popc(same));
-      }
-      __syncthreads();
-      // bins from the top: thread t holds bins 2047 - 2 t and 2046 - 2 t
-      const int h0 = hist[2047 - 2 * tid], h1 = hist[2046 - 2 * tid];
-      int all;
-      const int before = block_exclusive_sum(h0 + h1, warp_sum, &all);
-      if (before < need && before + h0 + h1 >= need) {
-        const bool upper = before + h0 >= need;
-        const uint32_t d = upper ? 2047 - 2 * tid : 2046 - 2 * tid;
-        s_prefix = pass == 2 ? (prefix << 10) | d : (prefix << 11) | d;
-        s_need = need - before - (upper ? 0 : h0);
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
-    }
-  }
-  // keys above `prefix` stay, and the first `need` that equal it
-  for (int j = tid; j < p.first; j += kSelThreads) {
-    kept[j] = j;
+  for (int64_t j = wtid; j < p.first; j += wide) {
+    kept[j] = static_cast<int32_t>(j);
     nw[j] = w[j];
   }
-  for (int j = tid; j < p.recent; j += kSelThreads) {
-    kept[p.keep - p.recent + j] = c1 + j;
+  for (int64_t j = wtid; j < p.recent; j += wide) {
+    kept[p.keep - p.recent + j] = static_cast<int32_t>(c1 + j);
     nw[p.keep - p.recent + j] = w[c1 + j];
   }
-  if (want == 0) return;
-  const int per_warp = (c1 - c0 + kSelThreads - 1) / kSelThreads * 32;  // a run of candidates for each warp
-  const int lo = min(c0 + warp * per_warp, c1), hi = min(lo + per_warp, c1);
-  int gt = 0, eq = 0;
-  for (int t = lo; t < hi; t += 32) {
-    const uint32_t k = t + lane < hi ? weight_key(w[t + lane]) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, t + lane < hi && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, t + lane < hi && k == prefix));
+  if (!choose) return;
+
+  auto cluster_sync = [&] {
+    if (cluster > 1) {
+      asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  };
+  auto remote = [&](const int32_t* local, uint32_t r) -> int32_t {  // the same variable of block r
+    uint32_t at;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(local)), "r"(r));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+  };
+  auto key_at = [&](int i) -> uint32_t { return i < nkeys ? s_keys[i] : weight_key(__ldg(w + r0 + i)); };
+
+  // The want-th largest key, digit by digit (11, 11 and 10 bits from the top).
+  uint32_t prefix = 0;
+  int need = p.keep - p.first - p.recent;  // how many keys with the prefix found so far stay
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    int32_t* hist = sh.hist[pass];
+    if (pass > 0) {
+      const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
+      const uint32_t mask = pass == 1 ? 2047u : 1023u;
+      for (int i = tid; i < nrun; i += kSelThreads) {
+        const uint32_t key = key_at(i);
+        if ((key >> above) == prefix) atomicAdd(&hist[(key >> shift) & mask], 1);
+      }
+    }
+    cluster_sync();
+    // bins from the top: thread t holds bins 2047 - 2 t and 2046 - 2 t
+    int h0 = 0, h1 = 0;
+    if (cluster == 1) {
+      h0 = hist[2047 - 2 * tid];
+      h1 = hist[2046 - 2 * tid];
+    } else {
+      for (uint32_t r = 0; r < static_cast<uint32_t>(cluster); ++r) {
+        h0 += remote(hist + 2047 - 2 * tid, r);
+        h1 += remote(hist + 2046 - 2 * tid, r);
+      }
+    }
+    int all;
+    const int before = block_exclusive_sum(h0 + h1, sh.warp_sum, &all);
+    if (before < need && before + h0 + h1 >= need) {
+      const bool upper = before + h0 >= need;
+      const uint32_t d = upper ? 2047 - 2 * tid : 2046 - 2 * tid;
+      sh.prefix = pass == 2 ? (prefix << 10) | d : (prefix << 11) | d;
+      sh.need = need - before - (upper ? 0 : h0);
+    }
+    __syncthreads();
+    prefix = sh.prefix;
+    need = sh.need;
+    __syncthreads();
   }
-  int all;
-  int gt0 = block_exclusive_sum(lane == 0 ? gt : 0, warp_sum, &all);
-  int eq0 = block_exclusive_sum(lane == 0 ? eq : 0, warp_sum, &all);
+  // keys above `prefix` stay, and the first `need` that equal it; each warp has a run of the block's run
+  const int per_warp = (nrun + kSelThreads - 1) / kSelThreads * 32;
+  const int lo = min(warp * per_warp, nrun), hi = min(lo + per_warp, nrun);
+  int gt = 0, eq = 0;
+  for (int i = lo; i < hi; i += 32) {
+    const uint32_t key = i + lane < hi ? key_at(i + lane) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i + lane < hi && key > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, i + lane < hi && key == prefix));
+  }
+  int all_gt, all_eq;
+  int gt0 = block_exclusive_sum(lane == 0 ? gt : 0, sh.warp_sum, &all_gt);
+  int eq0 = block_exclusive_sum(lane == 0 ? eq : 0, sh.warp_sum, &all_eq);
   gt0 = __shfl_sync(0xffffffffu, gt0, 0);
   eq0 = __shfl_sync(0xffffffffu, eq0, 0);
+  if (cluster > 1) {
+    if (tid == 0) {
+      sh.count[0] = all_gt;
+      sh.count[1] = all_eq;
+    }
+    cluster_sync();
+    for (uint32_t r = 0; r < rank; ++r) {
+      gt0 += remote(sh.count, r);
+      eq0 += remote(sh.count + 1, r);
+    }
+  }
   const uint32_t below = (1u << lane) - 1;
-  for (int t = lo; t < hi; t += 32) {
-    const float x = t + lane < hi ? w[t + lane] : 0.f;
-    const uint32_t k = weight_key(x);
-    const uint32_t mg = __ballot_sync(0xffffffffu, t + lane < hi && k > prefix);
-    const uint32_t me = __ballot_sync(0xffffffffu, t + lane < hi && k == prefix);
+  for (int i = lo; i < hi; i += 32) {
+    const uint32_t key = i + lane < hi ? key_at(i + lane) : 0u;
+    const uint32_t mg = __ballot_sync(0xffffffffu, i + lane < hi && key > prefix);
+    const uint32_t me = __ballot_sync(0xffffffffu, i + lane < hi && key == prefix);
     const int eq_rank = eq0 + __popc(me & below);
-    const bool mine = ((mg >> lane) & 1) || (((me >> lane) & 1) && eq_rank < need);
-    if (mine) {
+    if (((mg >> lane) & 1) || (((me >> lane) & 1) && eq_rank < need)) {
       const int j = p.first + gt0 + __popc(mg & below) + min(eq_rank, need);
-      kept[j] = t + lane;
-      nw[j] = x;
+      kept[j] = r0 + i + lane;
+      nw[j] = w[r0 + i + lane];
     }
     gt0 += __popc(mg);
     eq0 += __popc(me);
   }
+  if (cluster > 1) cluster_sync();  // no block leaves while another may still read its counts
 }
 
-// Moves the kept rows of 128 new positions of one head's K or V.
+// Moves the kept rows of 128 new positions of one head, K and V: the two share
+// the chain of loads that finds a row (kept position, page, row), which is
+// what a block waits for, and give each thread twice the rows in flight.
 template <int D>
-__global__ void __launch_bounds__(kThreads) fp8_evict_move_kernel(const Fp8EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8EvictParams p) {
   constexpr int kLanes = D / 16;             // threads of a row, 16 codes each
   constexpr int kRowsPerPass = kThreads / kLanes;
   constexpr int kPasses = kChunk / kRowsPerPass;
   __shared__ int32_t s_src[kChunk], s_dst[kChunk];  // cache rows, -1: none
-  __shared__ uint32_t s_amax[kChunk];
-  __shared__ float s_new[kChunk];
+  __shared__ uint32_t s_amax[2][kChunk];
+  __shared__ float s_new[2][kChunk];
 
   wait_prior_grid();
-  const int b = blockIdx.x / p.chunks, j0 = (blockIdx.x % p.chunks) * kChunk;
-  const int h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
   const int hkv = p.c.hkv, bs = p.c.block_shift, tid = threadIdx.x;
+  const int h = blockIdx.x % hkv;
+  const int b = blockIdx.x / hkv / p.chunks, j0 = blockIdx.x / hkv % p.chunks * kChunk;
   const int n = p.new_seqlens[b];
   if (j0 >= n) return;
   if (tid < kChunk) {
@@ -432,49 +507,57 @@ __global__ void __launch_bounds__(kThreads) fp8_evict_move_kernel(const Fp8Evict
     }
     s_src[tid] = src;
     s_dst[tid] = dst;
-    s_amax[tid] = 0;
+    s_amax[0][tid] = s_amax[1][tid] = 0;
   }
   __syncthreads();
   const int sub = tid % kLanes, r0 = tid / kLanes;
-  uint8_t* codes = (is_v ? p.c.vc : p.c.kc) + static_cast<int64_t>(h) * D + 16 * sub;
-  float* scales = (is_v ? p.c.vs : p.c.ks) + h;
-  uint4 raw[kPasses];
-  float sc[kPasses];
+  uint8_t* codes[2] = {p.c.kc + static_cast<int64_t>(h) * D + 16 * sub, p.c.vc + static_cast<int64_t>(h) * D + 16 * sub};
+  float* scales[2] = {p.c.ks + h, p.c.vs + h};
+  uint4 raw[2][kPasses];
+  float sc[2][kPasses];
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
     const int src = s_src[k * kRowsPerPass + r0];
-    raw[k] = make_uint4(0, 0, 0, 0);  // a token whose page is missing becomes zeros
-    sc[k] = 0.f;
-    if (src >= 0) {
-      raw[k] = *reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(src) * hkv * D);
-      sc[k] = scales[static_cast<int64_t>(src >> bs) * hkv];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      raw[v][k] = make_uint4(0, 0, 0, 0);  // a token whose page is missing becomes zeros
+      sc[v][k] = 0.f;
+      if (src >= 0) {
+        raw[v][k] = *reinterpret_cast<const uint4*>(codes[v] + static_cast<int64_t>(src) * hkv * D);
+        sc[v][k] = scales[v][static_cast<int64_t>(src >> bs) * hkv];
+      }
     }
   }
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-    uint32_t top = 0;  // largest magnitude code, byte by byte, without NaN
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m = w[i] & 0x7F7F7F7Fu;
-      const uint32_t nan = ((m + 0x01010101u) & 0x80808080u) >> 7;
-      top = __vmaxu4(top, m & ~(nan * 0xFFu));
-    }
-    top = max(max(top & 0xFFu, (top >> 8) & 0xFFu), max((top >> 16) & 0xFFu, top >> 24));
+    for (int v = 0; v < 2; ++v) {
+      const uint32_t w[4] = {raw[v][k].x, raw[v][k].y, raw[v][k].z, raw[v][k].w};
+      uint32_t top = 0;  // largest magnitude code, byte by byte, without NaN
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (sub == 0 && top) {
-      const uint32_t f16 = e4m3x2_to_f16x2(static_cast<uint16_t>(top));
-      const float a = fminf(__low2float(*reinterpret_cast<const __half2*>(&f16)) * sc[k], 3.4028234e38f);
-      atomicMax(&s_amax[(k * kRowsPerPass + r0) >> bs], __float_as_uint(a));
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = w[i] & 0x7F7F7F7Fu;
+        const uint32_t nan = ((m + 0x01010101u) & 0x80808080u) >> 7;
+        top = __vmaxu4(top, m & ~(nan * 0xFFu));
+      }
+      top = max(max(top & 0xFFu, (top >> 8) & 0xFFu), max((top >> 16) & 0xFFu, top >> 24));
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+      if (sub == 0 && top) {
+        const uint32_t f16 = e4m3x2_to_f16x2(static_cast<uint16_t>(top));
+        const float a = fminf(__low2float(*reinterpret_cast<const __half2*>(&f16)) * sc[v][k], 3.4028234e38f);
+        atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(a));
+      }
     }
   }
   __syncthreads();
-  if (tid < (kChunk >> bs)) {
-    const float s = e4m3_block_scale(__uint_as_float(s_amax[tid]));
-    s_new[tid] = s;
-    const int dst = s_dst[tid << bs];
-    if (dst >= 0) scales[static_cast<int64_t>(dst >> bs) * hkv] = s;
+  const int blocks = kChunk >> bs;
+  if (tid < 2 * blocks) {
+    const int v = tid >= blocks, i = tid - v * blocks;
+    const float s = e4m3_block_scale(__uint_as_float(s_amax[v][i]));
+    s_new[v][i] = s;
+    const int dst = s_dst[i << bs];
+    if (dst >= 0) scales[v][static_cast<int64_t>(dst >> bs) * hkv] = s;
   }
   __syncthreads();
 #pragma unroll
@@ -482,18 +565,50 @@ __global__ void __launch_bounds__(kThreads) fp8_evict_move_kernel(const Fp8Evict
     const int t = k * kRowsPerPass + r0;
     const int dst = s_dst[t];
     if (dst < 0) continue;
-    const float s = s_new[t >> bs];
-    uint4 out = raw[k];
-    if (s != sc[k]) {
-      float x[8];
-      decode8(make_uint2(raw[k].x, raw[k].y), sc[k], x);
-      const uint2 lo = encode8(x, s);
-      decode8(make_uint2(raw[k].z, raw[k].w), sc[k], x);
-      const uint2 hi = encode8(x, s);
-      out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const float s = s_new[v][t >> bs];
+      uint4 out = raw[v][k];
+      if (s != sc[v][k]) {
+        float x[8];
+        decode8(make_uint2(out.x, out.y), sc[v][k], x);
+        const uint2 lo = encode8(x, s);
+        decode8(make_uint2(out.z, out.w), sc[v][k], x);
+        const uint2 hi = encode8(x, s);
+        out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+      *reinterpret_cast<uint4*>(codes[v] + static_cast<int64_t>(dst) * hkv * D) = out;
     }
-    *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(dst) * hkv * D) = out;
   }
+}
+
+// The selection's clusters: as many blocks as give a full row of the page table about 16 keys
+// a thread, at most 8.
+static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  int cluster = 1;
+  while (cluster < 8 && cap > static_cast<int64_t>(cluster) * 16 * kSelThreads) cluster *= 2;
+  const int64_t run = ((cap + cluster - 1) / cluster + 31) / 32 * 32;
+  const int smem = static_cast<int>(run < kSelKeys ? run : kSelKeys) * 4;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(fp8_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<uint32_t>(p.batch) * p.c.hkv * cluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_evict_select_kernel, p, cluster);
 }
 
 cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status,
@@ -528,10 +643,9 @@ cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* 
   fp8_evict_init_kernel<<<(words + kThreads - 1) / kThreads, kThreads, 0, stream>>>(status, page_state, a.num_pages);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(fp8_evict_select_kernel, dim3(static_cast<uint32_t>(a.batch) * a.kv_heads), dim3(kSelThreads), 0,
-                   stream, p);
+  e = launch_select(p, stream);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<uint32_t>(a.batch) * static_cast<uint32_t>(p.chunks), static_cast<uint32_t>(a.kv_heads) * 2);
+  const dim3 grid(static_cast<uint32_t>(a.batch) * static_cast<uint32_t>(p.chunks) * static_cast<uint32_t>(a.kv_heads));
   return a.head_dim == 128 ? launch_after(fp8_evict_move_kernel<128>, grid, dim3(kThreads), 0, stream, p)
                            : launch_after(fp8_evict_move_kernel<64>, grid, dim3(kThreads), 0, stream, p);
 }
