@@ -294,7 +294,7 @@ jfa_status check_fp8_cache(const void* kc, const void* vc, const float* ks, cons
   if (head_dim != 64 && head_dim != 128) return JFA_ERR_UNSUPPORTED;
   if (kv_heads > 32767) return JFA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_pages) * page_size >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(max_pages) * page_size >= (int64_t(1) << 31) - 256) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_pages) * page_size >= (int64_t(1) << 31) - 16384) return JFA_ERR_INVALID_ARG;
   if (batch > 0 && num_pages > 0 && (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4)))
     return JFA_ERR_INVALID_ARG;
   if (batch > 0 && (!aligned(seqlens, 4) || (max_pages > 0 && !aligned(table, 4)))) return JFA_ERR_INVALID_ARG;
@@ -1059,7 +1059,7 @@ jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size
   if (a->keep < 1 || a->first < 0 || a->recent < 0 || a->new_max_pages < 0) return JFA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(a->first) + a->recent > a->keep) return JFA_ERR_INVALID_ARG;
   const int64_t new_cap = static_cast<int64_t>(a->new_max_pages) * a->page_size;
-  if (new_cap < a->keep || new_cap >= (int64_t(1) << 31) - 256) return JFA_ERR_INVALID_ARG;
+  if (new_cap < a->keep || new_cap >= (int64_t(1) << 31) - 16384) return JFA_ERR_INVALID_ARG;
   if (a->batch > 0 && (!aligned(a->new_page_table, 4) || !aligned(a->kept, 4) || !aligned(a->new_seqlens, 4) ||
                        !aligned(a->new_weights, 4) || (a->max_pages > 0 && !aligned(a->weights, 4))))
     return JFA_ERR_INVALID_ARG;

@@ -46,25 +46,26 @@ struct Fp8AppendParams {
   int32_t* status;
 };
 
-// e4m3 codes of eight values divided by s. A power of two (every scale that
-// this file writes) divides exactly by a multiplication; other scales take the
-// rounded quotient.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s) {
-  float y[8];
-  if ((__float_as_uint(s) & 0x7FFFFFu) == 0) {
-    const float inv = 1.f / s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0; }
+
+// e4m3 codes of eight values divided by s, the rounded quotient whatever s is.
+// (Kept out of line, like recode8: the usual paths below must stay small, the
+// kernels were losing time to instruction fetches with these inlined.)
+__device__ __noinline__ uint2 encode8(const float* x, float s) {
+  uint32_t r[2] = {0, 0};
+#pragma unroll 1
+  for (int i = 0; i < 8; i += 2) {
+    // infinities and NaN become NaN
+    const float a = fabsf(x[i]) < INFINITY ? __fdiv_rn(x[i], s) : __int_as_float(0x7fffffff);
+    const float b = fabsf(x[i + 1]) < INFINITY ? __fdiv_rn(x[i + 1], s) : __int_as_float(0x7fffffff);
+    r[i >> 2] |= f32x2_to_e4m3x2(a, b) << (8 * (i & 2));
   }
-  return make_uint2(f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16),
-                    f32x2_to_e4m3x2(y[4], y[5]) | (f32x2_to_e4m3x2(y[6], y[7]) << 16));
+  return make_uint2(r[0], r[1]);
 }
 
-// The values of eight codes at scale s.
-__device__ __forceinline__ void decode8(uint2 codes, float s, float (&x)[8]) {
+// Eight codes from the scale `from` to the scale `to`.
+__device__ __noinline__ uint2 recode8(uint2 codes, float from, float to) {
+  float x[8];
   const uint32_t w[2] = {codes.x, codes.y};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -72,11 +73,64 @@ __device__ __forceinline__ void decode8(uint2 codes, float s, float (&x)[8]) {
     e4m3x4_to_f16(w[i], lo, hi);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    x[4 * i] = a.x * s;
-    x[4 * i + 1] = a.y * s;
-    x[4 * i + 2] = b.x * s;
-    x[4 * i + 3] = b.y * s;
+    x[4 * i] = a.x * from;
+    x[4 * i + 1] = a.y * from;
+    x[4 * i + 2] = b.x * from;
+    x[4 * i + 3] = b.y * from;
   }
+  return encode8(x, to);
+}
+
+// Eight finite bf16 values divided by a power of two (inv: its inverse): the
+// division is exact, so the codes round once.
+__device__ __forceinline__ uint2 encode8_pow2(const uint4& v, float inv) {
+  return make_uint2(f32x2_to_e4m3x2(ptx::bf16lo(v.x) * inv, ptx::bf16hi(v.x) * inv) |
+                        (f32x2_to_e4m3x2(ptx::bf16lo(v.y) * inv, ptx::bf16hi(v.y) * inv) << 16),
+                    f32x2_to_e4m3x2(ptx::bf16lo(v.z) * inv, ptx::bf16hi(v.z) * inv) |
+                        (f32x2_to_e4m3x2(ptx::bf16lo(v.w) * inv, ptx::bf16hi(v.w) * inv) << 16));
+}
+
+__device__ __noinline__ uint2 encode8_bf16(uint4 v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = ptx::bf16lo(w[i]);
+    x[2 * i + 1] = ptx::bf16hi(w[i]);
+  }
+  return encode8(x, s);
+}
+
+// Four codes times a power of two up to 2^15, in fp16: the product of an e4m3
+// value and a power of two is exact there down to 2^-14, and what is smaller
+// rounds to a zero of its sign as e4m3 either way (its smallest step is 2^-9).
+__device__ __forceinline__ uint32_t scale4_pow2(uint32_t codes, __half2 ratio) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16(codes, lo, hi);
+  const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&lo), ratio);
+  const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hi), ratio);
+  uint16_t x, y;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(x) : "r"(*reinterpret_cast<const uint32_t*>(&a)));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(*reinterpret_cast<const uint32_t*>(&b)));
+  return static_cast<uint32_t>(x) | (static_cast<uint32_t>(y) << 16);
+}
+
+// The largest finite magnitude of eight bf16 values, as bf16 bits (which order
+// like the magnitudes); *finite: there is nothing else among them.
+__device__ __forceinline__ uint32_t amax8_bf16(const uint4& v, bool* finite) {
+  const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+  const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  uint32_t top = max(m & 0xFFFFu, m >> 16);
+  *finite = top < 0x7F80u;
+  if (!*finite) {  // infinities and NaN do not set the scale
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = w[i] & 0xFFFFu, hi = w[i] >> 16;
+      top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+  }
+  return top;
 }
 
 template <int D>
@@ -85,8 +139,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
   constexpr int kRowsPerPass = kThreads / kLanes;
   constexpr int kPasses = kChunk / kRowsPerPass;
   __shared__ int32_t s_row[kChunk];          // cache row of each position, -1: nothing there to touch
-  __shared__ uint32_t s_amax[kChunk];        // per scale block, the bits of a non-negative float
+  __shared__ uint32_t s_amax[kChunk];        // per scale block, bf16 bits
   __shared__ float s_new[kChunk], s_old[kChunk];
+  __shared__ float s_inv[kChunk];            // 1 / s_new if that is a power of two, else 0
 
   wait_prior_grid();  // the cleared status block
   const int hkv = p.c.hkv;
@@ -135,18 +190,15 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
       raw[k] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(o0) + pos - f) * hkv * D));
   }
   __syncthreads();
+  uint32_t odd = 0;  // rows of this thread that hold infinities or NaN
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-    float a = 0.f;
+    bool finite;
+    uint32_t a = amax8_bf16(raw[k], &finite);
+    if (!finite) odd |= 1u << k;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // infinities and NaN do not set the scale
-      const float x0 = fabsf(ptx::bf16lo(w[i])), x1 = fabsf(ptx::bf16hi(w[i]));
-      a = fmaxf(a, fmaxf(x0 < INFINITY ? x0 : 0.f, x1 < INFINITY ? x1 : 0.f));
-    }
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    if (sub == 0 && a > 0.f) atomicMax(&s_amax[(k * kRowsPerPass + r0) >> bs], __float_as_uint(a));
+    for (int off = kLanes / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+    if (sub == 0) atomicMax(&s_amax[(k * kRowsPerPass + r0) >> bs], a);
   }
   __syncthreads();
   float* scales = is_v ? p.c.vs : p.c.ks;
@@ -154,12 +206,13 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
     const int start = p0 + (tid << bs);
     const int pos = max(start, f);  // the block's first new position, if it has one
     if (pos < min(L, start + (1 << bs)) && s_row[pos - p0] >= 0) {
-      float s = e4m3_block_scale(__uint_as_float(s_amax[tid]));
+      float s = e4m3_block_scale(__uint_as_float(s_amax[tid] << 16));
       float* cell = scales + static_cast<int64_t>(s_row[pos - p0] >> bs) * hkv + h;
       const float old = start < f ? *cell : 0.f;
       s = fmaxf(s, old);
       s_old[tid] = start < f ? old : s;
       s_new[tid] = s;
+      s_inv[tid] = is_pow2(s) ? 1.f / s : 0.f;
       *cell = s;
     }
   }
@@ -171,21 +224,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
     const int row = s_row[t];
     if (row < 0) continue;
     uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<int64_t>(row) * hkv * D);
-    const float s = s_new[t >> bs];
-    float x[8];
+    const float inv = s_inv[t >> bs];
     if (pos >= f) {
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = ptx::bf16lo(w[i]);
-        x[2 * i + 1] = ptx::bf16hi(w[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fabsf(x[i]) < INFINITY ? x[i] : __int_as_float(0x7fffffff);
-      *dst = encode8(x, s);
-    } else if (s_old[t >> bs] != s) {  // an older token of a block whose scale has grown
-      decode8(*dst, s_old[t >> bs], x);
-      *dst = encode8(x, s);
+      *dst = inv != 0.f && !((odd >> k) & 1) ? encode8_pow2(raw[k], inv) : encode8_bf16(raw[k], s_new[t >> bs]);
+    } else if (s_old[t >> bs] != s_new[t >> bs]) {  // an older token of a block whose scale has grown
+      *dst = recode8(*dst, s_old[t >> bs], s_new[t >> bs]);
     }
   }
 }
@@ -275,36 +318,36 @@ __device__ __forceinline__ int block_exclusive_sum(int x, int32_t* warp_sum, int
   return (warp > 0 ? before : 0) + y - x;
 }
 
-// What stays of one sequence and KV head, in order: a cluster of blocks, each with a run of the
-// candidates, whose keys it reads once and keeps in shared memory (the first
-// kSelKeys of a run; the rest is read again for every pass). The blocks'
-// digit counts are added through distributed shared memory, so each finds
-// the same digits; then they write their own survivors, placed by the numbers of survivors
-// before them. What the passes cost is latency, not bytes: about 16 keys a
-// thread is where more blocks stop paying (a sequence of 131,071 tokens:
-// 240 us with one block re-reading its keys, see the launcher for the cluster sizes).
-struct SelShared {
+// What stays of one sequence and KV head, in order: a cluster of blocks, each
+// with a run of the candidates, each warp with a run of the block's. A thread
+// reads its keys once, 32 apart, and keeps the first kSelKeys of them in
+// registers (keys past those, in runs of more than 16,384, are read again for every
+// pass). The threshold is found by radix digits, counted in shared memory and
+// added over the cluster through distributed shared memory, so that every
+// block finds the same one; then the blocks write their survivors, placed by
+// the numbers of survivors before them. What this costs is the latency of its
+// few dependent steps and the instructions per key, not bytes.
+constexpr int kSelKeys = 16;
+struct alignas(16) SelShared {
   int32_t hist[3][2048];
   int32_t warp_sum[32];
-  int32_t count[2];  // survivors above the threshold, candidates that equal it
+  int32_t count[2];  // keys above the threshold, keys that equal it
   uint32_t prefix;
   int32_t need;
 };
-constexpr int kSelKeys = 40960;
 
 __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
-  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ SelShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 3 * 2048; i += kSelThreads) sh.hist[0][i] = 0;
   wait_prior_grid();
   allow_next_grid();
   const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0;
   const int seg = blockIdx.x / cluster;
   const int b = seg / p.c.hkv, h = seg % p.c.hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  const int64_t new_cap = static_cast<int64_t>(p.new_max_pages) * p.page_size;
-  const int64_t wide = static_cast<int64_t>(cluster) * kSelThreads;  // threads of the cluster
-  const int64_t wtid = static_cast<int64_t>(rank) * kSelThreads + tid;
+  const int new_cap = p.new_max_pages * p.page_size;
+  const int wide = cluster * kSelThreads, wtid = static_cast<int>(rank) * kSelThreads + tid;  // threads of the cluster
   int L = p.seqlens[b];
   if (L < 0 || L > cap || (L > 0 && p.c.num_pages == 0)) {
     if (tid == 0) flag_bad_cache(p.status, kSiteFp8Evict);
@@ -313,35 +356,30 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
   const int n = min(L, p.keep);
   const float* w = p.weights + seg * cap;
   int32_t* kept = p.kept + static_cast<int64_t>(seg) * p.keep;
-  float* nw = p.new_weights + seg * new_cap;
+  float* nw = p.new_weights + static_cast<int64_t>(seg) * new_cap;
 
-  // the candidates: this block's run of them
+  // the candidates c0 .. c1 - 1, and this warp's run lo .. hi - 1 of them
   const bool choose = L > p.keep && p.keep > p.first + p.recent;
   const int c0 = p.first, c1 = max(L - p.recent, c0);
-  const int run = choose ? ((c1 - c0 + cluster - 1) / cluster + 31) / 32 * 32 : 0;
-  const int r0 = min(c0 + static_cast<int>(rank) * run, c1), r1 = min(r0 + run, c1);
-  const int nrun = choose ? r1 - r0 : 0, nkeys = min(nrun, kSelKeys);
-  for (int i = tid; i < 3 * 2048; i += kSelThreads) sh.hist[0][i] = 0;
-  __syncthreads();
-  // keys, and the counts of their first digits
-#pragma unroll 1
-  for (int i0 = 0; i0 < nrun; i0 += 8 * kSelThreads) {
-    float x[8];
+  const int per_warp = choose ? ((c1 - c0 + cluster * 32 - 1) / (cluster * 32) + 31) / 32 * 32 : 0;
+  const int lo = static_cast<int>(min(c0 + static_cast<int64_t>(rank * 32 + warp) * per_warp, static_cast<int64_t>(c1)));
+  const int hi = min(lo + per_warp, c1);
+  const int steps = choose ? (hi - lo + 31) / 32 : 0;  // of 32 keys; the last may be partial
+  uint32_t key[kSelKeys];
+  {
+    float x[kSelKeys];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = i0 + k * kSelThreads + tid;
-      x[k] = i < nrun ? __ldg(w + r0 + i) : 0.f;
-    }
+    for (int c = 0; c < kSelKeys; ++c) x[c] = c < steps && lo + 32 * c + lane < hi ? __ldg(w + lo + 32 * c + lane) : 0.f;
+    __syncthreads();  // the counts are zero
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = i0 + k * kSelThreads + tid;
-      if (i < nrun) {
-        const uint32_t key = weight_key(x[k]);
-        if (i < kSelKeys) s_keys[i] = key;
-        atomicAdd(&sh.hist[0][key >> 21], 1);
-      }
+    for (int c = 0; c < kSelKeys; ++c) {
+      key[c] = weight_key(x[c]);
+      if (c < steps && lo + 32 * c + lane < hi) atomicAdd(&sh.hist[0][key[c] >> 21], 1);
     }
   }
+  auto late_key = [&](int c) -> uint32_t { return weight_key(__ldg(w + lo + 32 * c + lane)); };
+  for (int c = kSelKeys; c < steps; ++c)
+    if (lo + 32 * c + lane < hi) atomicAdd(&sh.hist[0][late_key(c) >> 21], 1);
   // meanwhile: pages read by this sequence and pages it will write
   if (h == 0 && rank == 0) {
     if (tid == 0) p.new_seqlens[b] = n;
@@ -357,21 +395,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
       if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicAdd(p.page_state + pg, 1u);
     }
   }
-  for (int64_t j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
-  for (int64_t j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
+  for (int j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
+  for (int j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
   if (L <= p.keep) {  // the same in all blocks of the cluster
-    for (int64_t j = wtid; j < n; j += wide) {
-      kept[j] = static_cast<int32_t>(j);
+    for (int j = wtid; j < n; j += wide) {
+      kept[j] = j;
       nw[j] = w[j];
     }
     return;
   }
-  for (int64_t j = wtid; j < p.first; j += wide) {
-    kept[j] = static_cast<int32_t>(j);
+  for (int j = wtid; j < p.first; j += wide) {
+    kept[j] = j;
     nw[j] = w[j];
   }
-  for (int64_t j = wtid; j < p.recent; j += wide) {
-    kept[p.keep - p.recent + j] = static_cast<int32_t>(c1 + j);
+  for (int j = wtid; j < p.recent; j += wide) {
+    kept[p.keep - p.recent + j] = c1 + j;
     nw[p.keep - p.recent + j] = w[c1 + j];
   }
   if (!choose) return;
@@ -383,14 +421,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
       __syncthreads();
     }
   };
-  auto remote = [&](const int32_t* local, uint32_t r) -> int32_t {  // the same variable of block r
+  auto remote_pair = [&](const int32_t* local, uint32_t r, int& x, int& y) {  // two words of block r's copy
     uint32_t at;
-    int32_t v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(local)), "r"(r));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(at) : "memory");
   };
-  auto key_at = [&](int i) -> uint32_t { return i < nkeys ? s_keys[i] : weight_key(__ldg(w + r0 + i)); };
 
   // The want-th largest key, digit by digit (11, 11 and 10 bits from the top).
   uint32_t prefix = 0;
@@ -401,9 +436,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
     if (pass > 0) {
       const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 1 ? 2047u : 1023u;
-      for (int i = tid; i < nrun; i += kSelThreads) {
-        const uint32_t key = key_at(i);
-        if ((key >> above) == prefix) atomicAdd(&hist[(key >> shift) & mask], 1);
+#pragma unroll
+      for (int c = 0; c < kSelKeys; ++c)
+        if ((key[c] >> above) == prefix && c < steps && lo + 32 * c + lane < hi)
+          atomicAdd(&hist[(key[c] >> shift) & mask], 1);
+      for (int c = kSelKeys; c < steps; ++c) {
+        if (lo + 32 * c + lane < hi) {
+          const uint32_t k = late_key(c);
+          if ((k >> above) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+        }
       }
     }
     cluster_sync();
@@ -413,9 +454,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
       h0 = hist[2047 - 2 * tid];
       h1 = hist[2046 - 2 * tid];
     } else {
-      for (uint32_t r = 0; r < static_cast<uint32_t>(cluster); ++r) {
-        h0 += remote(hist + 2047 - 2 * tid, r);
-        h1 += remote(hist + 2046 - 2 * tid, r);
+      int x[8], y[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        x[r] = y[r] = 0;
+        if (r < cluster) remote_pair(hist + 2046 - 2 * tid, r, x[r], y[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        h1 += x[r];
+        h0 += y[r];
       }
     }
     int all;
@@ -429,17 +477,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
     __syncthreads();
     prefix = sh.prefix;
     need = sh.need;
-    __syncthreads();
   }
-  // keys above `prefix` stay, and the first `need` that equal it; each warp has a run of the block's run
-  const int per_warp = (nrun + kSelThreads - 1) / kSelThreads * 32;
-  const int lo = min(warp * per_warp, nrun), hi = min(lo + per_warp, nrun);
+  // Keys above `prefix` stay, and the first `need` that equal it.
   int gt = 0, eq = 0;
-  for (int i = lo; i < hi; i += 32) {
-    const uint32_t key = i + lane < hi ? key_at(i + lane) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i + lane < hi && key > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i + lane < hi && key == prefix));
+#pragma unroll
+  for (int c = 0; c < kSelKeys; ++c) {
+    const bool in = c < steps && lo + 32 * c + lane < hi;
+    gt += in && key[c] > prefix;
+    eq += in && key[c] == prefix;
   }
+  for (int c = kSelKeys; c < steps; ++c) {
+    const bool in = lo + 32 * c + lane < hi;
+    const uint32_t k = in ? late_key(c) : 0u;
+    gt += in && k > prefix;
+    eq += in && k == prefix;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   int all_gt, all_eq;
   int gt0 = block_exclusive_sum(lane == 0 ? gt : 0, sh.warp_sum, &all_gt);
   int eq0 = block_exclusive_sum(lane == 0 ? eq : 0, sh.warp_sum, &all_eq);
@@ -452,24 +506,33 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
     }
     cluster_sync();
     for (uint32_t r = 0; r < rank; ++r) {
-      gt0 += remote(sh.count, r);
-      eq0 += remote(sh.count + 1, r);
+      int x, y;
+      remote_pair(sh.count, r, x, y);
+      gt0 += x;
+      eq0 += y;
     }
   }
   const uint32_t below = (1u << lane) - 1;
-  for (int i = lo; i < hi; i += 32) {
-    const uint32_t key = i + lane < hi ? key_at(i + lane) : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, i + lane < hi && key > prefix);
-    const uint32_t me = __ballot_sync(0xffffffffu, i + lane < hi && key == prefix);
+  auto emit = [&](int c, uint32_t k) {
+    const int t = lo + 32 * c + lane;
+    const uint32_t mg = __ballot_sync(0xffffffffu, t < hi && k > prefix);
+    const uint32_t me = __ballot_sync(0xffffffffu, t < hi && k == prefix);
     const int eq_rank = eq0 + __popc(me & below);
     if (((mg >> lane) & 1) || (((me >> lane) & 1) && eq_rank < need)) {
       const int j = p.first + gt0 + __popc(mg & below) + min(eq_rank, need);
-      kept[j] = r0 + i + lane;
-      nw[j] = w[r0 + i + lane];
+      kept[j] = t;
+      // the weight itself, from its key; the keys of -0 and NaN stand for two values
+      float x = __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+      if (k == 0x80000000u || k == 0x007FFFFFu) x = w[t];
+      nw[j] = x;
     }
     gt0 += __popc(mg);
     eq0 += __popc(me);
-  }
+  };
+#pragma unroll
+  for (int c = 0; c < kSelKeys; ++c)
+    if (c < steps) emit(c, key[c]);
+  for (int c = kSelKeys; c < steps; ++c) emit(c, lo + 32 * c + lane < hi ? late_key(c) : 0u);
   if (cluster > 1) cluster_sync();  // no block leaves while another may still read its counts
 }
 
@@ -533,21 +596,18 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const uint32_t w[4] = {raw[v][k].x, raw[v][k].y, raw[v][k].z, raw[v][k].w};
-      uint32_t top = 0;  // largest magnitude code, byte by byte, without NaN
+      __half2 top = __float2half2_rn(0.f);  // largest magnitude; the maximum passes over NaN
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t m = w[i] & 0x7F7F7F7Fu;
-        const uint32_t nan = ((m + 0x01010101u) & 0x80808080u) >> 7;
-        top = __vmaxu4(top, m & ~(nan * 0xFFu));
+        uint32_t lo, hi;
+        e4m3x4_to_f16(w[i] & 0x7F7F7F7Fu, lo, hi);
+        top = __hmax2(top, __hmax2(*reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&hi)));
       }
-      top = max(max(top & 0xFFu, (top >> 8) & 0xFFu), max((top >> 16) & 0xFFu, top >> 24));
+      float a = __half2float(__hmax(__low2half(top), __high2half(top)));
 #pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-      if (sub == 0 && top) {
-        const uint32_t f16 = e4m3x2_to_f16x2(static_cast<uint16_t>(top));
-        const float a = fminf(__low2float(*reinterpret_cast<const __half2*>(&f16)) * sc[v][k], 3.4028234e38f);
-        atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(a));
-      }
+      for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+      if (sub == 0)
+        atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(fminf(a * sc[v][k], 3.4028234e38f)));
     }
   }
   __syncthreads();
@@ -567,38 +627,33 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
     if (dst < 0) continue;
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const float s = s_new[v][t >> bs];
+      const float s = s_new[v][t >> bs], from = sc[v][k];
       uint4 out = raw[v][k];
-      if (s != sc[v][k]) {
-        float x[8];
-        decode8(make_uint2(out.x, out.y), sc[v][k], x);
-        const uint2 lo = encode8(x, s);
-        decode8(make_uint2(out.z, out.w), sc[v][k], x);
-        const uint2 hi = encode8(x, s);
-        out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if (s != from) {
+        // both powers of two: the ratio is one, and is exact; below fp16's range nothing is left of the codes
+        const float ratio = from / s;
+        if (is_pow2(from) && ratio <= 32768.f) {
+          const __half2 r = __float2half2_rn(ratio);
+          out = make_uint4(scale4_pow2(out.x, r), scale4_pow2(out.y, r), scale4_pow2(out.z, r), scale4_pow2(out.w, r));
+        } else {
+          const uint2 lo = recode8(make_uint2(out.x, out.y), from, s), hi = recode8(make_uint2(out.z, out.w), from, s);
+          out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
       }
       *reinterpret_cast<uint4*>(codes[v] + static_cast<int64_t>(dst) * hkv * D) = out;
     }
   }
 }
 
-// The selection's clusters: as many blocks as give a full row of the page table about 16 keys
-// a thread, at most 8.
+// The selection's clusters: enough blocks for a full row of the page table at 16 keys a thread
+// (what a thread keeps in registers), at most 8, the portable size.
 static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   int cluster = 1;
-  while (cluster < 8 && cap > static_cast<int64_t>(cluster) * 16 * kSelThreads) cluster *= 2;
-  const int64_t run = ((cap + cluster - 1) / cluster + 31) / 32 * 32;
-  const int smem = static_cast<int>(run < kSelKeys ? run : kSelKeys) * 4;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(fp8_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
-  });
-  if (e != cudaSuccess) return e;
+  while (cluster < 8 && cap > static_cast<int64_t>(cluster) * kSelKeys * kSelThreads) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<uint32_t>(p.batch) * p.c.hkv * cluster);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
