@@ -279,7 +279,8 @@ struct Fp8EvictParams {
   int32_t* status;
 };
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr uint32_t kPageRead = 0x80000000u;
 
 __global__ void __launch_bounds__(kThreads) fp8_evict_init_kernel(int32_t* status, uint32_t* page_state, int n) {
@@ -304,50 +305,49 @@ __device__ __forceinline__ int block_exclusive_sum(int x, int32_t* warp_sum, int
     const int z = __shfl_up_sync(0xffffffffu, y, off);
     if (lane >= off) y += z;
   }
-  __syncthreads();  // warp_sum may still be read from an earlier call
   if (lane == 31) warp_sum[warp] = y;
   __syncthreads();
-  int v = warp_sum[lane];  // kSelThreads / 32 = 32 warps, one sum a lane
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += z;
-  }
-  *total = __shfl_sync(0xffffffffu, v, 31);
-  const int before = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
-  return (warp > 0 ? before : 0) + y - x;
+  int v = lane < kSelWarps ? warp_sum[lane] : 0;
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+  *total = __reduce_add_sync(0xffffffffu, v);
+  return before + y - x;
 }
 
 // What stays of one sequence and KV head, in order: a cluster of blocks, each
 // with a run of the candidates, each warp with a run of the block's. A thread
-// reads its keys once, 32 apart, and keeps the first kSelKeys of them in
-// registers (keys past those, in runs of more than 16,384, are read again for every
-// pass). The threshold is found by radix digits, counted in shared memory and
-// added over the cluster through distributed shared memory, so that every
-// block finds the same one; then the blocks write their survivors, placed by
-// the numbers of survivors before them. What this costs is the latency of its
-// few dependent steps and the instructions per key, not bytes.
-constexpr int kSelKeys = 16;
+// reads its keys once, 32 apart, and keeps KEYS of them in registers (longer
+// runs, past 8 x 16,384 candidates, are read again for every pass). The
+// threshold is found by radix digits, counted in shared memory and added over
+// the cluster through distributed shared memory, so that every block finds the
+// same one; then the blocks write their survivors, placed by the numbers of
+// survivors before them. This is bound by instructions and by the latency of
+// its few dependent steps, not by bytes: hence few warps (the scans cost each
+// of them the same) with many keys, and a key of 0, below every weight's,
+// where a thread has none, instead of tests. Measured, one sequence of 131,071
+// tokens: 240 us with one block of 1024 threads that re-reads its keys, 29 us with
+// 8 blocks of 1024 and 16 keys behind tests.
 struct alignas(16) SelShared {
   int32_t hist[3][2048];
-  int32_t warp_sum[32];
-  int32_t count[2];  // keys above the threshold, keys that equal it
+  int32_t warp_sum[6][32];  // one row for each sum
+  int32_t count[2];         // keys above the threshold, keys that equal it
   uint32_t prefix;
   int32_t need;
 };
 
-__global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
+template <int KEYS>
+__global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
+    fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
   __shared__ SelShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 3 * 2048; i += kSelThreads) sh.hist[0][i] = 0;
+  for (int i = tid; i < 3 * 2048 / 4; i += kSelThreads) reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
   wait_prior_grid();
   allow_next_grid();
-  const uint32_t rank = cluster > 1 ? blockIdx.x % cluster : 0;
+  const int rank = cluster > 1 ? static_cast<int>(blockIdx.x % cluster) : 0;
   const int seg = blockIdx.x / cluster;
   const int b = seg / p.c.hkv, h = seg % p.c.hkv;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int new_cap = p.new_max_pages * p.page_size;
-  const int wide = cluster * kSelThreads, wtid = static_cast<int>(rank) * kSelThreads + tid;  // threads of the cluster
+  const int wide = cluster * kSelThreads, wtid = rank * kSelThreads + tid;  // threads of the cluster
   int L = p.seqlens[b];
   if (L < 0 || L > cap || (L > 0 && p.c.num_pages == 0)) {
     if (tid == 0) flag_bad_cache(p.status, kSiteFp8Evict);
@@ -361,25 +361,30 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
   // the candidates c0 .. c1 - 1, and this warp's run lo .. hi - 1 of them
   const bool choose = L > p.keep && p.keep > p.first + p.recent;
   const int c0 = p.first, c1 = max(L - p.recent, c0);
-  const int per_warp = choose ? ((c1 - c0 + cluster * 32 - 1) / (cluster * 32) + 31) / 32 * 32 : 0;
-  const int lo = static_cast<int>(min(c0 + static_cast<int64_t>(rank * 32 + warp) * per_warp, static_cast<int64_t>(c1)));
-  const int hi = min(lo + per_warp, c1);
-  const int steps = choose ? (hi - lo + 31) / 32 : 0;  // of 32 keys; the last may be partial
-  uint32_t key[kSelKeys];
+  const int runs = cluster * kSelWarps;
+  const int per_warp = choose ? ((c1 - c0 + runs - 1) / runs + 31) / 32 * 32 : 0;
+  const int lo = static_cast<int>(min(c0 + static_cast<int64_t>(rank * kSelWarps + warp) * per_warp, static_cast<int64_t>(c1)));
+  const int count = choose ? min(lo + per_warp, c1) - lo - lane : 0;  // keys at w[lo + lane + 32 c], 32 c < count
+  w += lo + lane;
+  uint32_t key[KEYS];
   {
-    float x[kSelKeys];
+    float x[KEYS];
 #pragma unroll
-    for (int c = 0; c < kSelKeys; ++c) x[c] = c < steps && lo + 32 * c + lane < hi ? __ldg(w + lo + 32 * c + lane) : 0.f;
+    for (int c = 0; c < KEYS; ++c) {
+      x[c] = 0.f;
+      if (32 * c < count) x[c] = __ldg(w + 32 * c);
+    }
     __syncthreads();  // the counts are zero
 #pragma unroll
-    for (int c = 0; c < kSelKeys; ++c) {
-      key[c] = weight_key(x[c]);
-      if (c < steps && lo + 32 * c + lane < hi) atomicAdd(&sh.hist[0][key[c] >> 21], 1);
+    for (int c = 0; c < KEYS; ++c) {
+      key[c] = 32 * c < count ? weight_key(x[c]) : 0u;
+      if (32 * c < per_warp) atomicAdd(&sh.hist[0][key[c] >> 21], 1);  // no weight has digit 0
     }
   }
-  auto late_key = [&](int c) -> uint32_t { return weight_key(__ldg(w + lo + 32 * c + lane)); };
-  for (int c = kSelKeys; c < steps; ++c)
-    if (lo + 32 * c + lane < hi) atomicAdd(&sh.hist[0][late_key(c) >> 21], 1);
+  auto late_key = [&](int c) -> uint32_t { return 32 * c < count ? weight_key(__ldg(w + 32 * c)) : 0u; };
+  const int steps = per_warp / 32;
+#pragma unroll 1
+  for (int c = KEYS; c < steps; ++c) atomicAdd(&sh.hist[0][late_key(c) >> 21], 1);
   // meanwhile: pages read by this sequence and pages it will write
   if (h == 0 && rank == 0) {
     if (tid == 0) p.new_seqlens[b] = n;
@@ -397,6 +402,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
   }
   for (int j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
   for (int j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
+  w -= lo + lane;
   if (L <= p.keep) {  // the same in all blocks of the cluster
     for (int j = wtid; j < n; j += wide) {
       kept[j] = j;
@@ -413,6 +419,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
     nw[p.keep - p.recent + j] = w[c1 + j];
   }
   if (!choose) return;
+  w += lo + lane;
 
   auto cluster_sync = [&] {
     if (cluster > 1) {
@@ -421,10 +428,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
       __syncthreads();
     }
   };
-  auto remote_pair = [&](const int32_t* local, uint32_t r, int& x, int& y) {  // two words of block r's copy
+  auto remote = [&](const int32_t* local, int r) -> uint32_t {  // the address of block r's copy
     uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(local)), "r"(r));
-    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(at) : "memory");
+    return at;
   };
 
   // The want-th largest key, digit by digit (11, 11 and 10 bits from the top).
@@ -437,42 +444,49 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
       const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 1 ? 2047u : 1023u;
 #pragma unroll
-      for (int c = 0; c < kSelKeys; ++c)
-        if ((key[c] >> above) == prefix && c < steps && lo + 32 * c + lane < hi)
-          atomicAdd(&hist[(key[c] >> shift) & mask], 1);
-      for (int c = kSelKeys; c < steps; ++c) {
-        if (lo + 32 * c + lane < hi) {
-          const uint32_t k = late_key(c);
-          if ((k >> above) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
-        }
+      for (int c = 0; c < KEYS; ++c)
+        if ((key[c] >> above) == prefix) atomicAdd(&hist[(key[c] >> shift) & mask], 1);
+#pragma unroll 1
+      for (int c = KEYS; c < steps; ++c) {
+        const uint32_t k = late_key(c);
+        if ((k >> above) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
       }
     }
     cluster_sync();
-    // bins from the top: thread t holds bins 2047 - 2 t and 2046 - 2 t
-    int h0 = 0, h1 = 0;
+    // bins from the top: thread t holds bins 2047 - 4 t down to 2044 - 4 t
+    const int32_t* mine = hist + 2044 - 4 * tid;
+    int4 n4 = make_int4(0, 0, 0, 0);
     if (cluster == 1) {
-      h0 = hist[2047 - 2 * tid];
-      h1 = hist[2046 - 2 * tid];
+      n4 = *reinterpret_cast<const int4*>(mine);
     } else {
-      int x[8], y[8];
+      int4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        x[r] = y[r] = 0;
-        if (r < cluster) remote_pair(hist + 2046 - 2 * tid, r, x[r], y[r]);
+        v[r] = make_int4(0, 0, 0, 0);
+        if (r < cluster)
+          asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[r].x), "=r"(v[r].y), "=r"(v[r].z), "=r"(v[r].w)
+                       : "r"(remote(mine, r)));
       }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        h1 += x[r];
-        h0 += y[r];
+        n4.x += v[r].x;
+        n4.y += v[r].y;
+        n4.z += v[r].z;
+        n4.w += v[r].w;
       }
     }
     int all;
-    const int before = block_exclusive_sum(h0 + h1, sh.warp_sum, &all);
-    if (before < need && before + h0 + h1 >= need) {
-      const bool upper = before + h0 >= need;
-      const uint32_t d = upper ? 2047 - 2 * tid : 2046 - 2 * tid;
-      sh.prefix = pass == 2 ? (prefix << 10) | d : (prefix << 11) | d;
-      sh.need = need - before - (upper ? 0 : h0);
+    int before = block_exclusive_sum(n4.x + n4.y + n4.z + n4.w, sh.warp_sum[pass], &all);
+    const int bins[4] = {n4.w, n4.z, n4.y, n4.x};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (before < need && before + bins[i] >= need) {
+        const uint32_t d = 2047 - 4 * tid - i;
+        sh.prefix = pass == 2 ? (prefix << 10) | d : (prefix << 11) | d;
+        sh.need = need - before;
+      }
+      before += bins[i];
     }
     __syncthreads();
     prefix = sh.prefix;
@@ -481,58 +495,60 @@ __global__ void __launch_bounds__(kSelThreads, 1) fp8_evict_select_kernel(const 
   // Keys above `prefix` stay, and the first `need` that equal it.
   int gt = 0, eq = 0;
 #pragma unroll
-  for (int c = 0; c < kSelKeys; ++c) {
-    const bool in = c < steps && lo + 32 * c + lane < hi;
-    gt += in && key[c] > prefix;
-    eq += in && key[c] == prefix;
+  for (int c = 0; c < KEYS; ++c) {
+    gt += key[c] > prefix;
+    eq += key[c] == prefix;
   }
-  for (int c = kSelKeys; c < steps; ++c) {
-    const bool in = lo + 32 * c + lane < hi;
-    const uint32_t k = in ? late_key(c) : 0u;
-    gt += in && k > prefix;
-    eq += in && k == prefix;
+#pragma unroll 1
+  for (int c = KEYS; c < steps; ++c) {
+    const uint32_t k = late_key(c);
+    gt += k > prefix;
+    eq += k == prefix;
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
-  int all_gt, all_eq;
-  int gt0 = block_exclusive_sum(lane == 0 ? gt : 0, sh.warp_sum, &all_gt);
-  int eq0 = block_exclusive_sum(lane == 0 ? eq : 0, sh.warp_sum, &all_eq);
-  gt0 = __shfl_sync(0xffffffffu, gt0, 0);
-  eq0 = __shfl_sync(0xffffffffu, eq0, 0);
+  // before this warp: the block's earlier warps, the cluster's earlier blocks
+  if (lane == 0) {
+    sh.warp_sum[3][warp] = gt;
+    sh.warp_sum[4][warp] = eq;
+  }
+  __syncthreads();
+  const int vg = lane < kSelWarps ? sh.warp_sum[3][lane] : 0, ve = lane < kSelWarps ? sh.warp_sum[4][lane] : 0;
+  int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? vg : 0);
+  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? ve : 0);
   if (cluster > 1) {
+    const int all_gt = __reduce_add_sync(0xffffffffu, vg), all_eq = __reduce_add_sync(0xffffffffu, ve);
     if (tid == 0) {
       sh.count[0] = all_gt;
       sh.count[1] = all_eq;
     }
     cluster_sync();
-    for (uint32_t r = 0; r < rank; ++r) {
-      int x, y;
-      remote_pair(sh.count, r, x, y);
-      gt0 += x;
-      eq0 += y;
-    }
+    int x = 0, y = 0;
+    if (lane < rank) asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(remote(sh.count, lane)));
+    gt0 += __reduce_add_sync(0xffffffffu, x);
+    eq0 += __reduce_add_sync(0xffffffffu, y);
   }
   const uint32_t below = (1u << lane) - 1;
   auto emit = [&](int c, uint32_t k) {
-    const int t = lo + 32 * c + lane;
-    const uint32_t mg = __ballot_sync(0xffffffffu, t < hi && k > prefix);
-    const uint32_t me = __ballot_sync(0xffffffffu, t < hi && k == prefix);
+    const uint32_t mg = __ballot_sync(0xffffffffu, k > prefix);
+    const uint32_t me = __ballot_sync(0xffffffffu, k == prefix);
     const int eq_rank = eq0 + __popc(me & below);
-    if (((mg >> lane) & 1) || (((me >> lane) & 1) && eq_rank < need)) {
+    if (k > prefix || (k == prefix && eq_rank < need)) {
       const int j = p.first + gt0 + __popc(mg & below) + min(eq_rank, need);
-      kept[j] = t;
-      // the weight itself, from its key; the keys of -0 and NaN stand for two values
+      kept[j] = lo + lane + 32 * c;
+      // the weight itself, from its key; the keys of 0 and -infinity stand for -0 and NaN too
       float x = __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-      if (k == 0x80000000u || k == 0x007FFFFFu) x = w[t];
+      if (k == 0x80000000u || k == 0x007FFFFFu) x = w[32 * c];
       nw[j] = x;
     }
     gt0 += __popc(mg);
     eq0 += __popc(me);
   };
 #pragma unroll
-  for (int c = 0; c < kSelKeys; ++c)
+  for (int c = 0; c < KEYS; ++c)
     if (c < steps) emit(c, key[c]);
-  for (int c = kSelKeys; c < steps; ++c) emit(c, lo + 32 * c + lane < hi ? late_key(c) : 0u);
+#pragma unroll 1
+  for (int c = KEYS; c < steps; ++c) emit(c, late_key(c));
   if (cluster > 1) cluster_sync();  // no block leaves while another may still read its counts
 }
 
@@ -645,12 +661,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
   }
 }
 
-// The selection's clusters: enough blocks for a full row of the page table at 16 keys a thread
-// (what a thread keeps in registers), at most 8, the portable size.
-static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
-  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  int cluster = 1;
-  while (cluster < 8 && cap > static_cast<int64_t>(cluster) * kSelKeys * kSelThreads) cluster *= 2;
+template <int KEYS>
+static cudaError_t launch_select_keys(const Fp8EvictParams& p, int cluster, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<uint32_t>(p.batch) * p.c.hkv * cluster);
   cfg.blockDim = dim3(kSelThreads);
@@ -663,7 +675,19 @@ static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_evict_select_kernel, p, cluster);
+  return cudaLaunchKernelEx(&cfg, fp8_evict_select_kernel<KEYS>, p, cluster);
+}
+
+// By the candidates that a full row of the page table can hold: one block for up to 8192 (4 keys a
+// thread up to 2048, else 16), clusters of up to 8 blocks (the portable size) past that, and
+// 32 keys a thread past 65,536.
+static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  if (cap <= 4 * kSelThreads) return launch_select_keys<4>(p, 1, stream);
+  int cluster = 1;
+  while (cluster < 8 && cap > static_cast<int64_t>(cluster) * 16 * kSelThreads) cluster *= 2;
+  return cap <= static_cast<int64_t>(cluster) * 16 * kSelThreads ? launch_select_keys<16>(p, cluster, stream)
+                                                                 : launch_select_keys<32>(p, cluster, stream);
 }
 
 cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status,
