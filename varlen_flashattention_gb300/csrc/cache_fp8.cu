@@ -296,42 +296,28 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum over the threads before this one (exclusive); *total gets the whole sum.
-__device__ __forceinline__ int block_exclusive_sum(int x, int32_t* warp_sum, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int y = x;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, y, off);
-    if (lane >= off) y += z;
-  }
-  if (lane == 31) warp_sum[warp] = y;
-  __syncthreads();
-  int v = lane < kSelWarps ? warp_sum[lane] : 0;
-  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
-  *total = __reduce_add_sync(0xffffffffu, v);
-  return before + y - x;
-}
-
 // What stays of one sequence and KV head, in order: a cluster of blocks, each
 // with a run of the candidates, each warp with a run of the block's. A thread
 // reads its keys once, 32 apart, and keeps KEYS of them in registers (longer
 // runs, past 8 x 16,384 candidates, are read again for every pass). The
-// threshold is found by radix digits, counted in shared memory and added over
-// the cluster through distributed shared memory, so that every block finds the
-// same one; then the blocks write their survivors, placed by the numbers of
-// survivors before them. This is bound by instructions and by the latency of
-// its few dependent steps, not by bytes: hence few warps (the scans cost each
-// of them the same) with many keys, and a key of 0, below every weight's,
-// where a thread has none, instead of tests. Measured, one sequence of 131,071
-// tokens: 240 us with one block of 1024 threads that re-reads its keys, 29 us with
-// 8 blocks of 1024 and 16 keys behind tests.
+// threshold is found by four digits of 8 bits, counted in shared memory (equal
+// digits of a warp cost no more than different ones) and added over the cluster
+// through distributed shared memory by one warp of each block, which all come
+// to the same digit; then the blocks list their survivors, placed by the numbers
+// of survivors before them. This is bound by instructions and by the latency of
+// its few dependent steps, not by bytes: hence few warps with many keys, a key
+// of 0, below every weight's, where a thread has none, instead of tests, small
+// digits (11 bits take a pass less, but 2048 counts from each of 8 blocks took
+// 2.8 us a pass), places from byte sums of four steps at once (population counts
+// run at an eighth of the rate), and no store to global memory before the
+// cluster's last barrier but one, which would wait for it.
 struct alignas(16) SelShared {
-  int32_t hist[3][2048];
-  int32_t warp_sum[6][32];  // one row for each sum
-  int32_t count[2];         // keys above the threshold, keys that equal it
-  uint32_t prefix;
-  int32_t need;
+  int32_t hist[4][256];
+  int32_t warp_sum[2][32];
+  int32_t count[2];  // this block's survivors: above the threshold (or all), equal to it
+  uint32_t digit;
+  int32_t left;      // how many keys with the prefix found so far stay
+  int32_t hits;      // how many there are
 };
 
 template <int KEYS>
@@ -339,7 +325,7 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
   __shared__ SelShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 3 * 2048 / 4; i += kSelThreads) reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
+  if (tid < 256) reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
   wait_prior_grid();
   allow_next_grid();
   const int rank = cluster > 1 ? static_cast<int>(blockIdx.x % cluster) : 0;
@@ -378,48 +364,43 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
 #pragma unroll
     for (int c = 0; c < KEYS; ++c) {
       key[c] = 32 * c < count ? weight_key(x[c]) : 0u;
-      if (32 * c < per_warp) atomicAdd(&sh.hist[0][key[c] >> 21], 1);  // no weight has digit 0
+      if (32 * c < per_warp) atomicAdd(&sh.hist[0][key[c] >> 24], 1);
     }
   }
   auto late_key = [&](int c) -> uint32_t { return 32 * c < count ? weight_key(__ldg(w + 32 * c)) : 0u; };
   const int steps = per_warp / 32;
 #pragma unroll 1
-  for (int c = KEYS; c < steps; ++c) atomicAdd(&sh.hist[0][late_key(c) >> 21], 1);
-  // meanwhile: pages read by this sequence and pages it will write
-  if (h == 0 && rank == 0) {
-    if (tid == 0) p.new_seqlens[b] = n;
-    const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-    const int32_t* nt = p.new_table + static_cast<int64_t>(b) * p.new_max_pages;
-    const int used = L > 0 ? fast_div(L - 1, p.c.page) + 1 : 0, fresh = n > 0 ? fast_div(n - 1, p.c.page) + 1 : 0;
-    for (int i = tid; i < used; i += kSelThreads) {
-      const uint32_t pg = static_cast<uint32_t>(pt[i]);
-      if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicOr(p.page_state + pg, kPageRead);
+  for (int c = KEYS; c < steps; ++c) atomicAdd(&sh.hist[0][late_key(c) >> 24], 1);
+  // Everything but the candidates' places: what is certain to stay, zeros, and
+  // the pages that this sequence reads and will write.
+  auto finish = [&] {
+    if (h == 0 && rank == 0) {
+      if (tid == 0) p.new_seqlens[b] = n;
+      const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+      const int32_t* nt = p.new_table + static_cast<int64_t>(b) * p.new_max_pages;
+      const int used = L > 0 ? fast_div(L - 1, p.c.page) + 1 : 0, fresh = n > 0 ? fast_div(n - 1, p.c.page) + 1 : 0;
+      for (int i = tid; i < used; i += kSelThreads) {
+        const uint32_t pg = static_cast<uint32_t>(pt[i]);
+        if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicOr(p.page_state + pg, kPageRead);
+      }
+      for (int i = tid; i < fresh; i += kSelThreads) {
+        const uint32_t pg = static_cast<uint32_t>(nt[i]);
+        if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicAdd(p.page_state + pg, 1u);
+      }
     }
-    for (int i = tid; i < fresh; i += kSelThreads) {
-      const uint32_t pg = static_cast<uint32_t>(nt[i]);
-      if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicAdd(p.page_state + pg, 1u);
+    for (int j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
+    for (int j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
+    if (L <= p.keep) {
+      for (int j = wtid; j < n; j += wide) kept[j] = j;
+    } else {
+      for (int j = wtid; j < p.first; j += wide) kept[j] = j;
+      for (int j = wtid; j < p.recent; j += wide) kept[p.keep - p.recent + j] = c1 + j;
     }
-  }
-  for (int j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
-  for (int j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
-  w -= lo + lane;
-  if (L <= p.keep) {  // the same in all blocks of the cluster
-    for (int j = wtid; j < n; j += wide) {
-      kept[j] = j;
-      nw[j] = w[j];
-    }
+  };
+  if (!choose) {  // the same in all blocks of the cluster
+    finish();
     return;
   }
-  for (int j = wtid; j < p.first; j += wide) {
-    kept[j] = j;
-    nw[j] = w[j];
-  }
-  for (int j = wtid; j < p.recent; j += wide) {
-    kept[p.keep - p.recent + j] = c1 + j;
-    nw[p.keep - p.recent + j] = w[c1 + j];
-  }
-  if (!choose) return;
-  w += lo + lane;
 
   auto cluster_sync = [&] {
     if (cluster > 1) {
@@ -434,93 +415,110 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     return at;
   };
 
-  // The want-th largest key, digit by digit (11, 11 and 10 bits from the top).
+  // The need-th largest key, digit by digit from the top.
   uint32_t prefix = 0;
-  int need = p.keep - p.first - p.recent;  // how many keys with the prefix found so far stay
+  int need = p.keep - p.first - p.recent;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    int32_t* hist = sh.hist[pass];
+  for (int pass = 0; pass < 4; ++pass) {
     if (pass > 0) {
-      const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
-      const uint32_t mask = pass == 1 ? 2047u : 1023u;
+      const int above = 32 - 8 * pass, shift = 24 - 8 * pass;
 #pragma unroll
       for (int c = 0; c < KEYS; ++c)
-        if ((key[c] >> above) == prefix) atomicAdd(&hist[(key[c] >> shift) & mask], 1);
+        if ((key[c] >> above) == prefix) atomicAdd(&sh.hist[pass][(key[c] >> shift) & 255], 1);
 #pragma unroll 1
       for (int c = KEYS; c < steps; ++c) {
         const uint32_t k = late_key(c);
-        if ((k >> above) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1);
+        if ((k >> above) == prefix) atomicAdd(&sh.hist[pass][(k >> shift) & 255], 1);
       }
     }
     cluster_sync();
-    // bins from the top: thread t holds bins 2047 - 4 t down to 2044 - 4 t
-    const int32_t* mine = hist + 2044 - 4 * tid;
-    int4 n4 = make_int4(0, 0, 0, 0);
-    if (cluster == 1) {
-      n4 = *reinterpret_cast<const int4*>(mine);
-    } else {
-      int4 v[8];
+    if (warp == 0) {
+      // lane l holds the digits 255 - 8 l down to 248 - 8 l
+      const int32_t* bins = sh.hist[pass] + 248 - 8 * lane;
+      int cnt[8];
+      if (cluster == 1) {
+        const int4 d = *reinterpret_cast<const int4*>(bins), u = *reinterpret_cast<const int4*>(bins + 4);
+        cnt[0] = u.w, cnt[1] = u.z, cnt[2] = u.y, cnt[3] = u.x, cnt[4] = d.w, cnt[5] = d.z, cnt[6] = d.y, cnt[7] = d.x;
+      } else {
+        int v[8][8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        v[r] = make_int4(0, 0, 0, 0);
-        if (r < cluster)
-          asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[r].x), "=r"(v[r].y), "=r"(v[r].z), "=r"(v[r].w)
-                       : "r"(remote(mine, r)));
-      }
+        for (int r = 0; r < 8; ++r) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        n4.x += v[r].x;
-        n4.y += v[r].y;
-        n4.z += v[r].z;
-        n4.w += v[r].w;
-      }
-    }
-    int all;
-    int before = block_exclusive_sum(n4.x + n4.y + n4.z + n4.w, sh.warp_sum[pass], &all);
-    const int bins[4] = {n4.w, n4.z, n4.y, n4.x};
+          for (int i = 0; i < 8; ++i) v[r][i] = 0;
+          if (r < cluster) {
+            const uint32_t at = remote(bins, r);
+            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[r][7]), "=r"(v[r][6]), "=r"(v[r][5]), "=r"(v[r][4]) : "r"(at));
+            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[r][3]), "=r"(v[r][2]), "=r"(v[r][1]), "=r"(v[r][0]) : "r"(at + 16));
+          }
+        }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (before < need && before + bins[i] >= need) {
-        const uint32_t d = 2047 - 4 * tid - i;
-        sh.prefix = pass == 2 ? (prefix << 10) | d : (prefix << 11) | d;
-        sh.need = need - before;
+        for (int i = 0; i < 8; ++i) {
+          cnt[i] = 0;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) cnt[i] += v[r][i];
+        }
       }
-      before += bins[i];
+      int own = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) own += cnt[i];
+      int upto = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+      }
+      int before = upto - own;
+      if (before < need && upto >= need) {  // one lane: the digit is one of its own
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < need && before + cnt[i] >= need) {
+            sh.digit = 255 - 8 * lane - i;
+            sh.left = need - before;
+            sh.hits = cnt[i];
+          }
+          before += cnt[i];
+        }
+      }
     }
     __syncthreads();
-    prefix = sh.prefix;
-    need = sh.need;
+    prefix = (prefix << 8) | sh.digit;
+    need = sh.left;
   }
-  // Keys above `prefix` stay, and the first `need` that equal it.
+  // Keys above `prefix` stay, and the first `need` of the sh.hits that equal it.
+  // Where all of those do, which is the usual case, no rank among them is needed.
+  const bool all_equal = sh.hits == need;
   int gt = 0, eq = 0;
 #pragma unroll
   for (int c = 0; c < KEYS; ++c) {
-    gt += key[c] > prefix;
-    eq += key[c] == prefix;
+    gt += key[c] > prefix || (all_equal && key[c] == prefix);
+    if (!all_equal) eq += key[c] == prefix;
   }
 #pragma unroll 1
   for (int c = KEYS; c < steps; ++c) {
     const uint32_t k = late_key(c);
-    gt += k > prefix;
-    eq += k == prefix;
+    gt += k > prefix || (all_equal && k == prefix);
+    eq += !all_equal && k == prefix;
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   // before this warp: the block's earlier warps, the cluster's earlier blocks
   if (lane == 0) {
-    sh.warp_sum[3][warp] = gt;
-    sh.warp_sum[4][warp] = eq;
+    sh.warp_sum[0][warp] = gt;
+    sh.warp_sum[1][warp] = eq;
   }
   __syncthreads();
-  const int vg = lane < kSelWarps ? sh.warp_sum[3][lane] : 0, ve = lane < kSelWarps ? sh.warp_sum[4][lane] : 0;
+  const int vg = lane < kSelWarps ? sh.warp_sum[0][lane] : 0, ve = lane < kSelWarps ? sh.warp_sum[1][lane] : 0;
   int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? vg : 0);
   int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? ve : 0);
   if (cluster > 1) {
-    const int all_gt = __reduce_add_sync(0xffffffffu, vg), all_eq = __reduce_add_sync(0xffffffffu, ve);
-    if (tid == 0) {
-      sh.count[0] = all_gt;
-      sh.count[1] = all_eq;
+    if (warp == 0) {
+      const int all_gt = __reduce_add_sync(0xffffffffu, vg), all_eq = __reduce_add_sync(0xffffffffu, ve);
+      if (lane == 0) {
+        sh.count[0] = all_gt;
+        sh.count[1] = all_eq;
+      }
     }
     cluster_sync();
     int x = 0, y = 0;
@@ -528,27 +526,58 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     gt0 += __reduce_add_sync(0xffffffffu, x);
     eq0 += __reduce_add_sync(0xffffffffu, y);
   }
+  int32_t* out = kept + p.first;
+  const int t0 = lo + lane;
+  if (all_equal) {
+#pragma unroll
+    for (int c = 0; c < KEYS; c += 4) {
+      if (c >= steps) break;
+      // byte i: the survivors of step c + i up to this lane
+      uint32_t own = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own |= (key[c + i] >= prefix ? 1u : 0u) << (8 * i);
+      uint32_t upto = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+      }
+      const uint32_t whole = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (key[c + i] >= prefix) out[gt0 + static_cast<int>((upto >> (8 * i)) & 255) - 1] = t0 + 32 * (c + i);
+        gt0 += static_cast<int>((whole >> (8 * i)) & 255);
+      }
+    }
+  }
   const uint32_t below = (1u << lane) - 1;
-  auto emit = [&](int c, uint32_t k) {
+  auto place = [&](int c, uint32_t k) {  // one step, with ranks among equal keys
     const uint32_t mg = __ballot_sync(0xffffffffu, k > prefix);
     const uint32_t me = __ballot_sync(0xffffffffu, k == prefix);
     const int eq_rank = eq0 + __popc(me & below);
-    if (k > prefix || (k == prefix && eq_rank < need)) {
-      const int j = p.first + gt0 + __popc(mg & below) + min(eq_rank, need);
-      kept[j] = lo + lane + 32 * c;
-      // the weight itself, from its key; the keys of 0 and -infinity stand for -0 and NaN too
-      float x = __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-      if (k == 0x80000000u || k == 0x007FFFFFu) x = w[32 * c];
-      nw[j] = x;
-    }
+    const int j = gt0 + __popc(mg & below) + min(eq_rank, need);
+    if (k > prefix || (k == prefix && eq_rank < need)) out[j] = t0 + 32 * c;
     gt0 += __popc(mg);
     eq0 += __popc(me);
   };
+  auto place_all = [&](int c, uint32_t k) {  // one step, every equal key stays
+    const uint32_t m = __ballot_sync(0xffffffffu, k >= prefix);
+    if (k >= prefix) out[gt0 + __popc(m & below)] = t0 + 32 * c;
+    gt0 += __popc(m);
+  };
+  if (!all_equal) {
 #pragma unroll
-  for (int c = 0; c < KEYS; ++c)
-    if (c < steps) emit(c, key[c]);
+    for (int c = 0; c < KEYS; ++c)
+      if (c < steps) place(c, key[c]);
+  }
 #pragma unroll 1
-  for (int c = KEYS; c < steps; ++c) emit(c, late_key(c));
+  for (int c = KEYS; c < steps; ++c) {
+    if (all_equal)
+      place_all(c, late_key(c));
+    else
+      place(c, late_key(c));
+  }
+  finish();
   if (cluster > 1) cluster_sync();  // no block leaves while another may still read its counts
 }
 
@@ -574,7 +603,9 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
     const int j = j0 + tid;
     int src = -1, dst = -1;
     if (j < n) {
-      const int t = p.kept[(static_cast<int64_t>(b) * hkv + h) * p.keep + j];
+      const int64_t seg = static_cast<int64_t>(b) * hkv + h;
+      const int t = p.kept[seg * p.keep + j];
+      p.new_weights[seg * p.new_max_pages * p.page_size + j] = p.weights[seg * p.max_pages * p.page_size + t];
       const int pg = fast_div(t, p.c.page), npg = fast_div(j, p.c.page);
       const uint32_t page = static_cast<uint32_t>(p.page_table[static_cast<int64_t>(b) * p.max_pages + pg]);
       const uint32_t fresh = static_cast<uint32_t>(p.new_table[static_cast<int64_t>(b) * p.new_max_pages + npg]);
