@@ -77,7 +77,7 @@ struct Fp8DecodeParams {
   float* part_lse2;    // [parts + B][hkv][rows], log2, -inf when empty
   __nv_bfloat16* o;
   float* lse;          // [B, q_len, Hq] natural log
-  float* lse2;         // [B, hkv, rows] log2 (weights only)
+  float* lse2;         // [B, hkv, rows] log2, +inf where a row sees no key (weights only)
   float* scores;       // [tiles][hkv][rows][16] log2 units (weights only)
   const float* w_in;   // [B, hkv, max_pages * page_size] or null
   float* w_out;
@@ -96,8 +96,13 @@ constexpr float kF8NoRef = -3.0e38f;  // a reference before the first visible to
 
 template <int D, int NR>
 struct F8Tile {
-  static constexpr int kCtasPerSm = NR == 1 ? 4 : 3;  // by the registers: 128 and 168
-  static constexpr int kStages = NR == 1 && D == 128 ? 3 : 4;
+  // By the registers: 128 a thread, or 168 and 255 with 16 rows. 16 rows at head_dim 128 in 168
+  // registers spill: 88 us against 67 us (16 x 0.5k-8k tokens, 4 query tokens of 4 heads).
+  static constexpr int kCtasPerSm = NR == 1 ? 4 : (D == 64 ? 3 : 2);
+  // One tile on its way while one is computed, per warp: with 16 warps that is
+  // 68 KB an SM. More queue up in front of the memory: 32 x 1k-32k tokens, NR 1,
+  // take 175 us with 2 stages and 187 us with 3. With 8 warps it takes two.
+  static constexpr int kStages = NR == 1 ? 2 : 3;
   static constexpr int kVOff = 16 * D;           // K rows, V rows, 16 + 16 scales
   static constexpr int kScaleOff = 32 * D;
   static constexpr int kStageBytes = kScaleOff + 128;
@@ -135,6 +140,9 @@ __device__ __forceinline__ uint32_t f8_transpose(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+
+// A row that sees no key counts nothing for the weights: its lse is kept as +inf there.
+__device__ __forceinline__ float f8_weight_lse(float z) { return z == -INFINITY ? INFINITY : z; }
 
 // A sequence's length, 0 where it is out of range.
 __device__ __forceinline__ int f8_length(const Fp8DecodeParams& p, int b, bool* bad) {
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
                              ptx::pack_bf16(acc[u][j + 3][e] * f, acc[u][j + 3][2 + e] * f));
             if (gq == 0) {
               p.lse[row] = z * 0.6931471805599453f;
-              if (WEIGHTS) p.lse2[(static_cast<int64_t>(b) * hkv + h) * nrows + r] = z;
+              if (WEIGHTS) p.lse2[(static_cast<int64_t>(b) * hkv + h) * nrows + r] = f8_weight_lse(z);
             }
           } else {
             const int64_t row = ((static_cast<int64_t>(part) + b) * hkv + h) * nrows + r;
@@ -601,52 +609,134 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
   if (lane == 0) p.errors[1 + blockIdx.x * kF8Warps + warp] = bad_page;
 }
 
-// Joins the parts of the sequences that were cut, a block per output row:
-// lse = log2 sum_i 2^lse_i, O = sum_i 2^(lse_i - lse) O_i, each warp over a run of
-// the parts, then the warps in order; a sequence without tokens gets zeros and
-// -inf. Also gathers the main kernel's findings into the status block.
-constexpr int kF8JoinWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(32 * kF8JoinWarps) fp8_decode_join_kernel(const Fp8DecodeParams p, int num_errors,
-                                                                            int weights) {
-  constexpr int kPer = D / 32;  // output columns of a lane
-  __shared__ float s_m[kF8JoinWarps], s_z[kF8JoinWarps], s_o[kF8JoinWarps][D];
+// Joins the parts of the sequences that were cut:
+//   lse = log2 sum_i 2^lse_i, O = sum_i 2^(lse_i - lse) O_i,
+// in a fixed order; a sequence without tokens gets zeros and -inf. Block 0 also
+// gathers the main kernel's findings into the status block.
+// Two shapes. kWide = false: a block of four warps per output row, each with a
+// run of the parts (many sequences, of a dozen parts or so each). kWide = true:
+// a block per 32 columns of a row, its 32 groups of eight lanes reading a part's
+// 128-byte piece each, four ahead, so that a sequence cut into hundreds of parts
+// is joined by all SMs.
+__device__ __forceinline__ void f8_report(const Fp8DecodeParams& p, int num_errors) {
+  bool bad = false;
+  for (int i = threadIdx.x; i < num_errors; i += blockDim.x) bad |= __ldcg(p.errors + i) != 0;
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x < kStatusBytes / 4)
+    p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8DecodeTable : 0));
+}
+
+constexpr int kF8WideThreads = 256;
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_kernel(const Fp8DecodeParams p,
+                                                                                       int num_errors) {
   wait_prior_grid();
   allow_next_grid();
+  if (blockIdx.x == 0) f8_report(p, num_errors);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) {
-    bool bad = false;
-    for (int i = threadIdx.x; i < num_errors; i += 32 * kF8JoinWarps) bad |= __ldcg(p.errors + i) != 0;
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x < kStatusBytes / 4)
-      p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8DecodeTable : 0));
-  }
   const int hkv = p.c.hkv, G = p.group, nrows = G * p.q_len;
-  const int seg = static_cast<int>(blockIdx.x / nrows), r = static_cast<int>(blockIdx.x % nrows);
-  const int b = seg / hkv, h = seg % hkv;
+  const int slice = kWide ? static_cast<int>(blockIdx.x % (D / 32)) : 0;
+  const int job = static_cast<int>(kWide ? blockIdx.x / (D / 32) : blockIdx.x);
+  const int seg = job / nrows, r = job % nrows, b = seg / hkv, h = seg % hkv;
   const int base = __ldcg(p.tile_base + b), end = __ldcg(p.tile_base + b + 1);
   const F8Line line(__ldcg(p.tile_base + p.batch), p.max_parts);
-  float o[kPer];
+  const int i0 = end > base ? line.part_of(base) : 0;
+  const int count = end > base ? line.part_of(end - 1) - i0 + 1 : 0;
+  if (count == 1) return;  // finished by its part
+  const int64_t first = ((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r;
+  const int step = hkv * nrows;  // rows from one part to the next
+  const float* lse = p.part_lse2 + first;
+  const float* po = p.part_o + first * D + 32 * slice;
+  const int64_t row = (static_cast<int64_t>(b) * p.q_len + r / G) * p.hq + static_cast<int64_t>(h) * G + r % G;
+  float top, z;  // largest lse and sum of 2^(lse - top) (top: 0 if every part is empty or NaN)
+
+  if constexpr (kWide) {
+    __shared__ float s_f[kFp8MaxWarps];
+    __shared__ float s_red[2][8];
+    __shared__ float s_o[8][32];
+    const int group = threadIdx.x >> 3, sub = threadIdx.x & 7;
+    float4 v[4];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) o[k] = 0.f;
-  float M = -INFINITY, Z = 0.f;  // the warp's sums, relative to its largest lse
-  if (end > base) {
-    const int i0 = line.part_of(base), count = line.part_of(end - 1) - i0 + 1;
-    if (count == 1) return;  // finished by its part
-    const int lo = count * warp / kF8JoinWarps, hi = count * (warp + 1) / kF8JoinWarps;
-    const float* lse = p.part_lse2 + ((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r;
-    const float* po = p.part_o + (((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r) * D;
-    const int64_t step = static_cast<int64_t>(hkv) * nrows;
-    for (int i = lo + lane; i < hi; i += 32) M = fmaxf(M, __ldcg(lse + i * step));
+    for (int k = 0; k < 4; ++k) {
+      const int i = group + 32 * k;
+      v[k] = i < count ? __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * step * D) + sub)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < count; i += kF8WideThreads) {
+      const float y = __ldcg(lse + static_cast<int64_t>(i) * step);
+      s_f[i] = y;
+      m = fmaxf(m, y);
+    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float ref = M == -INFINITY ? 0.f : M;  // every part may be empty, or NaN
-    for (int i = lo; i < hi; i += 8) {
-      float f[8], v[8][kPer];
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane == 0) s_red[0][warp] = m;
+    __syncthreads();
+    top = s_red[0][0];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t at = min(i + k, hi - 1) * step;
-        f[k] = i + k < hi ? ptx::ex2(__ldcg(lse + at) - ref) : 0.f;
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_red[0][w]);
+    if (top == -INFINITY) top = 0.f;
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < count; i += kF8WideThreads) {
+      const float f = ptx::ex2(s_f[i] - top);
+      s_f[i] = f;
+      sum += f;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    z = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) z += s_red[1][w];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = group; i < count; i += 128) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = i + 32 * k < count ? s_f[i + 32 * k] : 0.f;
+        o.x += f * v[k].x;
+        o.y += f * v[k].y;
+        o.z += f * v[k].z;
+        o.w += f * v[k].w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = i + 128 + 32 * k;
+        v[k] = j < count ? __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(j) * step * D) + sub)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int off = 8; off < 32; off <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+    }
+    if (lane < 8) *reinterpret_cast<float4*>(&s_o[warp][4 * sub]) = o;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) y += s_o[w][lane];
+    p.o[row * D + 32 * slice + lane] = __float2bfloat16(z == 0.f ? 0.f : y / z);
+  } else {
+    constexpr int kPer = D / 32, kWarps = 4;  // output columns of a lane
+    __shared__ float s_m[kWarps], s_z[kWarps], s_o[kWarps][D];
+    const int lo = count * warp / kWarps, hi = count * (warp + 1) / kWarps;
+    float o[kPer], m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+    for (int i = lo + lane; i < hi; i += 32) m = fmaxf(m, __ldcg(lse + static_cast<int64_t>(i) * step));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (m == -INFINITY) m = 0.f;
+    for (int i = lo; i < hi; i += 4) {
+      float f[4], v[4][kPer];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t at = static_cast<int64_t>(min(i + k, hi - 1)) * step;
+        f[k] = i + k < hi ? ptx::ex2(__ldcg(lse + at) - m) : 0.f;
         if constexpr (kPer == 4) {
           const float4 a = __ldcg(reinterpret_cast<const float4*>(po + at * D) + lane);
           v[k][0] = a.x, v[k][1] = a.y, v[k][2] = a.z, v[k][3] = a.w;
@@ -656,72 +746,83 @@ __global__ void __launch_bounds__(32 * kF8JoinWarps) fp8_decode_join_kernel(cons
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         if (i + k >= hi) break;
-        Z += f[k];
+        sum += f[k];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) o[e] += f[k] * v[k][e];
       }
     }
-  }
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_z[warp] = Z;
-  }
+    if (lane == 0) {
+      s_m[warp] = sum == 0.f ? -INFINITY : m;  // nothing in it: counts for nothing
+      s_z[warp] = sum;
+    }
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = o[e];
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float top = s_m[0];
+    for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    if (top == -INFINITY) top = 0.f;
+    z = 0.f;
+    float y = 0.f;
 #pragma unroll
-  for (int w = 1; w < kF8JoinWarps; ++w) top = fmaxf(top, s_m[w]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float z = 0.f, y = 0.f;
-#pragma unroll
-  for (int w = 0; w < kF8JoinWarps; ++w) {
-    // a warp whose parts were all empty or NaN has its sums relative to 0
-    const float f = ptx::ex2((s_m[w] == -INFINITY ? 0.f : s_m[w]) - ref);
-    if (s_z[w] == 0.f) continue;
-    z += s_z[w] * f;
-    y += s_o[w][threadIdx.x] * f;
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ptx::ex2(s_m[w] - top);
+      z += s_z[w] * f;
+      y += s_o[w][threadIdx.x] * f;
+    }
+    p.o[row * D + threadIdx.x] = __float2bfloat16(z == 0.f ? 0.f : y / z);
   }
-  const int64_t row = (static_cast<int64_t>(b) * p.q_len + r / G) * p.hq + static_cast<int64_t>(h) * G + r % G;
-  p.o[row * D + threadIdx.x] = __float2bfloat16(z == 0.f ? 0.f : y / z);
-  if (threadIdx.x == 0) {
-    const float lse2 = z == 0.f ? -INFINITY : ref + log2f(z);
+  if (threadIdx.x == 0 && slice == 0) {
+    const float lse2 = z == 0.f ? -INFINITY : top + log2f(z);
     p.lse[row] = lse2 * 0.6931471805599453f;
-    if (weights) p.lse2[static_cast<int64_t>(seg) * nrows + r] = lse2;
+    if (p.w_out) p.lse2[static_cast<int64_t>(seg) * nrows + r] = f8_weight_lse(lse2);
   }
 }
 
 // w_out = decay * w_in + sum over the rows of 2^(score - lse): half a warp per
-// tile and head, one lane per token; the blocks share the tiles evenly.
-__global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8DecodeParams p) {
+// tile and head, one lane per token; the blocks share the tiles evenly. Bound by
+// HBM: 4 bytes per row and 8 per token and head.
+__global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8DecodeParams p, const FastDiv by_heads) {
   wait_prior_grid();
   const int hkv = p.c.hkv, nrows = p.group * p.q_len;
-  const int64_t total = static_cast<int64_t>(p.tile_base[p.batch]) * hkv;
+  const int64_t total = static_cast<int64_t>(p.tile_base[p.batch]) * hkv;  // (tile, head) pairs
   const int64_t y0 = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
-  const int64_t y1 = static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x;
-  if (y0 >= y1) return;
+  const int count = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x - y0);
+  if (count <= 0) return;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  int b = f8_find_sequence(p.tile_base, p.batch, static_cast<int>(y0 / hkv));
+  const int x0 = static_cast<int>(y0 / hkv), h0 = static_cast<int>(y0 % hkv);
+  int b = f8_find_sequence(p.tile_base, p.batch, x0), next = p.tile_base[b + 1];
+  bool bad;
+  int L = f8_length(p, b, &bad), first = p.tile_base[b];
   const int half = threadIdx.x >> 4, tk = threadIdx.x & 15;
-  for (int64_t y = y0 + half; y < y1; y += 16) {
-    const int x = static_cast<int>(y / hkv), h = static_cast<int>(y % hkv);
-    while (p.tile_base[b + 1] <= x) ++b;
-    const int t = (x - p.tile_base[b]) * 16 + tk;
-    bool bad;
-    if (t >= f8_length(p, b, &bad)) continue;
+  for (int i = half; i < count; i += 16) {
+    const int q = fast_div(h0 + i, by_heads), x = x0 + q, h = h0 + i - q * hkv;
+    if (x >= next) {
+      do ++b;
+      while (p.tile_base[b + 1] <= x);
+      next = p.tile_base[b + 1];
+      first = p.tile_base[b];
+      L = f8_length(p, b, &bad);
+    }
+    const int t = (x - first) * 16 + tk;
+    if (t >= L) continue;
     const int64_t seg = static_cast<int64_t>(b) * hkv + h;
     const float* lse2 = p.lse2 + seg * nrows;
-    const float* s = p.scores + y * nrows * 16 + tk;
-    float sum = 0.f;
-    for (int r = 0; r < nrows; ++r) {
-      const float z = lse2[r];
-      sum += z == -INFINITY ? 0.f : ptx::ex2(s[r * 16] - z);
-    }
+    const float* s = p.scores + (y0 + i) * nrows * 16 + tk;
     const int64_t at = seg * cap + t;
-    p.w_out[at] = p.w_in ? fmaf(p.decay, p.w_in[at], sum) : sum;
+    float sum = p.w_in ? p.decay * __ldcs(p.w_in + at) : 0.f;
+    for (int r = 0; r < nrows; r += 4) {
+      float v[4], z[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = r + k < nrows ? __ldcs(s + (r + k) * 16) : -INFINITY;
+        z[k] = r + k < nrows ? lse2[r + k] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum += ptx::ex2(v[k] - z[k]);
+    }
+    p.w_out[at] = sum;
   }
 }
 
@@ -767,10 +868,15 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
     e = w ? launch_main<D, 2, true>(p, grid, stream) : launch_main<D, 2, false>(p, grid, stream);
   if (ev) cudaEventRecord(ev[1], stream);
   if (e != cudaSuccess) return e;
-  e = launch_after(fp8_decode_join_kernel<D>, dim3(static_cast<uint32_t>(p.batch) * p.c.hkv * nrows),
-                   dim3(32 * kF8JoinWarps), 0, stream, p, 1 + grid * kF8Warps, w ? 1 : 0);
+  // parts a sequence has on average: past 32, the wide join
+  const uint32_t rows = static_cast<uint32_t>(p.batch) * p.c.hkv * nrows;
+  const int errors = 1 + grid * kF8Warps;
+  e = p.max_parts > 32 * p.batch
+          ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32)), dim3(kF8WideThreads), 0, stream, p, errors)
+          : launch_after(fp8_decode_join_kernel<D, false>, dim3(rows), dim3(128), 0, stream, p, errors);
   if (e != cudaSuccess || !w) return e;
-  return launch_after(fp8_decode_weights_kernel, dim3(static_cast<uint32_t>(sms * 8)), dim3(256), 0, stream, p);
+  return launch_after(fp8_decode_weights_kernel, dim3(static_cast<uint32_t>(sms * 8)), dim3(256), 0, stream, p,
+                      make_fast_div(p.c.hkv));
 }
 
 cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream) {
