@@ -262,7 +262,7 @@ Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
   const int64_t parts = std::min(most, tiles) * a.kv_heads + segs;  // of one head each
   size_t off = kStatusBytes;
   L.errors = off;
-  off = align_up(off + 4 * (1 + kFp8MaxWarps), 256);
+  off = align_up(off + kFp8MaxWarps + 4, 256);
   L.tile_base = off;
   off = align_up(off + 4 * (static_cast<size_t>(a.batch) + 1), 256);
   L.part_o = off;
@@ -1011,12 +1011,11 @@ jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* a, void* ws, si
   if (a->weights && !aligned(a->weights, 4)) return JFA_ERR_INVALID_ARG;
   // blocks of the grid: batch x chunks of 128 positions x heads, K and V
   const double blocks = static_cast<double>(a->batch) * ((static_cast<int64_t>(a->max_new) + 126) / 128 + 1) * 2 * a->kv_heads;
-  if (blocks >= 2147483648.0) return JFA_ERR_INVALID_ARG;
+  if (blocks >= 2147483647.0) return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
   if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
   int32_t* status = static_cast<int32_t*>(ws);
-  if (launch_status_clear(status, stream) != cudaSuccess) return JFA_ERR_CUDA;
-  if (a->batch == 0) return JFA_OK;
+  if (a->batch == 0) return cuda_status(launch_status_clear(status, stream));
   return cuda_status(launch_cache_append_fp8(*a, status, stream));
 }
 
@@ -1037,7 +1036,7 @@ jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* a, void* ws, size_t ws_byte
   if (sms <= 0) return JFA_ERR_CUDA;
   Fp8DecodeBuffers buf{};
   buf.status = reinterpret_cast<int32_t*>(w);
-  buf.errors = reinterpret_cast<int32_t*>(w + L.errors);
+  buf.errors = w + L.errors;
   buf.tile_base = reinterpret_cast<int32_t*>(w + L.tile_base);
   buf.part_o = reinterpret_cast<float*>(w + L.part_o);
   buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);

@@ -133,6 +133,36 @@ __device__ __forceinline__ uint32_t amax8_bf16(const uint4& v, bool* finite) {
   return top;
 }
 
+// Offsets rise from 0 to total_new, and the new tokens are part of the length.
+__device__ __forceinline__ bool append_range_ok(const Fp8AppendParams& p, int b, int o0, int o1, int L) {
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  return o0 >= 0 && o1 >= o0 && o1 <= p.total_new && o1 - o0 <= p.max_new && L >= o1 - o0 && L <= cap &&
+         (b > 0 || o0 == 0) && (b < p.batch - 1 || o1 == p.total_new);
+}
+
+// One block checks the whole call, offsets, lengths and the pages written to, and
+// sets the status block; the others pass over what is wrong without a word.
+// That spares the launch that would have to clear the status block for them.
+__device__ void append_report(const Fp8AppendParams& p) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  for (int b = threadIdx.x >> 5; b < p.batch; b += kThreads / 32) {
+    const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
+    if (!append_range_ok(p, b, o0, o1, L)) {
+      bad = true;
+    } else if (o1 > o0) {
+      const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+      const int last = fast_div(L - 1, p.c.page);
+#pragma unroll 4
+      for (int i = fast_div(L - (o1 - o0), p.c.page) + lane; i <= last; i += 32)
+        bad |= static_cast<uint32_t>(pt[i]) >= static_cast<uint32_t>(p.c.num_pages);
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x < kStatusBytes / 4)
+    p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8Append : 0));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(const Fp8AppendParams p) {
   constexpr int kLanes = D / 8;              // threads of a row, 8 values each
@@ -143,19 +173,18 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
   __shared__ float s_new[kChunk], s_old[kChunk];
   __shared__ float s_inv[kChunk];            // 1 / s_new if that is a power of two, else 0
 
-  wait_prior_grid();  // the cleared status block
-  const int hkv = p.c.hkv;
-  const int h = blockIdx.x % (2 * hkv) >> 1;  // heads first: their rows are neighbours in memory
-  const bool is_v = blockIdx.x & 1;
-  const int b = blockIdx.x / (2 * hkv) / p.chunks, ci = blockIdx.x / (2 * hkv) % p.chunks;
-  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
-  // offsets rise from 0 to total_new, and the new tokens are part of the length
-  if (o0 < 0 || o1 < o0 || o1 > p.total_new || o1 - o0 > p.max_new || L < o1 - o0 || L > cap ||
-      (b == 0 && o0 != 0) || (b == p.batch - 1 && o1 != p.total_new)) {
-    if (threadIdx.x == 0) flag_bad_cache(p.status, kSiteFp8Append);
+  if (blockIdx.x == 0) {
+    append_report(p);
     return;
   }
+  const uint32_t block = blockIdx.x - 1;
+  const int hkv = p.c.hkv;
+  const int h = block % (2 * hkv) >> 1;  // heads first: their rows are neighbours in memory
+  const bool is_v = block & 1;
+  const int b = block / (2 * hkv) / p.chunks, ci = block / (2 * hkv) % p.chunks;
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
+  if (!append_range_ok(p, b, o0, o1, L)) return;
   const int f = L - (o1 - o0);                 // first new position
   const int p0 = ((f / kChunk) + ci) * kChunk;  // this block's positions: p0 .. p0 + 127
   if (o1 == o0 || p0 >= L) return;
@@ -171,8 +200,6 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
       const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + pg];
       if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.c.num_pages))
         row = page * p.page_size + (pos - pg * p.page_size);
-      else
-        flag_bad_cache(p.status, kSiteFp8Append);
     }
     s_row[tid] = row;
     s_amax[tid] = 0;
@@ -257,10 +284,13 @@ cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t*
   p.chunks = static_cast<int32_t>((static_cast<int64_t>(a.max_new) + kChunk - 2) / kChunk + 1);
   p.weights = a.weights;
   p.status = status;
-  const dim3 grid(static_cast<uint32_t>(p.batch) * static_cast<uint32_t>(p.chunks) *
-                  (2 * static_cast<uint32_t>(a.kv_heads)));
-  return a.head_dim == 128 ? launch_after(fp8_append_kernel<128>, grid, dim3(kThreads), 0, stream, p)
-                           : launch_after(fp8_append_kernel<64>, grid, dim3(kThreads), 0, stream, p);
+  const uint32_t grid = static_cast<uint32_t>(p.batch) * static_cast<uint32_t>(p.chunks) *
+                            (2 * static_cast<uint32_t>(a.kv_heads)) + 1;
+  if (a.head_dim == 128)
+    fp8_append_kernel<128><<<grid, kThreads, 0, stream>>>(p);
+  else
+    fp8_append_kernel<64><<<grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ evict
@@ -301,23 +331,25 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // reads its keys once, 32 apart, and keeps KEYS of them in registers (longer
 // runs, past 8 x 16,384 candidates, are read again for every pass). The
 // threshold is found by four digits of 8 bits, counted in shared memory (equal
-// digits of a warp cost no more than different ones) and added over the cluster
-// through distributed shared memory by one warp of each block, which all come
-// to the same digit; then the blocks list their survivors, placed by the numbers
+// digits of a warp cost no more than different ones) and added into every block
+// of the cluster through distributed shared memory (stores and additions there
+// overlap, loads of the 8 blocks' counts took 1.7 us a pass), where one warp of
+// each finds the same digit; then the blocks list their survivors, placed by the numbers
 // of survivors before them. This is bound by instructions and by the latency of
 // its few dependent steps, not by bytes: hence few warps with many keys, a key
 // of 0, below every weight's, where a thread has none, instead of tests, small
 // digits (11 bits take a pass less, but 2048 counts from each of 8 blocks took
 // 2.8 us a pass), places from byte sums of four steps at once (population counts
 // run at an eighth of the rate), and no store to global memory before the
-// cluster's last barrier but one, which would wait for it.
+// cluster's last barrier, which would wait for it.
 struct alignas(16) SelShared {
-  int32_t hist[4][256];
+  int32_t hist[4][256];      // this block's counts
+  int32_t sum[4][256];       // the cluster's
   int32_t warp_sum[2][32];
-  int32_t count[2];  // this block's survivors: above the threshold (or all), equal to it
+  int32_t count[2][8];       // survivors above the threshold (or all), and equal to it, of each block
   uint32_t digit;
-  int32_t left;      // how many keys with the prefix found so far stay
-  int32_t hits;      // how many there are
+  int32_t left;              // how many keys with the prefix found so far stay
+  int32_t hits;              // how many there are
 };
 
 template <int KEYS>
@@ -325,7 +357,9 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
   __shared__ SelShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 256) reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
+  reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);  // 512 threads: hist and sum
+  static_assert(kSelThreads * 16 == sizeof(sh.hist) + sizeof(sh.sum), "one int4 a thread clears both");
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before the first addition
   wait_prior_grid();
   allow_next_grid();
   const int rank = cluster > 1 ? static_cast<int>(blockIdx.x % cluster) : 0;
@@ -374,16 +408,17 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
   // Everything but the candidates' places: what is certain to stay, zeros, and
   // the pages that this sequence reads and will write.
   auto finish = [&] {
-    if (h == 0 && rank == 0) {
-      if (tid == 0) p.new_seqlens[b] = n;
+    if (h == 0 && wtid == 0) p.new_seqlens[b] = n;
+    {  // the sequence's blocks share its pages
+      const int me = h * wide + wtid, all = p.c.hkv * wide;
       const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
       const int32_t* nt = p.new_table + static_cast<int64_t>(b) * p.new_max_pages;
       const int used = L > 0 ? fast_div(L - 1, p.c.page) + 1 : 0, fresh = n > 0 ? fast_div(n - 1, p.c.page) + 1 : 0;
-      for (int i = tid; i < used; i += kSelThreads) {
+      for (int i = me; i < used; i += all) {
         const uint32_t pg = static_cast<uint32_t>(pt[i]);
         if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicOr(p.page_state + pg, kPageRead);
       }
-      for (int i = tid; i < fresh; i += kSelThreads) {
+      for (int i = me; i < fresh; i += all) {
         const uint32_t pg = static_cast<uint32_t>(nt[i]);
         if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicAdd(p.page_state + pg, 1u);
       }
@@ -398,6 +433,7 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     }
   };
   if (!choose) {  // the same in all blocks of the cluster
+    if (cluster > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     finish();
     return;
   }
@@ -431,35 +467,26 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
         if ((k >> above) == prefix) atomicAdd(&sh.hist[pass][(k >> shift) & 255], 1);
       }
     }
-    cluster_sync();
+    const int32_t* bins = sh.hist[pass];
+    __syncthreads();
+    if (cluster > 1) {
+      if (pass == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (tid < 256) {
+        const int32_t v = sh.hist[pass][tid];
+        if (v)
+          for (int r = 0; r < cluster; ++r)
+            asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(remote(&sh.sum[pass][tid], r)),
+                         "r"(v)
+                         : "memory");
+      }
+      cluster_sync();
+      bins = sh.sum[pass];
+    }
     if (warp == 0) {
       // lane l holds the digits 255 - 8 l down to 248 - 8 l
-      const int32_t* bins = sh.hist[pass] + 248 - 8 * lane;
-      int cnt[8];
-      if (cluster == 1) {
-        const int4 d = *reinterpret_cast<const int4*>(bins), u = *reinterpret_cast<const int4*>(bins + 4);
-        cnt[0] = u.w, cnt[1] = u.z, cnt[2] = u.y, cnt[3] = u.x, cnt[4] = d.w, cnt[5] = d.z, cnt[6] = d.y, cnt[7] = d.x;
-      } else {
-        int v[8][8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[r][i] = 0;
-          if (r < cluster) {
-            const uint32_t at = remote(bins, r);
-            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[r][7]), "=r"(v[r][6]), "=r"(v[r][5]), "=r"(v[r][4]) : "r"(at));
-            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[r][3]), "=r"(v[r][2]), "=r"(v[r][1]), "=r"(v[r][0]) : "r"(at + 16));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cnt[i] = 0;
-#pragma unroll
-          for (int r = 0; r < 8; ++r) cnt[i] += v[r][i];
-        }
-      }
+      const int4 d = *reinterpret_cast<const int4*>(bins + 248 - 8 * lane);
+      const int4 u = *reinterpret_cast<const int4*>(bins + 252 - 8 * lane);
+      const int cnt[8] = {u.w, u.z, u.y, u.x, d.w, d.z, d.y, d.x};
       int own = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) own += cnt[i];
@@ -515,16 +542,14 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
   if (cluster > 1) {
     if (warp == 0) {
       const int all_gt = __reduce_add_sync(0xffffffffu, vg), all_eq = __reduce_add_sync(0xffffffffu, ve);
-      if (lane == 0) {
-        sh.count[0] = all_gt;
-        sh.count[1] = all_eq;
+      if (lane < cluster) {
+        asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(remote(&sh.count[0][rank], lane)), "r"(all_gt) : "memory");
+        asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(remote(&sh.count[1][rank], lane)), "r"(all_eq) : "memory");
       }
     }
-    cluster_sync();
-    int x = 0, y = 0;
-    if (lane < rank) asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(remote(sh.count, lane)));
-    gt0 += __reduce_add_sync(0xffffffffu, x);
-    eq0 += __reduce_add_sync(0xffffffffu, y);
+    cluster_sync();  // and the last: nothing reaches into another block after it
+    gt0 += __reduce_add_sync(0xffffffffu, lane < rank ? sh.count[0][lane] : 0);
+    eq0 += __reduce_add_sync(0xffffffffu, lane < rank ? sh.count[1][lane] : 0);
   }
   int32_t* out = kept + p.first;
   const int t0 = lo + lane;
@@ -578,7 +603,6 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
       place(c, late_key(c));
   }
   finish();
-  if (cluster > 1) cluster_sync();  // no block leaves while another may still read its counts
 }
 
 // Moves the kept rows of 128 new positions of one head, K and V: the two share

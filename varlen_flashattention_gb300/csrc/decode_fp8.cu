@@ -72,7 +72,8 @@ struct Fp8DecodeParams {
   float scale_log2;
   int32_t* tile_base;  // [B + 1] 16-token tiles of the sequences before b
   int32_t max_parts;   // most parts of the line
-  int32_t* errors;     // [1 + warps of the main kernel]: lengths, then the warps' pages
+  int32_t grid;        // blocks of the main kernel (four warps each)
+  uint8_t* errors;     // a byte for each warp of the main kernel (pages), then a 32-bit word (lengths)
   float* part_o;       // [parts + B][hkv][rows][D], normalised
   float* part_lse2;    // [parts + B][hkv][rows], log2, -inf when empty
   __nv_bfloat16* o;
@@ -190,7 +191,7 @@ __device__ __forceinline__ bool f8_number_tiles(const Fp8DecodeParams& p, int32_
 __global__ void __launch_bounds__(1024) fp8_decode_plan_kernel(const Fp8DecodeParams p) {
   allow_next_grid();
   const bool bad = f8_number_tiles<1024>(p, p.tile_base);
-  if (threadIdx.x == 0) p.errors[0] = bad;
+  if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.errors)[p.grid] = bad;
 }
 
 // The line of tiles, cut into parts of equal length.
@@ -203,7 +204,11 @@ struct F8Line {
   }
   __device__ __forceinline__ int begin(int64_t i) const { return static_cast<int>(i * total / parts); }
   // the part that holds tile x: the last i with floor(i total / parts) <= x
-  __device__ __forceinline__ int part_of(int64_t x) const { return static_cast<int>(((x + 1) * parts - 1) / total); }
+  __device__ __forceinline__ int part_of(int64_t x) const {
+    const uint64_t n = static_cast<uint64_t>((x + 1) * parts - 1);
+    return static_cast<int>(n >> 32 ? n / static_cast<uint64_t>(total)
+                                    : static_cast<uint32_t>(n) / static_cast<uint32_t>(total));
+  }
 };
 
 // The sequence that holds tile x (a warp's lanes look at 32 bounds at a time).
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     const bool bad = f8_number_tiles<128>(p, s_base);
     if (blockIdx.x == 0) {
       for (int i = threadIdx.x; i <= p.batch; i += 128) p.tile_base[i] = s_base[i];
-      if (threadIdx.x == 0) p.errors[0] = bad;
+      if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.errors)[p.grid] = bad;
     }
     tile_base = s_base;
   } else {
@@ -606,33 +611,44 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     __syncwarp();  // the ring is filled again for the next job
   }
   bad_page = __any_sync(0xffffffffu, bad_page);
-  if (lane == 0) p.errors[1 + blockIdx.x * kF8Warps + warp] = bad_page;
+  if (lane == 0) p.errors[blockIdx.x * kF8Warps + warp] = bad_page;
 }
 
 // Joins the parts of the sequences that were cut:
 //   lse = log2 sum_i 2^lse_i, O = sum_i 2^(lse_i - lse) O_i,
-// in a fixed order; a sequence without tokens gets zeros and -inf. Block 0 also
+// in a fixed order; a sequence without tokens gets zeros and -inf. The last block
 // gathers the main kernel's findings into the status block.
 // Two shapes. kWide = false: a block of four warps per output row, each with a
 // run of the parts (many sequences, of a dozen parts or so each). kWide = true:
 // a block per 32 columns of a row, its 32 groups of eight lanes reading a part's
 // 128-byte piece each, four ahead, so that a sequence cut into hundreds of parts
 // is joined by all SMs.
-__device__ __forceinline__ void f8_report(const Fp8DecodeParams& p, int num_errors) {
-  bool bad = false;
-  for (int i = threadIdx.x; i < num_errors; i += blockDim.x) bad |= __ldcg(p.errors + i) != 0;
-  bad = __syncthreads_or(bad);
+template <int THREADS>
+__device__ __forceinline__ void f8_report(const Fp8DecodeParams& p) {
+  constexpr int kLoads = (kFp8MaxWarps / kF8Warps + THREADS) / THREADS;  // all in flight at once
+  uint32_t v[kLoads];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int i = static_cast<int>(threadIdx.x) + k * THREADS;
+    v[k] = i <= p.grid ? __ldcg(reinterpret_cast<const uint32_t*>(p.errors) + i) : 0u;
+  }
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) any |= v[k];
+  const bool bad = __syncthreads_or(any != 0);
   if (threadIdx.x < kStatusBytes / 4)
     p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8DecodeTable : 0));
 }
 
 constexpr int kF8WideThreads = 256;
 template <int D, bool kWide>
-__global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_kernel(const Fp8DecodeParams p,
-                                                                                       int num_errors) {
+__global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_kernel(const Fp8DecodeParams p) {
   wait_prior_grid();
   allow_next_grid();
-  if (blockIdx.x == 0) f8_report(p, num_errors);
+  if (blockIdx.x == gridDim.x - 1) {
+    f8_report<kWide ? kF8WideThreads : 128>(p);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hkv = p.c.hkv, G = p.group, nrows = G * p.q_len;
   const int slice = kWide ? static_cast<int>(blockIdx.x % (D / 32)) : 0;
@@ -792,37 +808,55 @@ __global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8Decode
   if (count <= 0) return;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int x0 = static_cast<int>(y0 / hkv), h0 = static_cast<int>(y0 % hkv);
-  int b = f8_find_sequence(p.tile_base, p.batch, x0), next = p.tile_base[b + 1];
+  int b = f8_find_sequence(p.tile_base, p.batch, x0), first = p.tile_base[b], next = p.tile_base[b + 1];
   bool bad;
-  int L = f8_length(p, b, &bad), first = p.tile_base[b];
+  int L = f8_length(p, b, &bad);
   const int half = threadIdx.x >> 4, tk = threadIdx.x & 15;
-  for (int i = half; i < count; i += 16) {
-    const int q = fast_div(h0 + i, by_heads), x = x0 + q, h = h0 + i - q * hkv;
-    if (x >= next) {
-      do ++b;
-      while (p.tile_base[b + 1] <= x);
-      next = p.tile_base[b + 1];
-      first = p.tile_base[b];
-      L = f8_length(p, b, &bad);
-    }
-    const int t = (x - first) * 16 + tk;
-    if (t >= L) continue;
-    const int64_t seg = static_cast<int64_t>(b) * hkv + h;
-    const float* lse2 = p.lse2 + seg * nrows;
-    const float* s = p.scores + (y0 + i) * nrows * 16 + tk;
-    const int64_t at = seg * cap + t;
-    float sum = p.w_in ? p.decay * __ldcs(p.w_in + at) : 0.f;
-    for (int r = 0; r < nrows; r += 4) {
-      float v[4], z[4];
+  constexpr int kAhead = 4;  // tiles of a half warp whose loads are in flight together
+  for (int i0 = half; i0 < count; i0 += 16 * kAhead) {
+    int64_t at[kAhead];  // the token's weight, -1: none
+    const float *s[kAhead], *lse2[kAhead];
+    float sum[kAhead];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = r + k < nrows ? __ldcs(s + (r + k) * 16) : -INFINITY;
-        z[k] = r + k < nrows ? lse2[r + k] : 0.f;
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + 16 * k;
+      at[k] = -1;
+      if (i >= count) continue;
+      const int q = fast_div(h0 + i, by_heads), x = x0 + q, h = h0 + i - q * hkv;
+      if (x >= next) {
+        do ++b;
+        while (p.tile_base[b + 1] <= x);
+        first = p.tile_base[b];
+        next = p.tile_base[b + 1];
+        L = f8_length(p, b, &bad);
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum += ptx::ex2(v[k] - z[k]);
+      const int t = (x - first) * 16 + tk;
+      if (t >= L) continue;
+      const int64_t seg = static_cast<int64_t>(b) * hkv + h;
+      at[k] = seg * cap + t;
+      s[k] = p.scores + (y0 + i) * nrows * 16 + tk;
+      lse2[k] = p.lse2 + seg * nrows;
     }
-    p.w_out[at] = sum;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) sum[k] = at[k] >= 0 && p.w_in ? p.decay * p.w_in[at[k]] : 0.f;
+    for (int r = 0; r < nrows; r += 4) {
+      float v[kAhead][4], z[kAhead][4];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = at[k] >= 0 && r + e < nrows;
+          v[k][e] = in ? s[k][(r + e) * 16] : -INFINITY;
+          z[k][e] = in ? lse2[k][r + e] : 0.f;
+        }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[k] += ptx::ex2(v[k][e] - z[k][e]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (at[k] >= 0) p.w_out[at[k]] = sum[k];
   }
 }
 
@@ -854,6 +888,7 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
   p.max_parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(warps / p.c.hkv, tiles)));
   const int grid = static_cast<int>(
       std::min<int64_t>(warps / kF8Warps, (static_cast<int64_t>(p.max_parts) * p.c.hkv + kF8Warps - 1) / kF8Warps));
+  p.grid = grid;
   cudaError_t e;
   if (p.batch > kF8ScanBatch) {
     fp8_decode_plan_kernel<<<1, 1024, 0, stream>>>(p);
@@ -870,10 +905,9 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
   if (e != cudaSuccess) return e;
   // parts a sequence has on average: past 32, the wide join
   const uint32_t rows = static_cast<uint32_t>(p.batch) * p.c.hkv * nrows;
-  const int errors = 1 + grid * kF8Warps;
   e = p.max_parts > 32 * p.batch
-          ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32)), dim3(kF8WideThreads), 0, stream, p, errors)
-          : launch_after(fp8_decode_join_kernel<D, false>, dim3(rows), dim3(128), 0, stream, p, errors);
+          ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p)
+          : launch_after(fp8_decode_join_kernel<D, false>, dim3(rows + 1), dim3(128), 0, stream, p);
   if (e != cudaSuccess || !w) return e;
   return launch_after(fp8_decode_weights_kernel, dim3(static_cast<uint32_t>(sms * 8)), dim3(256), 0, stream, p,
                       make_fast_div(p.c.hkv));

@@ -233,7 +233,7 @@ cudaError_t launch_decode_general(const DecodeLaunch& a, float* part_o, float* p
 constexpr int kFp8MaxWarps = 2560;  // most warps of the decode's main kernel
 struct Fp8DecodeBuffers {
   int32_t* status;
-  int32_t* errors;     // [1 + kFp8MaxWarps]
+  uint8_t* errors;     // [kFp8MaxWarps + 4]
   int32_t* tile_base;  // [B + 1]
   float* part_o;       // [parts + B][kv_heads][rows][D]
   float* part_lse2;    // [parts + B][kv_heads][rows]
