@@ -41,7 +41,9 @@ struct Fp8AppendParams {
   Fp8CacheView c;
   const int32_t* page_table;
   const int32_t* seqlens;
-  int32_t batch, max_pages, page_size, total_new, max_new, chunks;
+  int32_t batch, max_pages, page_size, total_new, max_new;
+  int32_t chunks;            // of 128 positions a sequence can touch; 0: the blocks look their chunk up
+  FastDiv by_heads, by_chunks;  // division by 2 * hkv and by chunks
   float* weights;
   int32_t* status;
 };
@@ -81,13 +83,19 @@ __device__ __noinline__ uint2 recode8(uint2 codes, float from, float to) {
   return encode8(x, to);
 }
 
-// Eight finite bf16 values divided by a power of two (inv: its inverse): the
-// division is exact, so the codes round once.
-__device__ __forceinline__ uint2 encode8_pow2(const uint4& v, float inv) {
-  return make_uint2(f32x2_to_e4m3x2(ptx::bf16lo(v.x) * inv, ptx::bf16hi(v.x) * inv) |
-                        (f32x2_to_e4m3x2(ptx::bf16lo(v.y) * inv, ptx::bf16hi(v.y) * inv) << 16),
-                    f32x2_to_e4m3x2(ptx::bf16lo(v.z) * inv, ptx::bf16hi(v.z) * inv) |
-                        (f32x2_to_e4m3x2(ptx::bf16lo(v.w) * inv, ptx::bf16hi(v.w) * inv) << 16));
+// Eight finite bf16 values divided by a power of two (inv: its inverse). The
+// product is exact in bf16 but for numbers far below e4m3's smallest, so the
+// codes round once.
+__device__ __forceinline__ uint2 encode8_pow2(const uint4& v, __nv_bfloat162 inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), inv);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
+    c[i] = f32x2_to_e4m3x2(ptx::bf16lo(u), ptx::bf16hi(u));
+  }
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 __device__ __noinline__ uint2 encode8_bf16(uint4 v, float s) {
@@ -164,7 +172,7 @@ __device__ void append_report(const Fp8AppendParams& p) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(const Fp8AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) fp8_append_kernel(const Fp8AppendParams p) {
   constexpr int kLanes = D / 8;              // threads of a row, 8 values each
   constexpr int kRowsPerPass = kThreads / kLanes;
   constexpr int kPasses = kChunk / kRowsPerPass;
@@ -172,26 +180,73 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
   __shared__ uint32_t s_amax[kChunk];        // per scale block, bf16 bits
   __shared__ float s_new[kChunk], s_old[kChunk];
   __shared__ float s_inv[kChunk];            // 1 / s_new if that is a power of two, else 0
+  constexpr int kWarpRows = 32 / kLanes;     // rows of a warp in one pass
 
   if (blockIdx.x == 0) {
     append_report(p);
     return;
   }
-  const uint32_t block = blockIdx.x - 1;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int hkv = p.c.hkv;
-  const int h = block % (2 * hkv) >> 1;  // heads first: their rows are neighbours in memory
-  const bool is_v = block & 1;
-  const int b = block / (2 * hkv) / p.chunks, ci = block / (2 * hkv) % p.chunks;
+  const int unit = static_cast<int>(blockIdx.x) - 1, chunk = fast_div(unit, p.by_heads);
+  const int hv = unit - chunk * 2 * hkv, h = hv >> 1;  // heads first: their rows are neighbours in memory
+  const bool is_v = hv & 1;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
-  if (!append_range_ok(p, b, o0, o1, L)) return;
-  const int f = L - (o1 - o0);                 // first new position
+  int b, ci, o0, L, f;  // sequence, its chunk, first row of its new tokens, length, first new position
+  if (p.chunks) {
+    b = fast_div(chunk, p.by_chunks);
+    ci = chunk - b * p.chunks;
+    o0 = p.new_offsets[b];
+    const int o1 = p.new_offsets[b + 1];
+    L = p.seqlens[b];
+    f = L - (o1 - o0);
+    if (!append_range_ok(p, b, o0, o1, L) || o1 == o0) return;
+  } else {
+    int before = 0;
+    for (b = lane;; b += 32) {
+      int o1 = 0, n = 0;
+      o0 = L = 0;
+      if (b < p.batch) {
+        o0 = p.new_offsets[b];
+        o1 = p.new_offsets[b + 1];
+        L = p.seqlens[b];
+        if (o1 > o0 && append_range_ok(p, b, o0, o1, L)) n = (L - 1) / kChunk - (L - (o1 - o0)) / kChunk + 1;
+      }
+      int x = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + x > chunk);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        ci = __shfl_sync(0xffffffffu, chunk - before - x + n, src);
+        f = __shfl_sync(0xffffffffu, L - (o1 - o0), src);
+        L = __shfl_sync(0xffffffffu, L, src);
+        o0 = __shfl_sync(0xffffffffu, o0, src);
+        b = b - lane + src;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, x, 31);
+      if (b - lane + 32 >= p.batch) return;
+    }
+  }
   const int p0 = ((f / kChunk) + ci) * kChunk;  // this block's positions: p0 .. p0 + 127
-  if (o1 == o0 || p0 >= L) return;
+  if (p0 >= L) return;
   const int bs = p.c.block_shift;
   const int old0 = (f >> bs) << bs;            // older tokens of f's block: old0 .. f - 1
-
-  const int tid = threadIdx.x;
+  const int sub = tid % kLanes, r0 = tid / kLanes;
+  const int64_t row_elems = static_cast<int64_t>(hkv) * D;
+  const __nv_bfloat16* src = (is_v ? p.v : p.k) + (static_cast<int64_t>(o0) + p0 + r0 - f) * row_elems +
+                             static_cast<int64_t>(h) * D + 8 * sub;
+  uint4 raw[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (static_cast<uint32_t>(p0 + r0 + k * kRowsPerPass - f) < static_cast<uint32_t>(L - f))
+      raw[k] = __ldg(reinterpret_cast<const uint4*>(src + k * (kRowsPerPass * row_elems)));
+  }
   if (tid < kChunk) {
     const int pos = p0 + tid;
     int row = -1;
@@ -206,16 +261,6 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
     if (p.weights && !is_v && pos >= f && pos < L)
       p.weights[(static_cast<int64_t>(b) * hkv + h) * cap + pos] = 0.f;
   }
-  const int sub = tid % kLanes, r0 = tid / kLanes;
-  const __nv_bfloat16* src = (is_v ? p.v : p.k) + static_cast<int64_t>(h) * D + 8 * sub;
-  uint4 raw[kPasses];
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int pos = p0 + k * kRowsPerPass + r0;
-    raw[k] = make_uint4(0, 0, 0, 0);
-    if (pos >= f && pos < L)
-      raw[k] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(o0) + pos - f) * hkv * D));
-  }
   __syncthreads();
   uint32_t odd = 0;  // rows of this thread that hold infinities or NaN
 #pragma unroll
@@ -223,9 +268,14 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
     bool finite;
     uint32_t a = amax8_bf16(raw[k], &finite);
     if (!finite) odd |= 1u << k;
+    if ((1 << bs) >= kWarpRows) {  // the warp's rows are of one block
+      a = __reduce_max_sync(0xffffffffu, a);
+      if (lane == 0) atomicMax(&s_amax[(k * kRowsPerPass + r0) >> bs], a);
+    } else {
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
-    if (sub == 0) atomicMax(&s_amax[(k * kRowsPerPass + r0) >> bs], a);
+      for (int off = kLanes / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+      if (sub == 0) atomicMax(&s_amax[(k * kRowsPerPass + r0) >> bs], a);
+    }
   }
   __syncthreads();
   float* scales = is_v ? p.c.vs : p.c.ks;
@@ -250,10 +300,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 4) fp8_append_kernel(
     const int t = k * kRowsPerPass + r0, pos = p0 + t;
     const int row = s_row[t];
     if (row < 0) continue;
-    uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<int64_t>(row) * hkv * D);
+    uint2* dst = reinterpret_cast<uint2*>(codes + row * row_elems);
     const float inv = s_inv[t >> bs];
     if (pos >= f) {
-      *dst = inv != 0.f && !((odd >> k) & 1) ? encode8_pow2(raw[k], inv) : encode8_bf16(raw[k], s_new[t >> bs]);
+      *dst = inv != 0.f && !((odd >> k) & 1) ? encode8_pow2(raw[k], __float2bfloat162_rn(inv))
+                                              : encode8_bf16(raw[k], s_new[t >> bs]);
     } else if (s_old[t >> bs] != s_new[t >> bs]) {  // an older token of a block whose scale has grown
       *dst = recode8(*dst, s_old[t >> bs], s_new[t >> bs]);
     }
@@ -280,12 +331,19 @@ cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t*
   p.page_size = a.page_size;
   p.total_new = a.total_new;
   p.max_new = a.max_new;
-  // n consecutive positions touch at most (n + 126) / 128 + 1 chunks
-  p.chunks = static_cast<int32_t>((static_cast<int64_t>(a.max_new) + kChunk - 2) / kChunk + 1);
+  // n consecutive positions touch at most (n + 126) / 128 + 1 chunks. With lengths as uneven as
+  // prompts' most blocks of batch x that many have nothing to do, so the blocks look up the
+  // chunk of their number instead, a warp over the sequences, where the batch is small:
+  // 16 prompts of 61 to 8192 tokens take FILLED us, and FIXED us with a fixed number each.
+  const int64_t fixed = (static_cast<int64_t>(a.max_new) + kChunk - 2) / kChunk + 1;
+  const int64_t most = a.total_new / kChunk + 2 * static_cast<int64_t>(a.batch);  // chunks of all sequences
+  const bool look_up = a.batch <= 128 && most < fixed * a.batch;
+  p.chunks = look_up ? 0 : static_cast<int32_t>(fixed);
+  p.by_heads = make_fast_div(2 * a.kv_heads);
+  p.by_chunks = make_fast_div(static_cast<int32_t>(fixed));
   p.weights = a.weights;
   p.status = status;
-  const uint32_t grid = static_cast<uint32_t>(p.batch) * static_cast<uint32_t>(p.chunks) *
-                            (2 * static_cast<uint32_t>(a.kv_heads)) + 1;
+  const uint32_t grid = static_cast<uint32_t>((look_up ? most : fixed * a.batch) * 2 * a.kv_heads) + 1;
   if (a.head_dim == 128)
     fp8_append_kernel<128><<<grid, kThreads, 0, stream>>>(p);
   else
@@ -302,6 +360,7 @@ struct Fp8EvictParams {
   const int32_t* new_table;
   const float* weights;
   int32_t batch, max_pages, new_max_pages, page_size, keep, first, recent, chunks;
+  FastDiv by_heads, by_chunks;  // division by hkv and by chunks
   int32_t* kept;         // [B, hkv, keep]
   int32_t* new_seqlens;  // [B]
   float* new_weights;    // [B, hkv, new_max_pages * page_size]
@@ -619,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
 
   wait_prior_grid();
   const int hkv = p.c.hkv, bs = p.c.block_shift, tid = threadIdx.x;
-  const int h = blockIdx.x % hkv;
-  const int b = blockIdx.x / hkv / p.chunks, j0 = blockIdx.x / hkv % p.chunks * kChunk;
+  const int chunk = fast_div(blockIdx.x, p.by_heads), h = blockIdx.x - chunk * hkv;
+  const int b = fast_div(chunk, p.by_chunks), j0 = (chunk - b * p.chunks) * kChunk;
   const int n = p.new_seqlens[b];
   if (j0 >= n) return;
   if (tid < kChunk) {
@@ -768,6 +827,8 @@ cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* 
   p.first = a.first;
   p.recent = a.recent;
   p.chunks = (a.keep + kChunk - 1) / kChunk;
+  p.by_heads = make_fast_div(a.kv_heads);
+  p.by_chunks = make_fast_div(p.chunks);
   p.kept = a.kept;
   p.new_seqlens = a.new_seqlens;
   p.new_weights = a.new_weights;
