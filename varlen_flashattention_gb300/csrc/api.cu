@@ -1072,8 +1072,10 @@ jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size
   if (ws_bytes < fp8_evict_bytes(a->num_pages)) return JFA_ERR_WORKSPACE_TOO_SMALL;
   int32_t* status = static_cast<int32_t*>(ws);
   if (a->batch == 0) return cuda_status(launch_status_clear(status, stream));
+  const int sms = sm_count();
+  if (sms <= 0) return JFA_ERR_CUDA;
   uint32_t* page_state = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  return cuda_status(launch_cache_evict_fp8(*a, page_state, status, stream));
+  return cuda_status(launch_cache_evict_fp8(*a, page_state, status, sms, stream));
 }
 
 jfa_status jfa_selftest_wait_timeout(int32_t budget_us, void* ws, cudaStream_t stream) {

@@ -25,6 +25,8 @@
 // is read once.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "fp8_cache.cuh"
 
 namespace jfa {
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
   const int lo = static_cast<int>(min(c0 + static_cast<int64_t>(rank * kSelWarps + warp) * per_warp, static_cast<int64_t>(c1)));
   const int count = choose ? min(lo + per_warp, c1) - lo - lane : 0;  // keys at w[lo + lane + 32 c], 32 c < count
   w += lo + lane;
+  const int steps = per_warp / 32;
   uint32_t key[KEYS];
   {
     float x[KEYS];
@@ -456,12 +459,19 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     __syncthreads();  // the counts are zero
 #pragma unroll
     for (int c = 0; c < KEYS; ++c) {
-      key[c] = 32 * c < count ? weight_key(x[c]) : 0u;
-      if (32 * c < per_warp) atomicAdd(&sh.hist[0][key[c] >> 24], 1);
+      key[c] = 0u;
+    }
+#pragma unroll
+    for (int g = 0; g < KEYS; g += 4) {
+      if (g >= steps) break;
+#pragma unroll
+      for (int c = g; c < g + 4; ++c) {
+        if (32 * c < count) key[c] = weight_key(x[c]);
+        atomicAdd(&sh.hist[0][key[c] >> 24], 1);  // no weight has digit 0
+      }
     }
   }
   auto late_key = [&](int c) -> uint32_t { return 32 * c < count ? weight_key(__ldg(w + 32 * c)) : 0u; };
-  const int steps = per_warp / 32;
 #pragma unroll 1
   for (int c = KEYS; c < steps; ++c) atomicAdd(&sh.hist[0][late_key(c) >> 24], 1);
   // Everything but the candidates' places: what is certain to stay, zeros, and
@@ -518,8 +528,12 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     if (pass > 0) {
       const int above = 32 - 8 * pass, shift = 24 - 8 * pass;
 #pragma unroll
-      for (int c = 0; c < KEYS; ++c)
-        if ((key[c] >> above) == prefix) atomicAdd(&sh.hist[pass][(key[c] >> shift) & 255], 1);
+      for (int g = 0; g < KEYS; g += 4) {
+        if (g >= steps) break;
+#pragma unroll
+        for (int c = g; c < g + 4; ++c)
+          if ((key[c] >> above) == prefix) atomicAdd(&sh.hist[pass][(key[c] >> shift) & 255], 1);
+      }
 #pragma unroll 1
       for (int c = KEYS; c < steps; ++c) {
         const uint32_t k = late_key(c);
@@ -576,10 +590,19 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
   // Where all of those do, which is the usual case, no rank among them is needed.
   const bool all_equal = sh.hits == need;
   int gt = 0, eq = 0;
+  if (all_equal) {
 #pragma unroll
-  for (int c = 0; c < KEYS; ++c) {
-    gt += key[c] > prefix || (all_equal && key[c] == prefix);
-    if (!all_equal) eq += key[c] == prefix;
+    for (int g = 0; g < KEYS; g += 4) {
+      if (g >= steps) break;
+#pragma unroll
+      for (int c = g; c < g + 4; ++c) gt += key[c] >= prefix;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < KEYS; ++c) {
+      gt += key[c] > prefix;
+      eq += key[c] == prefix;
+    }
   }
 #pragma unroll 1
   for (int c = KEYS; c < steps; ++c) {
@@ -664,31 +687,47 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
   finish();
 }
 
-// Moves the kept rows of 128 new positions of one head, K and V: the two share
-// the chain of loads that finds a row (kept position, page, row), which is
-// what a block waits for, and give each thread twice the rows in flight.
+// Moves the kept rows, 128 new positions of one head, K and V, at a time. What
+// finds a row is a chain of loads (kept position, page, state of the new page)
+// longer than the row's own, so the blocks stay and look up the next chunk's
+// rows while this one's are on their way.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8EvictParams p, int jobs) {
   constexpr int kLanes = D / 16;             // threads of a row, 16 codes each
   constexpr int kRowsPerPass = kThreads / kLanes;
   constexpr int kPasses = kChunk / kRowsPerPass;
-  __shared__ int32_t s_src[kChunk], s_dst[kChunk];  // cache rows, -1: none
+  __shared__ int32_t s_src[2][kChunk], s_dst[2][kChunk];  // cache rows, -1: none
   __shared__ uint32_t s_amax[2][kChunk];
   __shared__ float s_new[2][kChunk];
 
   wait_prior_grid();
   const int hkv = p.c.hkv, bs = p.c.block_shift, tid = threadIdx.x;
-  const int chunk = fast_div(blockIdx.x, p.by_heads), h = blockIdx.x - chunk * hkv;
-  const int b = fast_div(chunk, p.by_chunks), j0 = (chunk - b * p.chunks) * kChunk;
-  const int n = p.new_seqlens[b];
-  if (j0 >= n) return;
-  if (tid < kChunk) {
-    const int j = j0 + tid;
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int64_t new_cap = static_cast<int64_t>(p.new_max_pages) * p.page_size;
+  const int sub = tid % kLanes, r0 = tid / kLanes;
+  const int blocks = kChunk >> bs;
+  // job = (sequence, chunk, head), heads first
+  auto place = [&](int job, int& b, int& j0, int& h) {
+    const int chunk = fast_div(job, p.by_heads);
+    h = job - chunk * hkv;
+    b = fast_div(chunk, p.by_chunks);
+    j0 = (chunk - b * p.chunks) * kChunk;
+  };
+  auto kept_of = [&](int job) -> int {  // old position of this thread's new one, -1: none
+    if (job >= jobs || tid >= kChunk) return -1;
+    int b, j0, h;
+    place(job, b, j0, h);
+    return j0 + tid < p.keep ? p.kept[(static_cast<int64_t>(b) * hkv + h) * p.keep + j0 + tid] : -1;
+  };
+  auto look_up = [&](int job, int t, int buf) {
+    if (job >= jobs || tid >= kChunk) return;
     int src = -1, dst = -1;
-    if (j < n) {
+    if (t >= 0) {
+      int b, j0, h;
+      place(job, b, j0, h);
+      const int j = j0 + tid;
       const int64_t seg = static_cast<int64_t>(b) * hkv + h;
-      const int t = p.kept[seg * p.keep + j];
-      p.new_weights[seg * p.new_max_pages * p.page_size + j] = p.weights[seg * p.max_pages * p.page_size + t];
+      const float weight = p.weights[seg * cap + t];
       const int pg = fast_div(t, p.c.page), npg = fast_div(j, p.c.page);
       const uint32_t page = static_cast<uint32_t>(p.page_table[static_cast<int64_t>(b) * p.max_pages + pg]);
       const uint32_t fresh = static_cast<uint32_t>(p.new_table[static_cast<int64_t>(b) * p.new_max_pages + npg]);
@@ -697,80 +736,90 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
       // a page that some sequence still reads, or that is given out twice, is not written
       if (fresh < pages && p.page_state[fresh] == 1u) dst = static_cast<int>(fresh) * p.page_size + (j - npg * p.page_size);
       if (src < 0 || dst < 0) flag_bad_cache(p.status, kSiteFp8Evict);
+      p.new_weights[seg * new_cap + j] = weight;
     }
-    s_src[tid] = src;
-    s_dst[tid] = dst;
-    s_amax[0][tid] = s_amax[1][tid] = 0;
-  }
-  __syncthreads();
-  const int sub = tid % kLanes, r0 = tid / kLanes;
-  uint8_t* codes[2] = {p.c.kc + static_cast<int64_t>(h) * D + 16 * sub, p.c.vc + static_cast<int64_t>(h) * D + 16 * sub};
-  float* scales[2] = {p.c.ks + h, p.c.vs + h};
-  uint4 raw[2][kPasses];
-  float sc[2][kPasses];
+    s_src[buf][tid] = src;
+    s_dst[buf][tid] = dst;
+  };
+  const int step = gridDim.x;
+  int t_next = kept_of(blockIdx.x);
+  look_up(blockIdx.x, t_next, 0);
+  t_next = kept_of(blockIdx.x + step);
+  int buf = 0;
+  for (int job = blockIdx.x; job < jobs; job += step, buf ^= 1) {
+    if (tid < kChunk) s_amax[0][tid] = s_amax[1][tid] = 0;
+    __syncthreads();  // this chunk's rows are known
+    int b, j0, h;
+    place(job, b, j0, h);
+    uint8_t* codes[2] = {p.c.kc + static_cast<int64_t>(h) * D + 16 * sub, p.c.vc + static_cast<int64_t>(h) * D + 16 * sub};
+    float* scales[2] = {p.c.ks + h, p.c.vs + h};
+    uint4 raw[2][kPasses];
+    float sc[2][kPasses];
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int src = s_src[k * kRowsPerPass + r0];
+    for (int k = 0; k < kPasses; ++k) {
+      const int src = s_src[buf][k * kRowsPerPass + r0];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      raw[v][k] = make_uint4(0, 0, 0, 0);  // a token whose page is missing becomes zeros
-      sc[v][k] = 0.f;
-      if (src >= 0) {
-        raw[v][k] = *reinterpret_cast<const uint4*>(codes[v] + static_cast<int64_t>(src) * hkv * D);
-        sc[v][k] = scales[v][static_cast<int64_t>(src >> bs) * hkv];
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const uint32_t w[4] = {raw[v][k].x, raw[v][k].y, raw[v][k].z, raw[v][k].w};
-      __half2 top = __float2half2_rn(0.f);  // largest magnitude; the maximum passes over NaN
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t lo, hi;
-        e4m3x4_to_f16(w[i] & 0x7F7F7F7Fu, lo, hi);
-        top = __hmax2(top, __hmax2(*reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&hi)));
-      }
-      float a = __half2float(__hmax(__low2half(top), __high2half(top)));
-#pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-      if (sub == 0)
-        atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(fminf(a * sc[v][k], 3.4028234e38f)));
-    }
-  }
-  __syncthreads();
-  const int blocks = kChunk >> bs;
-  if (tid < 2 * blocks) {
-    const int v = tid >= blocks, i = tid - v * blocks;
-    const float s = e4m3_block_scale(__uint_as_float(s_amax[v][i]));
-    s_new[v][i] = s;
-    const int dst = s_dst[i << bs];
-    if (dst >= 0) scales[v][static_cast<int64_t>(dst >> bs) * hkv] = s;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int t = k * kRowsPerPass + r0;
-    const int dst = s_dst[t];
-    if (dst < 0) continue;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const float s = s_new[v][t >> bs], from = sc[v][k];
-      uint4 out = raw[v][k];
-      if (s != from) {
-        // both powers of two: the ratio is one, and is exact; below fp16's range nothing is left of the codes
-        const float ratio = from / s;
-        if (is_pow2(from) && ratio <= 32768.f) {
-          const __half2 r = __float2half2_rn(ratio);
-          out = make_uint4(scale4_pow2(out.x, r), scale4_pow2(out.y, r), scale4_pow2(out.z, r), scale4_pow2(out.w, r));
-        } else {
-          const uint2 lo = recode8(make_uint2(out.x, out.y), from, s), hi = recode8(make_uint2(out.z, out.w), from, s);
-          out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      for (int v = 0; v < 2; ++v) {
+        raw[v][k] = make_uint4(0, 0, 0, 0);  // a token whose page is missing becomes zeros
+        sc[v][k] = 0.f;
+        if (src >= 0) {
+          raw[v][k] = *reinterpret_cast<const uint4*>(codes[v] + static_cast<int64_t>(src) * hkv * D);
+          sc[v][k] = scales[v][static_cast<int64_t>(src >> bs) * hkv];
         }
       }
-      *reinterpret_cast<uint4*>(codes[v] + static_cast<int64_t>(dst) * hkv * D) = out;
+    }
+    look_up(job + step, t_next, buf ^ 1);
+    t_next = kept_of(job + 2 * step);
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t w[4] = {raw[v][k].x, raw[v][k].y, raw[v][k].z, raw[v][k].w};
+        __half2 top = __float2half2_rn(0.f);  // largest magnitude; the maximum passes over NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t lo, hi;
+          e4m3x4_to_f16(w[i] & 0x7F7F7F7Fu, lo, hi);
+          top = __hmax2(top, __hmax2(*reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&hi)));
+        }
+        float a = __half2float(__hmax(__low2half(top), __high2half(top)));
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        if (sub == 0)
+          atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(fminf(a * sc[v][k], 3.4028234e38f)));
+      }
+    }
+    __syncthreads();
+    if (tid < 2 * blocks) {
+      const int v = tid >= blocks, i = tid - v * blocks;
+      const float s = e4m3_block_scale(__uint_as_float(s_amax[v][i]));
+      s_new[v][i] = s;
+      const int dst = s_dst[buf][i << bs];
+      if (dst >= 0) scales[v][static_cast<int64_t>(dst >> bs) * hkv] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      const int t = k * kRowsPerPass + r0;
+      const int dst = s_dst[buf][t];
+      if (dst < 0) continue;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float s = s_new[v][t >> bs], from = sc[v][k];
+        uint4 out = raw[v][k];
+        if (s != from) {
+          // both powers of two: the ratio is one, and is exact; below fp16's range nothing is left of the codes
+          const float ratio = from / s;
+          if (is_pow2(from) && ratio <= 32768.f) {
+            const __half2 r = __float2half2_rn(ratio);
+            out = make_uint4(scale4_pow2(out.x, r), scale4_pow2(out.y, r), scale4_pow2(out.z, r), scale4_pow2(out.w, r));
+          } else {
+            const uint2 lo = recode8(make_uint2(out.x, out.y), from, s), hi = recode8(make_uint2(out.z, out.w), from, s);
+            out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          }
+        }
+        *reinterpret_cast<uint4*>(codes[v] + static_cast<int64_t>(dst) * hkv * D) = out;
+      }
     }
   }
 }
@@ -804,7 +853,7 @@ static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
                                                                  : launch_select_keys<32>(p, cluster, stream);
 }
 
-cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status,
+cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status, int sms,
                                    cudaStream_t stream) {
   Fp8EvictParams p{};
   p.c.kc = static_cast<uint8_t*>(a.k_cache);
@@ -840,9 +889,10 @@ cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* 
   if (e != cudaSuccess) return e;
   e = launch_select(p, stream);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<uint32_t>(a.batch) * static_cast<uint32_t>(p.chunks) * static_cast<uint32_t>(a.kv_heads));
-  return a.head_dim == 128 ? launch_after(fp8_evict_move_kernel<128>, grid, dim3(kThreads), 0, stream, p)
-                           : launch_after(fp8_evict_move_kernel<64>, grid, dim3(kThreads), 0, stream, p);
+  const int jobs = a.batch * p.chunks * a.kv_heads;
+  const dim3 grid(std::min(jobs, sms * 4));
+  return a.head_dim == 128 ? launch_after(fp8_evict_move_kernel<128>, grid, dim3(kThreads), 0, stream, p, jobs)
+                           : launch_after(fp8_evict_move_kernel<64>, grid, dim3(kThreads), 0, stream, p, jobs);
 }
 
 }  // namespace jfa
