@@ -87,18 +87,18 @@ def _need_offsets(t, name):
 def _device(**tensors):
     """The one CUDA device that holds every given tensor (None entries are
     skipped); the call runs there, on that device's stream."""
-    idx = None
+    first = None
     for name, t in tensors.items():
         if t is None:
             continue
         i = t.get_device()  # -1 on the host
+        if first is None:
+            first, idx = t, i
         if i < 0:
             raise ValueError(f"{name} must be on a CUDA device")
-        if idx is None:
-            idx = i
-        elif i != idx:
+        if i != idx:
             raise ValueError(f"{name} is on cuda:{i}, the other tensors on cuda:{idx}")
-    return torch.device("cuda", idx)
+    return first.device
 
 
 def _stream(stream):
@@ -120,8 +120,6 @@ def _events(events):
 
 
 def _workspace(nbytes, device, workspace):
-    if workspace is None:
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor")
     if workspace.get_device() != device.index:
@@ -156,14 +154,27 @@ def _run(entry, size_entry, a, device, workspace, stream, check):
 
 
 def _run_here(entry, size_entry, a, device, workspace, stream, check):
-    if stream is not None and stream.device_index != device.index:
-        raise ValueError(f"stream belongs to {stream.device}, the call runs on {device}")
     ref = ctypes.byref(a)
-    ws = _workspace(_entry(size_entry)(ref), device, workspace)
-    if stream is not None and workspace is None:
-        ws.record_stream(stream)  # allocated on the current stream, used on this one
-    _check(_entry(entry)(ref, ws.data_ptr(), _nbytes(ws), _stream(stream)), entry)
-    _finish(ws, check, stream, entry)
+    need = _entry(size_entry)(ref)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device_index != device.index:
+        raise ValueError(f"stream belongs to {stream.device}, the call runs on {device}")
+    else:
+        raw = stream.cuda_stream
+    if workspace is None:
+        nbytes = max(need, 256)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if stream is not None:
+            ws.record_stream(stream)  # allocated on the current stream, used on this one
+    else:
+        ws = _workspace(need, device, workspace)
+        nbytes = _nbytes(ws)
+    status = _entry(entry)(ref, ws.data_ptr(), nbytes, raw)
+    if status != _abi.JFA_OK:
+        raise JfaError(status, entry)
+    if check:
+        _finish(ws, check, stream, entry)
 
 
 def _check(status, where):
@@ -545,7 +556,22 @@ def _codes(t, name, shape):
 
 def _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k):
     """Shapes of an 8-bit cache and of the batch that reads it; the scales' second
-    dimension gives the block size."""
+    dimension gives the block size. Returns the caches as uint8 and (num_pages, page
+    size, block size, KV heads, head dim, batch, max_pages)."""
+    try:  # the usual case in one test; what follows it names what is wrong
+        num_pages, P, Hkv, d = shape = k_cache.shape
+        pages, blocks, heads = scale_shape = k_scale.shape
+        B, mp = page_table.shape
+        u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+        if (k_cache.dtype is u8 and v_cache.dtype is u8 and k_scale.dtype is f32 and v_scale.dtype is f32 and
+                page_table.dtype is i32 and seqlens_k.dtype is i32 and v_cache.shape == shape and
+                v_scale.shape == scale_shape and seqlens_k.shape == (B,) and pages == num_pages and heads == Hkv and
+                blocks > 0 and P % blocks == 0 and k_cache.is_contiguous() and v_cache.is_contiguous() and
+                k_scale.is_contiguous() and v_scale.is_contiguous() and page_table.is_contiguous() and
+                seqlens_k.is_contiguous()):
+            return k_cache, v_cache, (num_pages, P, P // blocks, Hkv, d, B, mp)
+    except (AttributeError, TypeError, ValueError):
+        pass
     k_cache = _codes(k_cache, "k_cache", 4)
     num_pages, P, Hkv, d = k_cache.shape
     v_cache = _codes(v_cache, "v_cache", k_cache.shape)
@@ -557,8 +583,9 @@ def _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
         raise ValueError(f"k_scale must hold a divisor of the page size {P} in dimension 1, got {blocks}")
     _need(seqlens_k, "seqlens_k", torch.int32, 1)
     _need(page_table, "page_table", torch.int32, 2)
-    _need(page_table, "page_table", torch.int32, (seqlens_k.numel(), page_table.shape[1]))
-    return k_cache, v_cache, num_pages, P, P // blocks, Hkv, d
+    B, mp = page_table.shape
+    _need(page_table, "page_table", torch.int32, (seqlens_k.numel(), mp))
+    return k_cache, v_cache, (num_pages, P, P // blocks, Hkv, d, B, mp)
 
 
 def jfa_cache_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k, new_offsets, max_new,
@@ -570,10 +597,9 @@ def jfa_cache_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, s
     page_table int32 [B, max_pages]; seqlens_k int32 [B]; new_offsets int32 [B+1]; max_new >= every
     sequence's count. weights (optional, fp32 [B, Hkv, max_pages * page_size]) is set to 0 at the new
     positions. Returns (k_cache, v_cache, k_scale, v_scale)."""
-    kc, vc, num_pages, P, block, Hkv, d = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
-    B, mp = page_table.shape
-    _need(k, "k", torch.bfloat16, 3)
-    _need(k, "k", torch.bfloat16, (k.shape[0], Hkv, d))
+    kc, vc, (num_pages, P, block, Hkv, d, B, mp) = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                                     seqlens_k)
+    _need(k, "k", torch.bfloat16, (k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0, Hkv, d))
     _need(v, "v", torch.bfloat16, k.shape)
     _need(new_offsets, "new_offsets", torch.int32, (B + 1,))
     if weights is not None:
@@ -596,16 +622,18 @@ def jfa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k,
     cached token's attention weight, summed over the group's query heads and the query tokens, for
     the tokens of each sequence; weights is updated in place if weights_out is not given, and
     weights_out alone receives the sums. Returns O bf16 [B, q_len, Hq, d], LSE fp32 [B, q_len, Hq]."""
-    _need(q, "q", torch.bfloat16, 4)
-    B, ql, Hq, _ = q.shape
-    kc, vc, num_pages, P, block, Hkv, d = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
-    _need(q, "q", torch.bfloat16, (seqlens_k.numel(), ql, Hq, d))
-    mp = page_table.shape[1]
+    kc, vc, (num_pages, P, block, Hkv, d, B, mp) = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                                     seqlens_k)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        _need(q, "q", torch.bfloat16, 4)
+    _, ql, Hq, _ = q.shape
+    _need(q, "q", torch.bfloat16, (B, ql, Hq, d))
+    if weights is not None:
+        _need(weights, "weights", torch.float32, (B, Hkv, mp * P))
     if weights_out is None:
         weights_out = weights
-    for n, t in (("weights", weights), ("weights_out", weights_out)):
-        if t is not None:
-            _need(t, n, torch.float32, (B, Hkv, mp * P))
+    else:
+        _need(weights_out, "weights_out", torch.float32, (B, Hkv, mp * P))
     if o is not None:
         _need(o, "o", torch.bfloat16, q.shape)
     if lse is not None:
@@ -614,12 +642,12 @@ def jfa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k,
                   seqlens_k=seqlens_k, weights=weights, weights_out=weights_out, o=o, lse=lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, ql, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    lse = k_scale.new_empty((B, ql, Hq)) if lse is None else lse
     a = _abi.DecodeFp8Args(_ptr(q), _ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
                            _ptr(seqlens_k), B, ql, Hq, Hkv, d, P, block, num_pages, mp, scale, _ptr(o), _ptr(lse),
                            _ptr(weights), _ptr(weights_out), float(decay), None)
-    ev, _keep = _events(events)
-    a.main_kernel_events = ev
+    if events is not None:
+        a.main_kernel_events, _keep = _events(events)
     _run("jfa_decode_fp8", "jfa_decode_fp8_workspace_size", a, dev, workspace, stream, check)
     return o, lse
 
@@ -633,30 +661,31 @@ def jfa_cache_evict_fp8(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_
     tokens a row, pages that no sequence of the call holds). weights: fp32 [B, Hkv, max_pages *
     page_size], as jfa_decode_fp8 accumulates them. Returns kept int32 [B, Hkv, keep] (old positions,
     -1 past the end), new_seqlens int32 [B] and new_weights fp32 [B, Hkv, new_max_pages * page_size]."""
-    kc, vc, num_pages, P, block, Hkv, d = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k)
-    B, mp = page_table.shape
-    keep = int(keep)
+    kc, vc, (num_pages, P, block, Hkv, d, B, mp) = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                                     seqlens_k)
+    keep, first, recent = int(keep), int(first), int(recent)
     _need(weights, "weights", torch.float32, (B, Hkv, mp * P))
-    _need(new_page_table, "new_page_table", torch.int32, 2)
-    nmp = new_page_table.shape[1]
+    nmp = new_page_table.shape[1] if isinstance(new_page_table, torch.Tensor) and new_page_table.dim() == 2 else 0
     _need(new_page_table, "new_page_table", torch.int32, (B, nmp))
     if keep < 1 or first < 0 or recent < 0 or first + recent > keep:
         raise ValueError(f"keep must be >= 1 and first + recent at most keep, got {keep}, {first}, {recent}")
     if nmp * P < keep:
         raise ValueError(f"new_page_table holds {nmp * P} tokens a sequence, keep is {keep}")
-    shapes = (("kept", kept, torch.int32, (B, Hkv, keep)), ("new_seqlens", new_seqlens, torch.int32, (B,)),
-              ("new_weights", new_weights, torch.float32, (B, Hkv, nmp * P)))
-    for n, t, dtype, shape in shapes:
-        if t is not None:
-            _need(t, n, dtype, shape)
+    if kept is not None:
+        _need(kept, "kept", torch.int32, (B, Hkv, keep))
+    if new_seqlens is not None:
+        _need(new_seqlens, "new_seqlens", torch.int32, (B,))
+    if new_weights is not None:
+        _need(new_weights, "new_weights", torch.float32, (B, Hkv, nmp * P))
     dev = _device(k_cache=kc, v_cache=vc, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
                   seqlens_k=seqlens_k, weights=weights, new_page_table=new_page_table, kept=kept,
                   new_seqlens=new_seqlens, new_weights=new_weights)
-    kept, new_seqlens, new_weights = (torch.empty(shape, dtype=dtype, device=dev) if t is None else t
-                                      for _, t, dtype, shape in shapes)
+    kept = page_table.new_empty((B, Hkv, keep)) if kept is None else kept
+    new_seqlens = torch.empty_like(seqlens_k) if new_seqlens is None else new_seqlens
+    new_weights = weights.new_empty((B, Hkv, nmp * P)) if new_weights is None else new_weights
     a = _abi.CacheEvictFp8Args(_ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(seqlens_k),
                                _ptr(weights), _ptr(new_page_table), B, Hkv, d, P, block, num_pages, mp, nmp, keep,
-                               int(first), int(recent), _ptr(kept), _ptr(new_seqlens), _ptr(new_weights))
+                               first, recent, _ptr(kept), _ptr(new_seqlens), _ptr(new_weights))
     _run("jfa_cache_evict_fp8", "jfa_cache_evict_fp8_workspace_size", a, dev, workspace, stream, check)
     return kept, new_seqlens, new_weights
 
