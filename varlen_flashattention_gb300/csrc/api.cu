@@ -279,7 +279,10 @@ Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
   return L;
 }
 
-size_t fp8_evict_bytes(int64_t num_pages) { return align_up(kStatusBytes + 4 * static_cast<size_t>(num_pages), 256); }
+// Evict: the status block and a byte for each entry of the new page table.
+size_t fp8_evict_bytes(int64_t batch, int64_t new_max_pages) {
+  return align_up(kStatusBytes + static_cast<size_t>(batch) * new_max_pages, 256);
+}
 
 // ------------------------------------------------------------------ validation
 
@@ -1046,7 +1049,7 @@ jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* a, void* ws, size_t ws_byte
 }
 
 size_t jfa_cache_evict_fp8_workspace_size(const jfa_cache_evict_fp8_args* a) {
-  return a ? fp8_evict_bytes(a->num_pages > 0 ? a->num_pages : 0) : 0;
+  return a ? fp8_evict_bytes(std::max(a->batch, 0), std::max(a->new_max_pages, 0)) : 0;
 }
 
 jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
@@ -1065,17 +1068,16 @@ jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size
   // other blocks still read what these would overwrite
   if (a->batch > 0 && (a->new_seqlens == a->seqlens_k || a->new_weights == a->weights)) return JFA_ERR_INVALID_ARG;
   // blocks of the grids: batch x heads x chunks of 128 kept tokens, or up to 8 of the selection
-  const double segs = static_cast<double>(a->batch) * a->kv_heads;
+  const double segs = static_cast<double>(a->batch) * a->kv_heads + 1;
   if (segs * std::max<int64_t>(8, (static_cast<int64_t>(a->keep) + 127) / 128) >= 2147483648.0)
     return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
-  if (ws_bytes < fp8_evict_bytes(a->num_pages)) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < fp8_evict_bytes(a->batch, a->new_max_pages)) return JFA_ERR_WORKSPACE_TOO_SMALL;
   int32_t* status = static_cast<int32_t*>(ws);
   if (a->batch == 0) return cuda_status(launch_status_clear(status, stream));
   const int sms = sm_count();
   if (sms <= 0) return JFA_ERR_CUDA;
-  uint32_t* page_state = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  return cuda_status(launch_cache_evict_fp8(*a, page_state, status, sms, stream));
+  return cuda_status(launch_cache_evict_fp8(*a, static_cast<uint8_t*>(ws) + kStatusBytes, status, sms, stream));
 }
 
 jfa_status jfa_selftest_wait_timeout(int32_t budget_us, void* ws, cudaStream_t stream) {

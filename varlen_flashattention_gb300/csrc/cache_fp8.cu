@@ -366,20 +366,14 @@ struct Fp8EvictParams {
   int32_t* kept;         // [B, hkv, keep]
   int32_t* new_seqlens;  // [B]
   float* new_weights;    // [B, hkv, new_max_pages * page_size]
-  uint32_t* page_state;  // [num_pages]: bit 31 = read from, below: how often it is written to
+  uint8_t* page_ok;      // [B, new_max_pages]: the new page may be written
+  int32_t bitmap_words;  // of the pages' bitmaps in shared memory
   int32_t* status;
 };
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr uint32_t kPageRead = 0x80000000u;
-
-__global__ void __launch_bounds__(kThreads) fp8_evict_init_kernel(int32_t* status, uint32_t* page_state, int n) {
-  allow_next_grid();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i < kStatusBytes / 4) status[i] = 0;
-  if (i < n) page_state[i] = 0;
-}
+constexpr int kMostBitmapWords = 16384;  // two bitmaps of 64 KB: pages are looked at in runs of 524,288
 
 // Order of the weights as unsigned numbers; NaN counts as -infinity, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -413,27 +407,105 @@ struct alignas(16) SelShared {
   int32_t hits;              // how many there are
 };
 
+// Every sequence's first `used(b)` entries of a table, each once, by one block: a
+// warp a sequence, or all of them on one sequence after the other where there
+// are few. f(b, i, entry) is called by the thread that read the entry.
+template <class Used, class F>
+__device__ __forceinline__ void for_entries(const int32_t* table, int batch, int width, Used used, F f) {
+  const bool few = batch < kSelWarps;
+  const int stride = few ? kSelThreads : 32, first = few ? threadIdx.x : threadIdx.x & 31;
+  for (int b = few ? 0 : threadIdx.x >> 5; b < batch; b += few ? 1 : kSelWarps) {
+    const int n = used(b);
+    const int32_t* row = table + static_cast<int64_t>(b) * width;
+    for (int i0 = first; i0 < n; i0 += 8 * stride) {
+      int32_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = i0 + k * stride < n ? row[i0 + k * stride] : 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * stride < n) f(b, i0 + k * stride, v[k]);
+    }
+  }
+}
+
+// One block checks the call beside the selection: lengths, table entries, and
+// that no new page is one that a sequence still reads or is given out twice.
+// It sets the status block and, for each new page in use, whether the move may
+// write to it; the other blocks pass over what is wrong without a word. That
+// spares the launch that would have to clear the status block, and counters of
+// pages in memory, for them.
+__device__ void evict_check(const Fp8EvictParams& p, uint32_t* bitmap) {
+  uint32_t *taken = bitmap, *bad_page = bitmap + p.bitmap_words;  // read from or given out; given out wrongly
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  bool bad = false;
+  auto length = [&](int b) {
+    const int L = p.seqlens[b];
+    const bool wrong = L < 0 || L > cap || (L > 0 && p.c.num_pages == 0);
+    bad |= wrong;
+    return wrong ? 0 : L;
+  };
+  auto used = [&](int b) {
+    const int L = length(b);
+    return L > 0 ? fast_div(L - 1, p.c.page) + 1 : 0;
+  };
+  auto fresh = [&](int b) {
+    const int n = min(length(b), p.keep);
+    return n > 0 ? fast_div(n - 1, p.c.page) + 1 : 0;
+  };
+  const uint32_t pages = static_cast<uint32_t>(p.c.num_pages), run = static_cast<uint32_t>(p.bitmap_words) * 32u;
+  for (uint32_t base = 0; base == 0 || base < pages; base += run) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.bitmap_words; i += kSelThreads) bitmap[i] = 0;
+    __syncthreads();
+    for_entries(p.page_table, p.batch, p.max_pages, used, [&](int, int, int32_t page) {
+      const uint32_t i = static_cast<uint32_t>(page) - base;
+      bad |= static_cast<uint32_t>(page) >= pages;
+      if (static_cast<uint32_t>(page) < pages && i < run) atomicOr(&taken[i >> 5], 1u << (i & 31));
+    });
+    __syncthreads();
+    for_entries(p.new_table, p.batch, p.new_max_pages, fresh, [&](int, int, int32_t page) {
+      const uint32_t i = static_cast<uint32_t>(page) - base, bit = 1u << (i & 31);
+      if (static_cast<uint32_t>(page) < pages && i < run && (atomicOr(&taken[i >> 5], bit) & bit))
+        atomicOr(&bad_page[i >> 5], bit);
+    });
+    __syncthreads();
+    for_entries(p.new_table, p.batch, p.new_max_pages, fresh, [&](int b, int j, int32_t page) {
+      const uint32_t i = static_cast<uint32_t>(page) - base;
+      const bool in = static_cast<uint32_t>(page) < pages;
+      if (in ? i >= run : base > 0) return;  // another run's
+      const bool ok = in && !((bad_page[i >> 5] >> (i & 31)) & 1);
+      p.page_ok[static_cast<int64_t>(b) * p.new_max_pages + j] = ok;
+      bad |= !ok;
+    });
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x < kStatusBytes / 4)
+    p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8Evict : 0));
+}
+
 template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     fp8_evict_select_kernel(const Fp8EvictParams p, int cluster) {
   __shared__ SelShared sh;
+  extern __shared__ uint32_t s_bitmap[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (static_cast<int>(blockIdx.x) < cluster) {
+    allow_next_grid();
+    if (blockIdx.x == 0) evict_check(p, s_bitmap);
+    return;
+  }
   reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);  // 512 threads: hist and sum
   static_assert(kSelThreads * 16 == sizeof(sh.hist) + sizeof(sh.sum), "one int4 a thread clears both");
   if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before the first addition
-  wait_prior_grid();
   allow_next_grid();
   const int rank = cluster > 1 ? static_cast<int>(blockIdx.x % cluster) : 0;
-  const int seg = blockIdx.x / cluster;
+  const int seg = static_cast<int>(blockIdx.x) / cluster - 1;  // the first cluster's first block checks the call
   const int b = seg / p.c.hkv, h = seg % p.c.hkv;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int new_cap = p.new_max_pages * p.page_size;
   const int wide = cluster * kSelThreads, wtid = rank * kSelThreads + tid;  // threads of the cluster
   int L = p.seqlens[b];
-  if (L < 0 || L > cap || (L > 0 && p.c.num_pages == 0)) {
-    if (tid == 0) flag_bad_cache(p.status, kSiteFp8Evict);
-    L = 0;
-  }
+  if (L < 0 || L > cap || (L > 0 && p.c.num_pages == 0)) L = 0;
   const int n = min(L, p.keep);
   const float* w = p.weights + seg * cap;
   int32_t* kept = p.kept + static_cast<int64_t>(seg) * p.keep;
@@ -474,24 +546,9 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
   auto late_key = [&](int c) -> uint32_t { return 32 * c < count ? weight_key(__ldg(w + 32 * c)) : 0u; };
 #pragma unroll 1
   for (int c = KEYS; c < steps; ++c) atomicAdd(&sh.hist[0][late_key(c) >> 24], 1);
-  // Everything but the candidates' places: what is certain to stay, zeros, and
-  // the pages that this sequence reads and will write.
+  // Everything but the candidates' places: what is certain to stay, and zeros.
   auto finish = [&] {
     if (h == 0 && wtid == 0) p.new_seqlens[b] = n;
-    {  // the sequence's blocks share its pages
-      const int me = h * wide + wtid, all = p.c.hkv * wide;
-      const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-      const int32_t* nt = p.new_table + static_cast<int64_t>(b) * p.new_max_pages;
-      const int used = L > 0 ? fast_div(L - 1, p.c.page) + 1 : 0, fresh = n > 0 ? fast_div(n - 1, p.c.page) + 1 : 0;
-      for (int i = me; i < used; i += all) {
-        const uint32_t pg = static_cast<uint32_t>(pt[i]);
-        if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicOr(p.page_state + pg, kPageRead);
-      }
-      for (int i = me; i < fresh; i += all) {
-        const uint32_t pg = static_cast<uint32_t>(nt[i]);
-        if (pg < static_cast<uint32_t>(p.c.num_pages)) atomicAdd(p.page_state + pg, 1u);
-      }
-    }
     for (int j = n + wtid; j < p.keep; j += wide) kept[j] = -1;
     for (int j = n + wtid; j < new_cap; j += wide) nw[j] = 0.f;
     if (L <= p.keep) {
@@ -733,9 +790,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
       const uint32_t fresh = static_cast<uint32_t>(p.new_table[static_cast<int64_t>(b) * p.new_max_pages + npg]);
       const uint32_t pages = static_cast<uint32_t>(p.c.num_pages);
       if (page < pages) src = static_cast<int>(page) * p.page_size + (t - pg * p.page_size);
-      // a page that some sequence still reads, or that is given out twice, is not written
-      if (fresh < pages && p.page_state[fresh] == 1u) dst = static_cast<int>(fresh) * p.page_size + (j - npg * p.page_size);
-      if (src < 0 || dst < 0) flag_bad_cache(p.status, kSiteFp8Evict);
+      if (p.page_ok[static_cast<int64_t>(b) * p.new_max_pages + npg])  // then it is one of the pages
+        dst = static_cast<int>(fresh) * p.page_size + (j - npg * p.page_size);
       p.new_weights[seg * new_cap + j] = weight;
     }
     s_src[buf][tid] = src;
@@ -827,17 +883,22 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
 template <int KEYS>
 static cudaError_t launch_select_keys(const Fp8EvictParams& p, int cluster, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<uint32_t>(p.batch) * p.c.hkv * cluster);
+  cfg.gridDim = dim3((static_cast<uint32_t>(p.batch) * p.c.hkv + 1) * cluster);
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.bitmap_words) * 8;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(fp8_evict_select_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMostBitmapWords * 8);
+  });
+  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, fp8_evict_select_kernel<KEYS>, p, cluster);
 }
 
@@ -853,7 +914,7 @@ static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
                                                                  : launch_select_keys<32>(p, cluster, stream);
 }
 
-cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status, int sms,
+cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint8_t* page_ok, int32_t* status, int sms,
                                    cudaStream_t stream) {
   Fp8EvictParams p{};
   p.c.kc = static_cast<uint8_t*>(a.k_cache);
@@ -881,13 +942,10 @@ cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* 
   p.kept = a.kept;
   p.new_seqlens = a.new_seqlens;
   p.new_weights = a.new_weights;
-  p.page_state = page_state;
+  p.page_ok = page_ok;
+  p.bitmap_words = std::max(1, std::min((a.num_pages + 31) / 32, kMostBitmapWords));
   p.status = status;
-  const int words = a.num_pages > static_cast<int>(kStatusBytes / 4) ? a.num_pages : static_cast<int>(kStatusBytes / 4);
-  fp8_evict_init_kernel<<<(words + kThreads - 1) / kThreads, kThreads, 0, stream>>>(status, page_state, a.num_pages);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  e = launch_select(p, stream);
+  const cudaError_t e = launch_select(p, stream);
   if (e != cudaSuccess) return e;
   const int jobs = a.batch * p.chunks * a.kv_heads;
   const dim3 grid(std::min(jobs, sms * 4));

@@ -244,7 +244,7 @@ struct Fp8DecodeBuffers {
 inline int64_t fp8_seq_tiles(int64_t max_pages, int64_t page_size) { return (max_pages * page_size + 15) / 16; }
 cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t* status, cudaStream_t stream);
-cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint32_t* page_state, int32_t* status, int sms,
+cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint8_t* page_ok, int32_t* status, int sms,
                                    cudaStream_t stream);
 // Clears a call's status block (a kernel, not a memset, so that the call's next
 // kernel can start as its programmatic dependent).
