@@ -58,6 +58,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8_cache.cuh"
 
@@ -97,13 +98,17 @@ constexpr float kF8NoRef = -3.0e38f;  // a reference before the first visible to
 
 template <int D, int NR>
 struct F8Tile {
-  // By the registers: 128 a thread, or 168 and 255 with 16 rows. 16 rows at head_dim 128 in 168
-  // registers spill: 88 us against 67 us (16 x 0.5k-8k tokens, 4 query tokens of 4 heads).
-  static constexpr int kCtasPerSm = NR == 1 ? 4 : (D == 64 ? 3 : 2);
+  // By the registers: 128 a thread, or 255 with 16 rows. (16 rows at head_dim 128 in 168 registers
+  // spill, 88 us against 67 us for 16 x 0.5k-8k tokens with 4 query tokens of 4 heads; with Q
+  // in shared memory instead of 32 of the registers they take 70 us.)
+  static constexpr int kCtasPerSm = NR == 1 ? 4 : 2;
+  // Tiles computed together. 16 rows leave 8 warps an SM, too few to cover the chain of a tile's
+  // steps by each other's work: two tiles give each warp two such chains.
+  static constexpr int kTogether = NR;
   // One tile on its way while one is computed, per warp: with 16 warps that is
   // 68 KB an SM. More queue up in front of the memory: 32 x 1k-32k tokens, NR 1,
-  // take 175 us with 2 stages and 187 us with 3. With 8 warps it takes two.
-  static constexpr int kStages = NR == 1 ? 2 : 3;
+  // take 175 us with 2 stages and 187 us with 3. With 8 warps that is two, and two computed.
+  static constexpr int kStages = NR == 1 ? 2 : 4;
   static constexpr int kVOff = 16 * D;           // K rows, V rows, 16 + 16 scales
   static constexpr int kScaleOff = 32 * D;
   static constexpr int kStageBytes = kScaleOff + 128;
@@ -133,6 +138,13 @@ __device__ __forceinline__ void f8_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 __device__ __forceinline__ uint32_t f8_pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// log2 of a scale (0, for a missing token, gives -inf).
+__device__ __forceinline__ float f8_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // 8 x 8 matrix of 16-bit elements, transposed between the lanes of a warp.
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     };
     enter();
     look_up(x0);
-    for (int i = 0; i < kStages - 1; ++i) {
+    for (int i = 0; i < kStages - T::kTogether; ++i) {
       issue(i);
       look_up(x0 + i + 1);
     }
@@ -396,76 +408,104 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
         for (int j = 0; j < kSteps; ++j) acc[u][j][0] = acc[u][j][1] = acc[u][j][2] = acc[u][j][3] = 0.f;
       }
 
-      for (; x < x_stop; ++x) {
+      // ---- N neighbouring tiles, from tile x of the line on
+      auto step = [&](auto tag) {
+        constexpr int N = decltype(tag)::value;
         const int i = x - x0;
-        const int t0 = (x - base) * 16;
-        __syncwarp();  // every lane has read the slot that is refilled now (tile i - 1)
-        issue(i + kStages - 1);
-        look_up(x + kStages);
-        f8_wait<kStages - 1>();  // this lane's copies of tile i have landed
-        __syncwarp();            // and the other lanes'
-        const uint8_t* st = ring + (i % kStages) * T::kStageBytes;
-        const float* sc = reinterpret_cast<const float*>(st + T::kScaleOff);
-        const float ks0 = sc[gq], ks1 = sc[gq + 8];
-        const float lv0 = __log2f(sc[16 + gq]), lv1 = __log2f(sc[24 + gq]);
-
-        // S^T = K Q^T
-        float s[NR][4];
+        __syncwarp();  // every lane has read the slots that are refilled now
 #pragma unroll
-        for (int u = 0; u < NR; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint8_t* src = D == 128 ? st + gq * 128 + (((qq + 4 * c) ^ ((gq & 1) << 2)) << 4)
-                                        : st + gq * 64 + (qq << 4);
-          const uint4 k0 = *reinterpret_cast<const uint4*>(src);
-          const uint4 k1 = *reinterpret_cast<const uint4*>(src + 8 * D);
-          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16(w0[w], a0, a2);
-            e4m3x4_to_f16(w1[w], a1, a3);
-#pragma unroll
-            for (int u = 0; u < NR; ++u) f8_mma(s[u], a0, a1, a2, a3, qb[u][4 * c + w][0], qb[u][4 * c + w][1]);
-          }
+        for (int t = 0; t < N; ++t) {
+          issue(i + kStages - T::kTogether + t);
+          look_up(x + kStages - T::kTogether + t + 1);
         }
-        // scaled scores: s[u][0..1] token g, rows 2q and 2q + 1; s[u][2..3] token g + 8
-        const bool partial = t0 + 16 > lim_min;
-        bool raise = false;
+        f8_wait<kStages - T::kTogether>();  // this lane's copies of the N tiles have landed
+        __syncwarp();                       // and the other lanes'
+        const uint8_t* st[N];
+        int t0[N];
+        float ks[N][2], lv[N][2], s[N][NR][4];
 #pragma unroll
-        for (int u = 0; u < NR; ++u) {
+        for (int t = 0; t < N; ++t) {
+          st[t] = ring + ((i + t) % kStages) * T::kStageBytes;
+          t0[t] = (x + t - base) * 16;
+          const float* sc = reinterpret_cast<const float*>(st[t] + T::kScaleOff);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            s[u][e] *= ks0 * rq[u][e];
-            s[u][2 + e] *= ks1 * rq[u][e];
-            if (partial) {
-              if (t0 + gq >= lim[u][e]) s[u][e] = -INFINITY;
-              if (t0 + gq + 8 >= lim[u][e]) s[u][2 + e] = -INFINITY;
-            }
-            raise |= fmaxf(s[u][e], s[u][2 + e]) > m[u][e] + kF8Slack;
-            raise |= fmaxf(s[u][e] + lv0, s[u][2 + e] + lv1) > n[u][e] + (kF8WShift + kF8Slack);
+            ks[t][e] = sc[gq + 8 * e];
+            lv[t][e] = f8_log2(sc[16 + gq + 8 * e]);
           }
         }
-        if constexpr (WEIGHTS) {
-          float* out = p.scores + (static_cast<int64_t>(x) * hkv + h) * nrows * 16;
+
+        // S^T = K Q^T
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+          for (int u = 0; u < NR; ++u) s[t][u][0] = s[t][u][1] = s[t][u][2] = s[t][u][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 k0[N], k1[N];
+#pragma unroll
+          for (int t = 0; t < N; ++t) {
+            const uint8_t* src = D == 128 ? st[t] + gq * 128 + (((qq + 4 * c) ^ ((gq & 1) << 2)) << 4)
+                                          : st[t] + gq * 64 + (qq << 4);
+            k0[t] = *reinterpret_cast<const uint4*>(src);
+            k1[t] = *reinterpret_cast<const uint4*>(src + 8 * D);
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(w == 0 ? k0[t].x : (w == 1 ? k0[t].y : (w == 2 ? k0[t].z : k0[t].w)), a0, a2);
+              e4m3x4_to_f16(w == 0 ? k1[t].x : (w == 1 ? k1[t].y : (w == 2 ? k1[t].z : k1[t].w)), a1, a3);
+#pragma unroll
+              for (int u = 0; u < NR; ++u) f8_mma(s[t][u], a0, a1, a2, a3, qb[u][4 * c + w][0], qb[u][4 * c + w][1]);
+            }
+        }
+        // scaled scores: s[..][0..1] token g, rows 2q and 2q + 1; s[..][2..3] token g + 8
+        const bool partial = t0[N - 1] + 16 > lim_min;
+        bool raise = false;
+#pragma unroll
+        for (int t = 0; t < N; ++t)
 #pragma unroll
           for (int u = 0; u < NR; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int r = 8 * u + 2 * qq + e;
-              if (r < nrows) {
-                out[r * 16 + gq] = s[u][e];
-                out[r * 16 + gq + 8] = s[u][2 + e];
+              s[t][u][e] *= ks[t][0] * rq[u][e];
+              s[t][u][2 + e] *= ks[t][1] * rq[u][e];
+              if (partial) {
+                if (t0[t] + gq >= lim[u][e]) s[t][u][e] = -INFINITY;
+                if (t0[t] + gq + 8 >= lim[u][e]) s[t][u][2 + e] = -INFINITY;
               }
+              raise |= fmaxf(s[t][u][e], s[t][u][2 + e]) > m[u][e] + kF8Slack;
+              raise |= fmaxf(s[t][u][e] + lv[t][0], s[t][u][2 + e] + lv[t][1]) > n[u][e] + (kF8WShift + kF8Slack);
             }
+        if constexpr (WEIGHTS) {
+#pragma unroll
+          for (int t = 0; t < N; ++t) {
+            float* out = p.scores + (static_cast<int64_t>(x + t) * hkv + h) * nrows * 16;
+#pragma unroll
+            for (int u = 0; u < NR; ++u)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = 8 * u + 2 * qq + e;
+                if (r < nrows) {
+                  out[r * 16 + gq] = s[t][u][e];
+                  out[r * 16 + gq + 8] = s[t][u][2 + e];
+                }
+              }
+          }
         }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
           for (int u = 0; u < NR; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float a = fmaxf(s[u][e], s[u][2 + e]);
-              float c = fmaxf(s[u][e] + lv0, s[u][2 + e] + lv1);
+              float a = -INFINITY, c = -INFINITY;
+#pragma unroll
+              for (int t = 0; t < N; ++t) {
+                a = fmaxf(a, fmaxf(s[t][u][e], s[t][u][2 + e]));
+                c = fmaxf(c, fmaxf(s[t][u][e] + lv[t][0], s[t][u][2 + e] + lv[t][1]));
+              }
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) {
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
@@ -484,60 +524,69 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
             }
         }
         // P^T as the B operand
-        uint32_t pb2[NR][2];
+        uint32_t pt2[N][NR][2];
 #pragma unroll
-        for (int u = 0; u < NR; ++u) {
+        for (int t = 0; t < N; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) l[u][e] += ptx::ex2(s[u][e] - m[u][e]) + ptx::ex2(s[u][2 + e] - m[u][e]);
-          pb2[u][0] = f8_transpose(f8_pack_f16(ptx::ex2(s[u][0] + lv0 - n[u][0]), ptx::ex2(s[u][1] + lv0 - n[u][1])));
-          pb2[u][1] = f8_transpose(f8_pack_f16(ptx::ex2(s[u][2] + lv1 - n[u][0]), ptx::ex2(s[u][3] + lv1 - n[u][1])));
-        }
-        // O^T += V^T P^T
-        uint32_t vw[4][kEpl / 4];
+          for (int u = 0; u < NR; ++u) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint8_t* vt = st + T::kVOff;
-          if constexpr (D == 128) {  // token 2q + (w & 1) + 8 (w / 2), piece g
-            const uint4 v = *reinterpret_cast<const uint4*>(vt + (2 * qq + (w & 1) + 8 * (w >> 1)) * 128 +
-                                                            ((gq ^ (2 * qq)) << 4));
-            vw[w][0] = v.x;
-            vw[w][1] = v.y;
-            vw[w][2] = v.z;
-            vw[w][3] = v.w;
-          } else {  // line q + 4 (w / 2), half w & 1, piece g / 2, its half g & 1
-            const uint2 v = *reinterpret_cast<const uint2*>(vt + (qq + 4 * (w >> 1)) * 128 +
-                                                            (((((w & 1) << 2) | (gq >> 1)) ^ (2 * qq)) << 4) +
-                                                            ((gq & 1) << 3));
-            vw[w][0] = v.x;
-            vw[w][1] = v.y;
+            for (int e = 0; e < 2; ++e)
+              l[u][e] += ptx::ex2(s[t][u][e] - m[u][e]) + ptx::ex2(s[t][u][2 + e] - m[u][e]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              pt2[t][u][k] = f8_transpose(f8_pack_f16(ptx::ex2(s[t][u][2 * k] + lv[t][k] - n[u][0]),
+                                                      ptx::ex2(s[t][u][2 * k + 1] + lv[t][k] - n[u][1])));
           }
-        }
+        // O^T += V^T P^T
+        uint32_t vw[N][4][kEpl / 4];
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint8_t* vt = st[t] + T::kVOff;
+            if constexpr (D == 128) {  // token 2q + (w & 1) + 8 (w / 2), piece g
+              const uint4 v = *reinterpret_cast<const uint4*>(vt + (2 * qq + (w & 1) + 8 * (w >> 1)) * 128 +
+                                                              ((gq ^ (2 * qq)) << 4));
+              vw[t][w][0] = v.x;
+              vw[t][w][1] = v.y;
+              vw[t][w][2] = v.z;
+              vw[t][w][3] = v.w;
+            } else {  // line q + 4 (w / 2), half w & 1, piece g / 2, its half g & 1
+              const uint2 v = *reinterpret_cast<const uint2*>(vt + (qq + 4 * (w >> 1)) * 128 +
+                                                              (((((w & 1) << 2) | (gq >> 1)) ^ (2 * qq)) << 4) +
+                                                              ((gq & 1) << 3));
+              vw[t][w][0] = v.x;
+              vw[t][w][1] = v.y;
+            }
+          }
         if (partial && QL > 1) {
           // A value that some rows may not see must not reach them even as
           // 0 * NaN: NaN codes leave V and are put into the rows that do see
           // them, where a second product counts them.
-          bool bad_v = false;
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
+          for (int t = 0; t < N; ++t) {
+            bool bad_v = false;
 #pragma unroll
-            for (int k = 0; k < kEpl / 4; ++k) bad_v |= e4m3_any_nan(vw[w][k]);
-          if (__any_sync(0xffffffffu, bad_v)) {
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+              for (int k = 0; k < kEpl / 4; ++k) bad_v |= e4m3_any_nan(vw[t][w][k]);
+            if (!__any_sync(0xffffffffu, bad_v)) continue;
             uint32_t one[4][kEpl / 4];  // e4m3 1.0 (0x38) where the code is NaN
 #pragma unroll
             for (int w = 0; w < 4; ++w)
 #pragma unroll
               for (int k = 0; k < kEpl / 4; ++k) {
-                const uint32_t hit = (((vw[w][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;  // 0x01 per byte
+                const uint32_t hit = (((vw[t][w][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 a byte
                 one[w][k] = hit * 0x38u;
-                vw[w][k] &= ~(hit * 0xFFu);
+                vw[t][w][k] &= ~(hit * 0xFFu);
               }
 #pragma unroll
             for (int u = 0; u < NR; ++u) {
               float see[4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                see[e] = t0 + gq < lim[u][e] ? 1.f : 0.f;
-                see[2 + e] = t0 + gq + 8 < lim[u][e] ? 1.f : 0.f;
+                see[e] = t0[t] + gq < lim[u][e] ? 1.f : 0.f;
+                see[2 + e] = t0[t] + gq + 8 < lim[u][e] ? 1.f : 0.f;
               }
               const uint32_t b0 = f8_transpose(f8_pack_f16(see[0], see[1]));
               const uint32_t b1 = f8_transpose(f8_pack_f16(see[2], see[3]));
@@ -557,16 +606,22 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
           }
         }
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-          // bytes (token a, d), (token a + 1, d), (token a, d + 1), (token a + 1, d + 1)
-          const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16(__byte_perm(vw[0][j >> 1], vw[1][j >> 1], sel), a0, a1);
-          e4m3x4_to_f16(__byte_perm(vw[2][j >> 1], vw[3][j >> 1], sel), a2, a3);
+        for (int t = 0; t < N; ++t)
 #pragma unroll
-          for (int u = 0; u < NR; ++u) f8_mma(acc[u][j], a0, a1, a2, a3, pb2[u][0], pb2[u][1]);
-        }
-      }
+          for (int j = 0; j < kSteps; ++j) {
+            // bytes (token a, d), (token a + 1, d), (token a, d + 1), (token a + 1, d + 1)
+            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16(__byte_perm(vw[t][0][j >> 1], vw[t][1][j >> 1], sel), a0, a1);
+            e4m3x4_to_f16(__byte_perm(vw[t][2][j >> 1], vw[t][3][j >> 1], sel), a2, a3);
+#pragma unroll
+            for (int u = 0; u < NR; ++u) f8_mma(acc[u][j], a0, a1, a2, a3, pt2[t][u][0], pt2[t][u][1]);
+          }
+        x += N;
+      };
+      if constexpr (T::kTogether == 2)
+        while (x + 1 < x_stop) step(std::integral_constant<int, 2>{});
+      while (x < x_stop) step(std::integral_constant<int, 1>{});
 
       // ---- the end of the sequence, or of the part
       const bool whole = x_first == base && x_stop == end;
@@ -799,6 +854,7 @@ __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_
 // w_out = decay * w_in + sum over the rows of 2^(score - lse): half a warp per
 // tile and head, one lane per token; the blocks share the tiles evenly. Bound by
 // HBM: 4 bytes per row and 8 per token and head.
+template <int kAhead, int kRows>  // tiles of a half warp and rows of each whose loads are in flight together
 __global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8DecodeParams p, const FastDiv by_heads) {
   wait_prior_grid();
   const int hkv = p.c.hkv, nrows = p.group * p.q_len;
@@ -812,7 +868,6 @@ __global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8Decode
   bool bad;
   int L = f8_length(p, b, &bad);
   const int half = threadIdx.x >> 4, tk = threadIdx.x & 15;
-  constexpr int kAhead = 4;  // tiles of a half warp whose loads are in flight together
   for (int i0 = half; i0 < count; i0 += 16 * kAhead) {
     int64_t at[kAhead];  // the token's weight, -1: none
     const float *s[kAhead], *lse2[kAhead];
@@ -839,12 +894,12 @@ __global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8Decode
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) sum[k] = at[k] >= 0 && p.w_in ? p.decay * p.w_in[at[k]] : 0.f;
-    for (int r = 0; r < nrows; r += 4) {
-      float v[kAhead][4], z[kAhead][4];
+    for (int r = 0; r < nrows; r += kRows) {
+      float v[kAhead][kRows], z[kAhead][kRows];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kRows; ++e) {
           const bool in = at[k] >= 0 && r + e < nrows;
           v[k][e] = in ? s[k][(r + e) * 16] : -INFINITY;
           z[k][e] = in ? lse2[k][r + e] : 0.f;
@@ -852,7 +907,7 @@ __global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8Decode
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[k] += ptx::ex2(v[k][e] - z[k][e]);
+        for (int e = 0; e < kRows; ++e) sum[k] += ptx::ex2(v[k][e] - z[k][e]);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
@@ -909,8 +964,11 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
           ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p)
           : launch_after(fp8_decode_join_kernel<D, false>, dim3(rows + 1), dim3(128), 0, stream, p);
   if (e != cudaSuccess || !w) return e;
-  return launch_after(fp8_decode_weights_kernel, dim3(static_cast<uint32_t>(sms * 8)), dim3(256), 0, stream, p,
-                      make_fast_div(p.c.hkv));
+  const dim3 g(static_cast<uint32_t>(sms * 8)), block(256);
+  const FastDiv by_heads = make_fast_div(p.c.hkv);
+  if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p, by_heads);
+  if (nrows <= 8) return launch_after(fp8_decode_weights_kernel<2, 8>, g, block, 0, stream, p, by_heads);
+  return launch_after(fp8_decode_weights_kernel<1, 16>, g, block, 0, stream, p, by_heads);
 }
 
 cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream) {
