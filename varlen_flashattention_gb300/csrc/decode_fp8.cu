@@ -88,7 +88,7 @@ struct Fp8DecodeParams {
 };
 
 constexpr int kF8Warps = 4;
-constexpr int kF8MinTiles = 2;    // fewest tiles of a part
+constexpr int kF8MinTiles = 1;    // fewest tiles of a part (a short sequence's time grows by 0.6 us a tile)
 constexpr int kF8ScanBatch = 512; // batches up to this number their tiles in every block
 // A score may pass its reference by this much before the reference moves.
 constexpr float kF8Slack = 8.f;
@@ -115,8 +115,18 @@ struct F8Tile {
   static constexpr int kRingBytes = kF8Warps * kStages * kStageBytes;
 };
 
-__device__ __forceinline__ void f8_cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Codes are read once: they make way first in L2, for the parts' results and the
+// scores that the next kernels read (one sequence of 131k tokens 51 -> 48 us, four
+// draft tokens with weights 60 -> 54 us).
+__device__ __forceinline__ uint64_t f8_read_once() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void f8_cp_async16(uint32_t dst, const void* src, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void f8_cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -214,12 +224,14 @@ struct F8Line {
     total = tiles;
     parts = min(static_cast<int64_t>(max_parts), (total + kF8MinTiles - 1) / kF8MinTiles);
   }
-  __device__ __forceinline__ int begin(int64_t i) const { return static_cast<int>(i * total / parts); }
+  __device__ __forceinline__ int begin(int64_t i) const { return quotient(static_cast<uint64_t>(i * total), parts); }
   // the part that holds tile x: the last i with floor(i total / parts) <= x
   __device__ __forceinline__ int part_of(int64_t x) const {
-    const uint64_t n = static_cast<uint64_t>((x + 1) * parts - 1);
-    return static_cast<int>(n >> 32 ? n / static_cast<uint64_t>(total)
-                                    : static_cast<uint32_t>(n) / static_cast<uint32_t>(total));
+    return quotient(static_cast<uint64_t>((x + 1) * parts - 1), total);
+  }
+  // n / d, in 32 bits where both fit (a 64-bit division is a hundred instructions)
+  static __device__ __forceinline__ int quotient(uint64_t n, int64_t d) {
+    return static_cast<int>(n >> 32 ? n / static_cast<uint64_t>(d) : static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
   }
 };
 
@@ -262,6 +274,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
   const int64_t jobs = line.parts * hkv;
   uint8_t* ring = smem + warp * kStages * T::kStageBytes;
   const uint32_t ring_u32 = ptx::smem_u32(ring);
+  const uint64_t read_once = f8_read_once();
   bool bad_page = false;
 
   // Where this lane's copies of step u go: token tk(u), 16-byte piece cp of its row.
@@ -329,8 +342,8 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
           const int r = __shfl_sync(0xffffffffu, row, tk);
           const int64_t off = (static_cast<int64_t>(max(r, 0)) * hkv + h) * D + cp * 16;
           const uint32_t n = r >= 0 ? 16 : 0;  // missing tokens are zeros
-          f8_cp_async16(st + k_place(tk), p.c.kc + off, n);
-          f8_cp_async16(st + T::kVOff + v_place(tk), p.c.vc + off, n);
+          f8_cp_async16(st + k_place(tk), p.c.kc + off, n, read_once);
+          f8_cp_async16(st + T::kVOff + v_place(tk), p.c.vc + off, n, read_once);
         }
       }
       f8_commit();  // one group per call, empty past the last tile
@@ -673,11 +686,13 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
 //   lse = log2 sum_i 2^lse_i, O = sum_i 2^(lse_i - lse) O_i,
 // in a fixed order; a sequence without tokens gets zeros and -inf. The last block
 // gathers the main kernel's findings into the status block.
-// Two shapes. kWide = false: a block of four warps per output row, each with a
-// run of the parts (many sequences, of a dozen parts or so each). kWide = true:
-// a block per 32 columns of a row, its 32 groups of eight lanes reading a part's
-// 128-byte piece each, four ahead, so that a sequence cut into hundreds of parts
-// is joined by all SMs.
+// Two shapes. kWide = false: a warp per output row, for many sequences of a dozen
+// parts or so: the lanes hold the parts' lse, and the first eight parts' rows are
+// on their way before the lse are there. A sequence of more than 64 parts among
+// them has its rows joined by the block's four warps, one row after the other.
+// kWide = true: a block per 32 columns of a row, its 32 groups of eight lanes
+// reading a part's 128-byte piece each, four ahead, so that a sequence cut into
+// hundreds of parts is joined by all SMs.
 template <int THREADS>
 __device__ __forceinline__ void f8_report(const Fp8DecodeParams& p) {
   constexpr int kLoads = (kFp8MaxWarps / kF8Warps + THREADS) / THREADS;  // all in flight at once
@@ -695,6 +710,149 @@ __device__ __forceinline__ void f8_report(const Fp8DecodeParams& p) {
     p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8DecodeTable : 0));
 }
 
+// Where the parts of an output row lie.
+struct F8Row {
+  int count;         // parts; 0: the sequence is empty, 1: finished by its part
+  int step;          // rows from one part to the next
+  const float* lse;  // of the first part
+  const float* po;
+  int64_t out;       // row of O
+  int64_t w;         // index of the row's lse among the weights'
+  __device__ __forceinline__ F8Row(const Fp8DecodeParams& p, int job, int D) {
+    const int hkv = p.c.hkv, G = p.group, nrows = G * p.q_len;
+    const int seg = job / nrows, r = job - seg * nrows, b = seg / hkv, h = seg - b * hkv;
+    const int base = __ldcg(p.tile_base + b), end = __ldcg(p.tile_base + b + 1);
+    const F8Line line(__ldcg(p.tile_base + p.batch), p.max_parts);
+    const int i0 = end > base ? line.part_of(base) : 0;
+    count = end > base ? line.part_of(end - 1) - i0 + 1 : 0;
+    const int64_t first = ((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r;
+    step = hkv * nrows;
+    lse = p.part_lse2 + first;
+    po = p.part_o + first * D;
+    out = (static_cast<int64_t>(b) * p.q_len + r / G) * p.hq + static_cast<int64_t>(h) * G + r % G;
+    w = static_cast<int64_t>(seg) * nrows + r;
+  }
+};
+
+// The row's lse from its largest part's (0 if every part is empty or NaN) and the sum relative to it.
+__device__ __forceinline__ void f8_write_lse(const Fp8DecodeParams& p, const F8Row& row, float top, float z) {
+  const float lse2 = z == 0.f ? -INFINITY : top + log2f(z);
+  p.lse[row.out] = lse2 * 0.6931471805599453f;
+  if (p.w_out) p.lse2[row.w] = f8_weight_lse(lse2);
+}
+
+template <int D>
+__device__ __forceinline__ void join_rows(const Fp8DecodeParams& p) {
+  constexpr int kPer = D / 32, kWarps = 4;  // output columns of a lane
+  __shared__ float s_m[kWarps], s_z[kWarps], s_o[kWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = p.batch * p.c.hkv * p.group * p.q_len;
+  const int mine = static_cast<int>(blockIdx.x) * kWarps + warp;
+  auto load = [&](const F8Row& row, int i, float (&v)[kPer]) {
+    const float* src = row.po + static_cast<int64_t>(i) * row.step * D;
+    if constexpr (kPer == 4) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else {
+      const float2 a = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+      v[0] = a.x, v[1] = a.y;
+    }
+  };
+  const F8Row row(p, min(mine, rows - 1), D);
+  const bool is_long = __syncthreads_or(row.count > 64);
+  if (!is_long) {
+    if (mine >= rows || row.count == 1) return;
+    float v[8][kPer], o[kPer];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < row.count) load(row, k, v[k]);
+    float y[2];  // lane l: parts l and l + 32
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      y[k] = lane + 32 * k < row.count ? __ldcg(row.lse + static_cast<int64_t>(lane + 32 * k) * row.step) : -INFINITY;
+    float m = fmaxf(y[0], y[1]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (m == -INFINITY) m = 0.f;
+    const float f[2] = {ptx::ex2(y[0] - m), ptx::ex2(y[1] - m)};
+    float z = f[0] + f[1];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+    for (int i = 0; i < row.count; i += 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i + k >= row.count) break;
+        const float g = __shfl_sync(0xffffffffu, i < 32 ? f[0] : f[1], i + k);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] += g * v[k][e];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + 8 + k < row.count) load(row, i + 8 + k, v[k]);
+    }
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    if constexpr (kPer == 4)
+      reinterpret_cast<uint2*>(p.o + row.out * D)[lane] =
+          make_uint2(ptx::pack_bf16(o[0] * inv, o[1] * inv), ptx::pack_bf16(o[2] * inv, o[3] * inv));
+    else
+      reinterpret_cast<uint32_t*>(p.o + row.out * D)[lane] = ptx::pack_bf16(o[0] * inv, o[1] * inv);
+    if (lane == 0) f8_write_lse(p, row, m, z);
+    return;
+  }
+  for (int j = 0; j < kWarps; ++j) {
+    const int job = static_cast<int>(blockIdx.x) * kWarps + j;
+    if (job >= rows) return;
+    const F8Row r(p, job, D);
+    if (r.count == 1) continue;
+    const int lo = r.count * warp / kWarps, hi = r.count * (warp + 1) / kWarps;
+    float o[kPer], m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+    for (int i = lo + lane; i < hi; i += 32) m = fmaxf(m, __ldcg(r.lse + static_cast<int64_t>(i) * r.step));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (m == -INFINITY) m = 0.f;
+    for (int i = lo; i < hi; i += 8) {
+      float f[8], v[8][kPer];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[k] = i + k < hi ? ptx::ex2(__ldcg(r.lse + static_cast<int64_t>(i + k) * r.step) - m) : 0.f;
+        if (i + k < hi) load(r, i + k, v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i + k >= hi) break;
+        sum += f[k];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] += f[k] * v[k][e];
+      }
+    }
+    if (lane == 0) {
+      s_m[warp] = sum == 0.f ? -INFINITY : m;  // nothing in it: counts for nothing
+      s_z[warp] = sum;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+      if (top == -INFINITY) top = 0.f;
+      float z = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ptx::ex2(s_m[w] - top);
+        z += s_z[w] * f;
+        y += s_o[w][threadIdx.x] * f;
+      }
+      p.o[r.out * D + threadIdx.x] = __float2bfloat16(z == 0.f ? 0.f : y / z);
+      if (threadIdx.x == 0) f8_write_lse(p, r, top, z);
+    }
+    __syncthreads();
+  }
+}
+
 constexpr int kF8WideThreads = 256;
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_kernel(const Fp8DecodeParams p) {
@@ -704,24 +862,19 @@ __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_
     f8_report<kWide ? kF8WideThreads : 128>(p);
     return;
   }
+  if constexpr (!kWide) {
+    join_rows<D>(p);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hkv = p.c.hkv, G = p.group, nrows = G * p.q_len;
-  const int slice = kWide ? static_cast<int>(blockIdx.x % (D / 32)) : 0;
-  const int job = static_cast<int>(kWide ? blockIdx.x / (D / 32) : blockIdx.x);
-  const int seg = job / nrows, r = job % nrows, b = seg / hkv, h = seg % hkv;
-  const int base = __ldcg(p.tile_base + b), end = __ldcg(p.tile_base + b + 1);
-  const F8Line line(__ldcg(p.tile_base + p.batch), p.max_parts);
-  const int i0 = end > base ? line.part_of(base) : 0;
-  const int count = end > base ? line.part_of(end - 1) - i0 + 1 : 0;
-  if (count == 1) return;  // finished by its part
-  const int64_t first = ((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r;
-  const int step = hkv * nrows;  // rows from one part to the next
-  const float* lse = p.part_lse2 + first;
-  const float* po = p.part_o + first * D + 32 * slice;
-  const int64_t row = (static_cast<int64_t>(b) * p.q_len + r / G) * p.hq + static_cast<int64_t>(h) * G + r % G;
+  const int slice = static_cast<int>(blockIdx.x % (D / 32));
+  const F8Row row(p, static_cast<int>(blockIdx.x / (D / 32)), D);
+  const int count = row.count, step = row.step;
+  if (count == 1) return;
+  const float *lse = row.lse, *po = row.po + 32 * slice;
   float top, z;  // largest lse and sum of 2^(lse - top) (top: 0 if every part is empty or NaN)
 
-  if constexpr (kWide) {
+  {
     __shared__ float s_f[kFp8MaxWarps];
     __shared__ float s_red[2][8];
     __shared__ float s_o[8][32];
@@ -790,65 +943,9 @@ __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_
     float y = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) y += s_o[w][lane];
-    p.o[row * D + 32 * slice + lane] = __float2bfloat16(z == 0.f ? 0.f : y / z);
-  } else {
-    constexpr int kPer = D / 32, kWarps = 4;  // output columns of a lane
-    __shared__ float s_m[kWarps], s_z[kWarps], s_o[kWarps][D];
-    const int lo = count * warp / kWarps, hi = count * (warp + 1) / kWarps;
-    float o[kPer], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-    for (int i = lo + lane; i < hi; i += 32) m = fmaxf(m, __ldcg(lse + static_cast<int64_t>(i) * step));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (m == -INFINITY) m = 0.f;
-    for (int i = lo; i < hi; i += 4) {
-      float f[4], v[4][kPer];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t at = static_cast<int64_t>(min(i + k, hi - 1)) * step;
-        f[k] = i + k < hi ? ptx::ex2(__ldcg(lse + at) - m) : 0.f;
-        if constexpr (kPer == 4) {
-          const float4 a = __ldcg(reinterpret_cast<const float4*>(po + at * D) + lane);
-          v[k][0] = a.x, v[k][1] = a.y, v[k][2] = a.z, v[k][3] = a.w;
-        } else {
-          const float2 a = __ldcg(reinterpret_cast<const float2*>(po + at * D) + lane);
-          v[k][0] = a.x, v[k][1] = a.y;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (i + k >= hi) break;
-        sum += f[k];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += f[k] * v[k][e];
-      }
-    }
-    if (lane == 0) {
-      s_m[warp] = sum == 0.f ? -INFINITY : m;  // nothing in it: counts for nothing
-      s_z[warp] = sum;
-    }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = o[e];
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    if (top == -INFINITY) top = 0.f;
-    z = 0.f;
-    float y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ptx::ex2(s_m[w] - top);
-      z += s_z[w] * f;
-      y += s_o[w][threadIdx.x] * f;
-    }
-    p.o[row * D + threadIdx.x] = __float2bfloat16(z == 0.f ? 0.f : y / z);
+    p.o[row.out * D + 32 * slice + lane] = __float2bfloat16(z == 0.f ? 0.f : y / z);
   }
-  if (threadIdx.x == 0 && slice == 0) {
-    const float lse2 = z == 0.f ? -INFINITY : top + log2f(z);
-    p.lse[row] = lse2 * 0.6931471805599453f;
-    if (p.w_out) p.lse2[static_cast<int64_t>(seg) * nrows + r] = f8_weight_lse(lse2);
-  }
+  if (threadIdx.x == 0 && slice == 0) f8_write_lse(p, row, top, z);
 }
 
 // w_out = decay * w_in + sum over the rows of 2^(score - lse): half a warp per
@@ -962,9 +1059,9 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
   const uint32_t rows = static_cast<uint32_t>(p.batch) * p.c.hkv * nrows;
   e = p.max_parts > 32 * p.batch
           ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p)
-          : launch_after(fp8_decode_join_kernel<D, false>, dim3(rows + 1), dim3(128), 0, stream, p);
+          : launch_after(fp8_decode_join_kernel<D, false>, dim3((rows + 3) / 4 + 1), dim3(128), 0, stream, p);
   if (e != cudaSuccess || !w) return e;
-  const dim3 g(static_cast<uint32_t>(sms * 8)), block(256);
+  const dim3 g(static_cast<uint32_t>(sms * 4)), block(256);  // as many as fit at once
   const FastDiv by_heads = make_fast_div(p.c.hkv);
   if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p, by_heads);
   if (nrows <= 8) return launch_after(fp8_decode_weights_kernel<2, 8>, g, block, 0, stream, p, by_heads);
