@@ -74,6 +74,7 @@ struct Fp8DecodeParams {
   int32_t* tile_base;  // [B + 1] 16-token tiles of the sequences before b
   int32_t max_parts;   // most parts of the line
   int32_t grid;        // blocks of the main kernel (four warps each)
+  FastDiv by_heads;    // division by hkv
   uint8_t* errors;     // a byte for each warp of the main kernel (pages), then a 32-bit word (lengths)
   float* part_o;       // [parts + B][hkv][rows][D], normalised
   float* part_lse2;    // [parts + B][hkv][rows], log2, -inf when empty
@@ -174,10 +175,11 @@ __device__ __forceinline__ int f8_length(const Fp8DecodeParams& p, int b, bool* 
   return *bad ? 0 : L;
 }
 
-// Numbers the tiles: base[b] = sum over b' < b of ceil(L_b' / 16), b = 0 .. batch.
-// Every thread of the block takes part; true if a length was out of range.
+// Numbers the tiles: base[b] = sum over b' < b of ceil(L_b' / 16), b = 0 .. batch;
+// len, if given, receives the lengths. Every thread of the block takes part; true
+// if a length was out of range.
 template <int THREADS>
-__device__ __forceinline__ bool f8_number_tiles(const Fp8DecodeParams& p, int32_t* base) {
+__device__ __forceinline__ bool f8_number_tiles(const Fp8DecodeParams& p, int32_t* base, int32_t* len = nullptr) {
   __shared__ int32_t warp_sum[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) base[0] = 0;
@@ -187,7 +189,9 @@ __device__ __forceinline__ bool f8_number_tiles(const Fp8DecodeParams& p, int32_
     int x = 0;
     if (b0 + tid < p.batch) {
       bool bad;
-      x = (f8_length(p, b0 + tid, &bad) + 15) >> 4;
+      const int L = f8_length(p, b0 + tid, &bad);
+      if (len) len[b0 + tid] = L;
+      x = (L + 15) >> 4;
       any |= bad;
     }
 #pragma unroll
@@ -253,11 +257,11 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
   constexpr int kEpl = D / 8;     // head dimensions a lane holds of each of its query rows
   constexpr int kStages = T::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int32_t s_base[kF8ScanBatch + 1];
+  __shared__ int32_t s_base[kF8ScanBatch + 1], s_len[kF8ScanBatch];
 
   const int32_t* tile_base = p.tile_base;
   if (p.batch <= kF8ScanBatch) {
-    const bool bad = f8_number_tiles<128>(p, s_base);
+    const bool bad = f8_number_tiles<128>(p, s_base, s_len);
     if (blockIdx.x == 0) {
       for (int i = threadIdx.x; i <= p.batch; i += 128) p.tile_base[i] = s_base[i];
       if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.errors)[p.grid] = bad;
@@ -271,7 +275,11 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
   const int gq = lane >> 2, qq = lane & 3;
   const int hkv = p.c.hkv, G = p.group, QL = p.q_len, nrows = G * QL;
   const F8Line line(tile_base[p.batch], p.max_parts);
-  const int64_t jobs = line.parts * hkv;
+  const int jobs = static_cast<int>(line.parts) * hkv;  // at most the larger of the warps and hkv
+  auto length = [&](int b) -> int {
+    bool bad;
+    return p.batch <= kF8ScanBatch ? s_len[b] : f8_length(p, b, &bad);
+  };
   uint8_t* ring = smem + warp * kStages * T::kStageBytes;
   const uint32_t ring_u32 = ptx::smem_u32(ring);
   const uint64_t read_once = f8_read_once();
@@ -290,9 +298,8 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     return (tk >> 1) * 128 + (((((tk & 1) << 2) | cp) ^ (tk & 6)) << 4);
   };
 
-  for (int64_t job = static_cast<int64_t>(blockIdx.x) * kF8Warps + warp; job < jobs;
-       job += static_cast<int64_t>(gridDim.x) * kF8Warps) {
-    const int part = static_cast<int>(job / hkv), h = static_cast<int>(job % hkv);
+  for (int job = blockIdx.x * kF8Warps + warp; job < jobs; job += gridDim.x * kF8Warps) {
+    const int part = fast_div(job, p.by_heads), h = job - part * hkv;
     const int x0 = line.begin(part), x1 = line.begin(part + 1);
     int b = f8_find_sequence(tile_base, p.batch, x0);
 
@@ -301,8 +308,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     const int32_t* ppt = nullptr;
     int page = 0, slot = -1;  // of this lane's token (lane % 16) of the tile to copy next
     auto enter = [&]() {
-      bool bad;
-      pL = f8_length(p, pb, &bad);
+      pL = length(pb);
       pbase = tile_base[pb];
       pend = tile_base[pb + 1];
       ppt = p.page_table + static_cast<int64_t>(pb) * p.max_pages;
@@ -358,8 +364,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     for (int x = x0; x < x1;) {
       // ---- the sequence b, from tile t_lo on
       while (tile_base[b + 1] <= x) ++b;
-      bool bad;
-      const int L = f8_length(p, b, &bad);
+      const int L = length(b);
       const int base = tile_base[b], end = tile_base[b + 1];
       const int x_first = x, x_stop = min(end, x1);
 
@@ -952,7 +957,7 @@ __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_
 // tile and head, one lane per token; the blocks share the tiles evenly. Bound by
 // HBM: 4 bytes per row and 8 per token and head.
 template <int kAhead, int kRows>  // tiles of a half warp and rows of each whose loads are in flight together
-__global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8DecodeParams p, const FastDiv by_heads) {
+__global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8DecodeParams p) {
   wait_prior_grid();
   const int hkv = p.c.hkv, nrows = p.group * p.q_len;
   const int64_t total = static_cast<int64_t>(p.tile_base[p.batch]) * hkv;  // (tile, head) pairs
@@ -974,7 +979,7 @@ __global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8Decode
       const int i = i0 + 16 * k;
       at[k] = -1;
       if (i >= count) continue;
-      const int q = fast_div(h0 + i, by_heads), x = x0 + q, h = h0 + i - q * hkv;
+      const int q = fast_div(h0 + i, p.by_heads), x = x0 + q, h = h0 + i - q * hkv;
       if (x >= next) {
         do ++b;
         while (p.tile_base[b + 1] <= x);
@@ -1041,6 +1046,7 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
   const int grid = static_cast<int>(
       std::min<int64_t>(warps / kF8Warps, (static_cast<int64_t>(p.max_parts) * p.c.hkv + kF8Warps - 1) / kF8Warps));
   p.grid = grid;
+  p.by_heads = make_fast_div(p.c.hkv);
   cudaError_t e;
   if (p.batch > kF8ScanBatch) {
     fp8_decode_plan_kernel<<<1, 1024, 0, stream>>>(p);
@@ -1062,10 +1068,9 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
           : launch_after(fp8_decode_join_kernel<D, false>, dim3((rows + 3) / 4 + 1), dim3(128), 0, stream, p);
   if (e != cudaSuccess || !w) return e;
   const dim3 g(static_cast<uint32_t>(sms * 4)), block(256);  // as many as fit at once
-  const FastDiv by_heads = make_fast_div(p.c.hkv);
-  if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p, by_heads);
-  if (nrows <= 8) return launch_after(fp8_decode_weights_kernel<2, 8>, g, block, 0, stream, p, by_heads);
-  return launch_after(fp8_decode_weights_kernel<1, 16>, g, block, 0, stream, p, by_heads);
+  if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p);
+  if (nrows <= 8) return launch_after(fp8_decode_weights_kernel<2, 8>, g, block, 0, stream, p);
+  return launch_after(fp8_decode_weights_kernel<1, 16>, g, block, 0, stream, p);
 }
 
 cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream) {
