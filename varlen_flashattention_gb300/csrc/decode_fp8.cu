@@ -953,67 +953,57 @@ __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_
   if (threadIdx.x == 0 && slice == 0) f8_write_lse(p, row, top, z);
 }
 
-// w_out = decay * w_in + sum over the rows of 2^(score - lse): half a warp per
-// tile and head, one lane per token; the blocks share the tiles evenly. Bound by
-// HBM: 4 bytes per row and 8 per token and head.
-template <int kAhead, int kRows>  // tiles of a half warp and rows of each whose loads are in flight together
-__global__ void __launch_bounds__(256) fp8_decode_weights_kernel(const Fp8DecodeParams p) {
+// w_out = decay * w_in + sum over the rows of 2^(score - lse). Like the main kernel a
+// warp takes a part of the line of tiles for one head: a lane per token, two tiles
+// at a time, the rows' lse in registers, kAhead pairs of tiles and kRows rows
+// (16 loads a lane) in flight. Bound by HBM: 4 bytes per row and 8 per token and head.
+constexpr int kF8WeightWarps = 8;
+template <int kAhead, int kRows>
+__global__ void __launch_bounds__(32 * kF8WeightWarps) fp8_decode_weights_kernel(const Fp8DecodeParams p, int max_parts) {
   wait_prior_grid();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hkv = p.c.hkv, nrows = p.group * p.q_len;
-  const int64_t total = static_cast<int64_t>(p.tile_base[p.batch]) * hkv;  // (tile, head) pairs
-  const int64_t y0 = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
-  const int count = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x - y0);
-  if (count <= 0) return;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  const int x0 = static_cast<int>(y0 / hkv), h0 = static_cast<int>(y0 % hkv);
-  int b = f8_find_sequence(p.tile_base, p.batch, x0), first = p.tile_base[b], next = p.tile_base[b + 1];
-  bool bad;
-  int L = f8_length(p, b, &bad);
-  const int half = threadIdx.x >> 4, tk = threadIdx.x & 15;
-  for (int i0 = half; i0 < count; i0 += 16 * kAhead) {
-    int64_t at[kAhead];  // the token's weight, -1: none
-    const float *s[kAhead], *lse2[kAhead];
-    float sum[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + 16 * k;
-      at[k] = -1;
-      if (i >= count) continue;
-      const int q = fast_div(h0 + i, p.by_heads), x = x0 + q, h = h0 + i - q * hkv;
-      if (x >= next) {
-        do ++b;
-        while (p.tile_base[b + 1] <= x);
-        first = p.tile_base[b];
-        next = p.tile_base[b + 1];
-        L = f8_length(p, b, &bad);
-      }
-      const int t = (x - first) * 16 + tk;
-      if (t >= L) continue;
+  const F8Line line(p.tile_base[p.batch], max_parts);
+  const int jobs = static_cast<int>(line.parts) * hkv;
+  const int64_t pair = static_cast<int64_t>(hkv) * nrows * 32;  // scores from one pair of tiles to the next
+  for (int job = blockIdx.x * kF8WeightWarps + warp; job < jobs; job += gridDim.x * kF8WeightWarps) {
+    const int part = fast_div(job, p.by_heads), h = job - part * hkv;
+    int x = line.begin(part);
+    const int x1 = line.begin(part + 1);
+    int b = f8_find_sequence(p.tile_base, p.batch, x);
+    while (x < x1) {
+      while (p.tile_base[b + 1] <= x) ++b;
+      bool bad;
+      const int base = p.tile_base[b], stop = min(p.tile_base[b + 1], x1);
+      const int end = min(f8_length(p, b, &bad), (stop - base) * 16);  // tokens of this part of the sequence
       const int64_t seg = static_cast<int64_t>(b) * hkv + h;
-      at[k] = seg * cap + t;
-      s[k] = p.scores + (y0 + i) * nrows * 16 + tk;
-      lse2[k] = p.lse2 + seg * nrows;
-    }
+      float z[kRows];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) sum[k] = at[k] >= 0 && p.w_in ? p.decay * p.w_in[at[k]] : 0.f;
-    for (int r = 0; r < nrows; r += kRows) {
-      float v[kAhead][kRows], z[kAhead][kRows];
+      for (int r = 0; r < kRows; ++r) z[r] = r < nrows ? p.lse2[seg * nrows + r] : INFINITY;
+      int t = (x - base) * 16 + lane;
+      const float* s = p.scores + ((static_cast<int64_t>(x) + (lane >> 4)) * hkv + h) * nrows * 16 + (lane & 15);
+      const float* in = p.w_in ? p.w_in + seg * cap : nullptr;
+      float* out = p.w_out + seg * cap;
+      for (; t - lane < end; t += 32 * kAhead, s += kAhead * pair) {
+        float v[kAhead][kRows], sum[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
+        for (int k = 0; k < kAhead; ++k) {
+          const bool have = t + 32 * k < end;
+          sum[k] = have && in ? in[t + 32 * k] : 0.f;
 #pragma unroll
-        for (int e = 0; e < kRows; ++e) {
-          const bool in = at[k] >= 0 && r + e < nrows;
-          v[k][e] = in ? s[k][(r + e) * 16] : -INFINITY;
-          z[k][e] = in ? lse2[k][r + e] : 0.f;
+          for (int r = 0; r < kRows; ++r) v[k][r] = have && r < nrows ? s[k * pair + r * 16] : -INFINITY;
         }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
+        for (int k = 0; k < kAhead; ++k) {
+          sum[k] *= p.decay;
 #pragma unroll
-        for (int e = 0; e < kRows; ++e) sum[k] += ptx::ex2(v[k][e] - z[k][e]);
+          for (int r = 0; r < kRows; ++r) sum[k] += ptx::ex2(v[k][r] - z[r]);
+          if (t + 32 * k < end) out[t + 32 * k] = sum[k];
+        }
+      }
+      x = stop;
     }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (at[k] >= 0) p.w_out[at[k]] = sum[k];
   }
 }
 
@@ -1067,10 +1057,12 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
           ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p)
           : launch_after(fp8_decode_join_kernel<D, false>, dim3((rows + 3) / 4 + 1), dim3(128), 0, stream, p);
   if (e != cudaSuccess || !w) return e;
-  const dim3 g(static_cast<uint32_t>(sms * 4)), block(256);  // as many as fit at once
-  if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p);
-  if (nrows <= 8) return launch_after(fp8_decode_weights_kernel<2, 8>, g, block, 0, stream, p);
-  return launch_after(fp8_decode_weights_kernel<1, 16>, g, block, 0, stream, p);
+  const int blocks = sms * 4;  // as many as fit at once
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks * kF8WeightWarps / p.c.hkv, tiles)));
+  const dim3 g(blocks), block(32 * kF8WeightWarps);
+  if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p, parts);
+  if (nrows <= 8) return launch_after(fp8_decode_weights_kernel<2, 8>, g, block, 0, stream, p, parts);
+  return launch_after(fp8_decode_weights_kernel<1, 16>, g, block, 0, stream, p, parts);
 }
 
 cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffers& w, int sms, cudaStream_t stream) {
@@ -1103,7 +1095,7 @@ cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffe
   p.scores = w.scores;
   p.w_in = a.weights;
   p.w_out = a.weights_out;
-  p.decay = a.decay;
+  p.decay = a.weights ? a.decay : 0.f;
   p.status = w.status;
   return a.head_dim == 128 ? launch_dim<128>(p, a.main_kernel_events, sms, stream)
                            : launch_dim<64>(p, a.main_kernel_events, sms, stream);
