@@ -183,7 +183,7 @@ def test_decode_arguments_are_refused(lib):
 
 
 def test_append_and_evict_arguments_are_refused(lib):
-    for bad in (dict(total_new=-1), dict(max_new=-1), dict(new_offsets=None), dict(k=FAKE + 8), dict(v=None),
+    for bad in (dict(total_new=-1), dict(max_new=-1), dict(batch=0), dict(new_offsets=None), dict(k=FAKE + 8), dict(v=None),
                 dict(weights=FAKE + 2), dict(batch=1 << 25, max_new=1 << 20)):
         assert lib.jfa_cache_append_fp8(ctypes.byref(_append_args(**bad)), FAKE, 1 << 40, None) == \
             _abi.JFA_ERR_INVALID_ARG, bad
@@ -212,6 +212,9 @@ CACHE_ERRORS = [
     (dict(v_scale=torch.ones(10, 1, 2)), ValueError, "v_scale must have shape"),
     (dict(page_table=torch.zeros(2, 4, dtype=i32)), ValueError, "page_table must have shape"),
     (dict(seqlens_k=torch.ones(3, dtype=torch.int64)), TypeError, "seqlens_k must be"),
+    (dict(page_table=torch.zeros(4, 3, dtype=i32).t()), ValueError, "page_table must be contiguous"),
+    (dict(v_cache=torch.zeros(10, 2, 16, 64, dtype=u8).transpose(1, 2)), ValueError, "v_cache must be contiguous"),
+    (dict(k_scale=None), TypeError, "k_scale must be a torch.Tensor"),
 ]
 
 

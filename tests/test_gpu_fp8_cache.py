@@ -16,7 +16,8 @@ are derived per output row from the arithmetic, with u = 2^-24:
     relative down to fp16's smallest normal number; below it is 2^-25 absolute. A
     weight is held as w_j = P_j vs_j / r with r at most 2^-7 of the largest P_j vs_j
     (vs: the scale of the value's block), so a key adds at most 2^-25 * 448 * r <=
-    2^-32 * 448 * max_j P_j vs_j more, and all L keys L times that;
+    2^-32 * 448 * max_j P_j vs_j more, and all L keys L times that. bf16's own half
+    step is likewise 2^-134 absolute below its smallest normal number 2^-126;
   * a token's weight, in fp32: (2 |ds| + 2^-20) of itself.
 """
 import numpy as np
@@ -84,7 +85,7 @@ def check_decode(c, q, o, lse, scale, w_in=None, w_out=None, w_was=None, decay=1
     ds = (c["d"] + 8) * 2.0 ** -23 * A + 2.0 ** -20
     o, lse = np64(o), np64(lse)
     bound = (2.0 ** -11 + 2.0 ** -13 + 2 * ds)[..., None] * absO + 2.0 ** -8 * np.abs(O) + \
-        (448 * 2.0 ** -32 * top)[..., None]
+        (448 * 2.0 ** -32 * top)[..., None] + 2.0 ** -134
     assert (np.isnan(o) == np.isnan(O)).all(), what
     bad = ~(np.abs(o - O) <= bound) & ~np.isnan(O)
     assert not bad.any(), f"{what}: O off by {np.nanmax(np.abs(o - O) - bound):.3e} over its bound at {np.argwhere(bad)[:3]}"
@@ -147,6 +148,53 @@ def test_decode_cut_and_joined(lens):
             assert torch.allclose(w[b].double().sum(-1), torch.full((2,), 4.0, device="cuda").double(), atol=1e-4)
 
 
+@pytest.mark.parametrize("B", [31, 513, 700])
+def test_decode_many_sequences(B):
+    """Past 512 sequences one kernel numbers the tiles for all blocks of the next."""
+    lens = [int(x) for x in np.random.default_rng(20).integers(0, 60, B)]
+    c = _case(20, lens, 1, 64, 16, 16)
+    g = _gpu(c)
+    q = _bf16(c["rng"], B, 2, 4, 64)
+    w = torch.zeros(B, 1, c["cap"]).cuda()
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), weights_out=w, check=True)
+    check_decode(c, q, o, lse, 64 ** -0.5, None, w, np.zeros(w.shape, dtype=np.float32), what=f"B={B}")
+    g["lens"][B - 1] = -1
+    with pytest.raises(jfa.JfaError, match="inconsistent device input"):
+        jfa.jfa_decode_fp8(q.cuda(), *_cache(g), check=True)
+
+
+@pytest.mark.parametrize("H,lens", [(40, [700, 3]), (2700, [20, 0, 35])])
+def test_decode_many_heads(H, lens):
+    """More heads than a part's warps, and than all warps."""
+    c = _case(21, lens, H, 64, 16, 16)
+    g = _gpu(c)
+    q = _bf16(c["rng"], len(lens), 1, H, 64)
+    w = torch.zeros(len(lens), H, c["cap"]).cuda()
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), weights_out=w, check=True)
+    check_decode(c, q, o, lse, 0.125, None, w, np.zeros(w.shape, dtype=np.float32), what=f"H={H}")
+
+
+def test_decode_one_long_among_short():
+    """One sequence cut into more than 64 parts in a batch whose rows a warp each joins."""
+    lens = [30000] + [20] * 19
+    c = _case(22, lens, 1, 64, 16, 16)
+    g = _gpu(c)
+    q = _bf16(c["rng"], len(lens), 1, 5, 64)
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), check=True)
+    check_decode(c, q, o, lse, 0.125, what="one long")
+
+
+def test_decode_shared_pages():
+    """Sequences that share a prefix's pages, and a sequence that holds a page twice."""
+    c = _case(23, [64, 64, 100], 2, 64, 16, 8)
+    c["table"][1, :3] = c["table"][0, :3]
+    c["table"][2, 4] = c["table"][2, 1]
+    g = _gpu(c)
+    q = _bf16(c["rng"], 3, 2, 6, 64)
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), check=True)
+    check_decode(c, q, o, lse, 0.125, what="shared")
+
+
 def test_decode_scales_of_every_size():
     """Blocks of very different magnitude, blocks of zeros, and scales that are no powers of two."""
     c = _case(3, [500, 64, 1000], 2, 128, 16, 16)
@@ -164,6 +212,29 @@ def test_decode_scales_of_every_size():
     g = _gpu(c)
     o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), scale=0.2, check=True)
     check_decode(c, q, o, lse, 0.2, what="scales")
+
+
+def test_decode_of_the_smallest_values():
+    """Values near fp32's smallest normal number keep their size (fp32 outputs of the parts, bf16 O)."""
+    c = _case(26, [33, 4000], 1, 128, 16, 16)
+    c["vs"][:] = 2.0 ** -126
+    c["vs"][c["table"][1, 100]] = 2.0 ** -120
+    g = _gpu(c)
+    q = _bf16(c["rng"], 2, 1, 4, 128)
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), check=True)
+    check_decode(c, q, o, lse, 128 ** -0.5, what="small")
+    assert (o != 0).float().mean() > 0.99
+
+
+def test_decode_records_events_around_its_main_kernel():
+    c = _case(27, [3000], 2, 64, 16, 16)
+    g = _gpu(c)
+    q = _bf16(c["rng"], 1, 1, 8, 64).cuda()
+    ev = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+    o, lse = jfa.jfa_decode_fp8(q, *_cache(g), events=ev, check=True)
+    assert 0 < ev[0].elapsed_time(ev[1]) < 1000
+    o2, lse2 = jfa.jfa_decode_fp8(q, *_cache(g), check=True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_decode_few_keys_dominate():
@@ -261,6 +332,25 @@ def test_append(d, P, block, old, new):
     assert (gw.cpu().numpy() == w).all()
 
 
+@pytest.mark.parametrize("B,new_hi", [(200, 3), (150, 400), (40, 700)])
+def test_append_many_sequences(B, new_hi):
+    """Blocks with a fixed chunk each (batches past 128), and blocks that look theirs up."""
+    rng = np.random.default_rng(24)
+    old, new = rng.integers(0, 40, B), rng.integers(0, new_hi + 1, B)
+    new[3] = new_hi
+    lens = [int(a + b) for a, b in zip(old, new)]
+    c = _case(24, lens, 1, 64, 16, 8)
+    n = int(new.sum())
+    k, v = _bf16(rng, n, 1, 64), _bf16(rng, n, 1, 64)
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    g = _gpu(c)
+    jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.from_numpy(offs).cuda(), new_hi, check=True)
+    kvo.append(np64(k), np64(v), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, offs)
+    for x in ("kc", "vc"):
+        assert _same_codes(g[x].cpu().numpy(), c[x]), x
+    assert (g["ks"].cpu().numpy() == c["ks"]).all() and (g["vs"].cpu().numpy() == c["vs"]).all()
+
+
 def test_append_extreme_values():
     """Subnormal and largest bf16 values, and a caller's scale that is no power of two."""
     x = torch.tensor([2.0 ** -133, -2.0 ** -126, 3.3895e38, 448.0, 449.0, 1.0, -0.0, 2.0 ** -140]).to(torch.bfloat16)
@@ -316,15 +406,18 @@ def test_evict(d, P, block, keep, first, recent):
         assert _same_codes(g[x].cpu().numpy(), c[x]), x
 
 
-@pytest.mark.parametrize("L,keep", [(70001, 5000), (33333, 33000), (131072, 1)])
-def test_evict_long(L, keep):
-    """Selection over a long sequence (positions and weights; the rows move as above)."""
+@pytest.mark.parametrize("L,keep", [(70001, 5000), (33333, 33000), (131072, 1), (5000, 77), (9001, 4000),
+                                    (20000, 3), (200003, 40001), (140000, 139999)])
+@pytest.mark.parametrize("ties", [2, 9])
+def test_evict_long(L, keep, ties):
+    """Selection over a long sequence (positions and weights; the rows move as above): every number of
+    blocks and keys a thread, with ties at the border and without."""
     rng = np.random.default_rng(10)
     pages, P = -(-L // 128), 128
     fresh = -(-keep // P)
     kc = torch.zeros(pages + fresh, P, 1, 64, dtype=torch.uint8, device="cuda")
     ks = torch.ones(pages + fresh, 1, 1, device="cuda")
-    w = np.round(np.abs(rng.standard_cauchy((1, 1, pages * P))), 2).astype(np.float32)  # many ties
+    w = np.round(np.abs(rng.standard_cauchy((1, 1, pages * P))), ties).astype(np.float32)
     table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
     new = torch.arange(pages, pages + fresh, dtype=torch.int32, device="cuda")[None]
     kept, nl, nw = jfa.jfa_cache_evict_fp8(kc, kc.clone(), ks, ks.clone(), table, torch.tensor([L], dtype=torch.int32,
@@ -332,6 +425,36 @@ def test_evict_long(L, keep):
     expect = np.sort(np.lexsort((np.arange(L), -w[0, 0, :L]))[:keep])
     assert (kept[0, 0].cpu().numpy() == expect).all() and int(nl[0]) == keep
     assert (nw[0, 0, :keep].cpu().numpy() == w[0, 0, expect]).all()
+
+
+def test_evict_many_sequences_and_pages():
+    """A warp checks a sequence past 15 of them; more pages than a bitmap holds are looked at in runs."""
+    rng = np.random.default_rng(25)
+    B, L, keep, pages = 20, 300, 50, 600_000
+    table = rng.permutation(pages).astype(np.int32)[:B * (L + keep)].reshape(B, L + keep)
+    src, new = np.ascontiguousarray(table[:, :L]), np.ascontiguousarray(table[:, L:])
+    kc = torch.zeros(pages, 1, 1, 64, dtype=torch.uint8, device="cuda")
+    ks = torch.ones(pages, 1, 1, device="cuda")
+    codes = rng.integers(0, 127, (B, L, 64)).astype(np.uint8)
+    kc[torch.from_numpy(src.ravel()).cuda().long(), 0, 0] = torch.from_numpy(codes.reshape(-1, 64)).cuda()
+    w = rng.random((B, 1, L)).astype(np.float32)
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+
+    def call(table, fresh):
+        return jfa.jfa_cache_evict_fp8(kc, kc, ks, ks, torch.from_numpy(table).cuda(), lens, torch.from_numpy(w).cuda(),
+                                       keep, torch.from_numpy(fresh).cuda(), check=True)
+    kept = call(src, new)[0].cpu().numpy()[:, 0]
+    got = kc[torch.from_numpy(new.ravel()).cuda().long(), 0, 0].cpu().numpy().reshape(B, keep, 64)
+    scale = ks[torch.from_numpy(new.ravel()).cuda().long(), 0, 0].cpu().numpy().reshape(B, keep, 1)
+    for b in range(B):
+        expect = np.sort(np.lexsort((np.arange(L), -w[b, 0]))[:keep])
+        assert (kept[b] == expect).all()
+        assert (kvo.e4m3_decode(got[b]) * scale[b] == kvo.e4m3_decode(codes[b, expect])).all()
+    for bad in (int(src[19, 299]), int(new[0, 0]), pages, -1):  # still held, given out twice, no page
+        wrong = new.copy()
+        wrong[17, 49] = bad
+        with pytest.raises(jfa.JfaError, match="inconsistent device input"):
+            call(src, wrong)
 
 
 # ------------------------------------------------------------------ wrong device data
@@ -530,6 +653,12 @@ def test_cache_on_side_streams():
         torch.cuda.synchronize()
     for (c, _, q, _, _), (o, lse) in zip(runs, got):
         check_decode(c, q, o, lse, 128 ** -0.5, what="streams")
+    # results and workspace of the binding's own, on a stream that is not the current one
+    c, g, q, qg, _ = runs[0]
+    streams[1].wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        o, lse = jfa.jfa_decode_fp8(qg, *_cache(g), stream=streams[1], check=True)
+    check_decode(c, q, o, lse, 128 ** -0.5, what="own results")
 
 
 def test_float8_tensors_and_empty_batches():

@@ -643,6 +643,9 @@ def jfa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k,
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     o = torch.empty_like(q) if o is None else o
     lse = k_scale.new_empty((B, ql, Hq)) if lse is None else lse
+    if stream is not None:  # new memory belongs to the current stream
+        o.record_stream(stream)
+        lse.record_stream(stream)
     a = _abi.DecodeFp8Args(_ptr(q), _ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
                            _ptr(seqlens_k), B, ql, Hq, Hkv, d, P, block, num_pages, mp, scale, _ptr(o), _ptr(lse),
                            _ptr(weights), _ptr(weights_out), float(decay), None)
@@ -683,6 +686,9 @@ def jfa_cache_evict_fp8(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_
     kept = page_table.new_empty((B, Hkv, keep)) if kept is None else kept
     new_seqlens = torch.empty_like(seqlens_k) if new_seqlens is None else new_seqlens
     new_weights = weights.new_empty((B, Hkv, nmp * P)) if new_weights is None else new_weights
+    if stream is not None:  # new memory belongs to the current stream
+        for t in (kept, new_seqlens, new_weights):
+            t.record_stream(stream)
     a = _abi.CacheEvictFp8Args(_ptr(kc), _ptr(vc), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(seqlens_k),
                                _ptr(weights), _ptr(new_page_table), B, Hkv, d, P, block, num_pages, mp, nmp, keep,
                                first, recent, _ptr(kept), _ptr(new_seqlens), _ptr(new_weights))

@@ -1008,7 +1008,7 @@ jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* a, void* ws, si
                                         a->batch, a->kv_heads, a->head_dim, a->page_size, a->block_size, a->num_pages,
                                         a->max_pages);
   if (st != JFA_OK) return st;
-  if (a->total_new < 0 || a->max_new < 0) return JFA_ERR_INVALID_ARG;
+  if (a->total_new < 0 || a->max_new < 0 || (a->batch == 0 && a->total_new > 0)) return JFA_ERR_INVALID_ARG;
   if (a->batch > 0 && !aligned(a->new_offsets, 4)) return JFA_ERR_INVALID_ARG;
   if (a->batch > 0 && a->total_new > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return JFA_ERR_INVALID_ARG;
   if (a->weights && !aligned(a->weights, 4)) return JFA_ERR_INVALID_ARG;

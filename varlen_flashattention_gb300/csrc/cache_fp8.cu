@@ -373,7 +373,7 @@ struct Fp8EvictParams {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMostBitmapWords = 16384;  // two bitmaps of 64 KB: pages are looked at in runs of 524,288
+constexpr int kMostBitmapWords = 8192;  // two bitmaps of 32 KB (two blocks still fit an SM): runs of 262,144 pages
 
 // Order of the weights as unsigned numbers; NaN counts as -infinity, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {

@@ -653,7 +653,13 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
           const int r = 8 * u + 2 * qq + e;
           if (r >= nrows) continue;
           // a row that saw no token: zeros and -inf (NaN stays NaN)
-          const float f = sum == 0.f ? 0.f : ptx::ex2(n[u][e] - m[u][e]) / sum;
+          // 2^(n - m) / sum in two factors: with values of 2^-126 the whole would leave fp32's range
+          const float half = ptx::ex2(0.5f * (n[u][e] - m[u][e])), f = sum == 0.f ? 0.f : half / sum;
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) {
+            acc[u][j][e] *= half;
+            acc[u][j][2 + e] *= half;
+          }
           const float z = sum == 0.f ? -INFINITY : m[u][e] + log2f(sum);
           if (whole) {
             const int64_t row = (static_cast<int64_t>(b) * QL + r / G) * p.hq + static_cast<int64_t>(h) * G + r % G;
