@@ -377,11 +377,23 @@ def test_append_extreme_values():
 @pytest.mark.parametrize("d,P,block", [(128, 16, 16), (64, 16, 8), (128, 1, 1), (64, 24, 8), (128, 128, 128)])
 @pytest.mark.parametrize("keep,first,recent", [(40, 4, 8), (1, 0, 0), (130, 0, 130), (257, 100, 0), (2000, 3, 3)])
 def test_evict(d, P, block, keep, first, recent):
-    lens = [0, 1, 40, 41, 500, 1300]
+    _evict_case([0, 1, 40, 41, 500, 1300], 2, d, P, block, keep, first, recent)
+
+
+@pytest.mark.parametrize("lens,H,d,P,block,keep", [
+    ([0, 1, 40, 41, 500, 1300] + [90] * 34, 8, 128, 16, 16, 100),
+    ([0, 30, 60, 61, 700, 9000] + [200] * 20, 8, 64, 24, 8, 61),
+])
+def test_evict_fills_the_card(lens, H, d, P, block, keep):
+    """More (sequence, head) pairs than the card's SMs hold blocks for."""
+    _evict_case(lens, H, d, P, block, keep, 2, 5)
+
+
+def _evict_case(lens, H, d, P, block, keep, first, recent):
     width = -(-keep // P)
-    c = _case(9, lens, 2, d, P, block, spare=width * len(lens) + 1)
+    c = _case(9, lens, H, d, P, block, spare=width * len(lens) + 1)
     rng = c["rng"]
-    w = np.exp(2 * rng.standard_normal((len(lens), 2, c["cap"]))).astype(np.float32)
+    w = np.exp(2 * rng.standard_normal((len(lens), H, c["cap"]))).astype(np.float32)
     w[rng.random(w.shape) < 0.3] = 0
     w[4, 0] = 1.0            # all equal: the lowest positions stay
     w[5, 1, 7:900:3] = np.nan
@@ -425,6 +437,32 @@ def test_evict_long(L, keep, ties):
     expect = np.sort(np.lexsort((np.arange(L), -w[0, 0, :L]))[:keep])
     assert (kept[0, 0].cpu().numpy() == expect).all() and int(nl[0]) == keep
     assert (nw[0, 0, :keep].cpu().numpy() == w[0, 0, expect]).all()
+
+
+def test_evict_long_with_many_heads():
+    """40 heads of one long sequence, eight blocks each, and the rows they keep."""
+    L, keep, H = 70000, 1000, 40
+    rng = np.random.default_rng(28)
+    pages, fresh = -(-L // 128), -(-keep // 128)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc = torch.randint(0, 127, (pages + fresh, 128, H, 64), generator=g, device="cuda", dtype=torch.uint8)
+    vc = torch.randint(0, 127, (pages + fresh, 128, H, 64), generator=g, device="cuda", dtype=torch.uint8)
+    ks, vs = torch.ones(pages + fresh, 2, H, device="cuda"), torch.ones(pages + fresh, 2, H, device="cuda")
+    w = rng.random((1, H, pages * 128)).astype(np.float32)
+    table = torch.arange(pages + fresh, dtype=torch.int32, device="cuda")[None]
+    kept, _, nw = jfa.jfa_cache_evict_fp8(kc, vc, ks, vs, table[:, :pages].contiguous(),
+                                          torch.tensor([L], dtype=torch.int32, device="cuda"),
+                                          torch.from_numpy(w).cuda(), keep, table[:, pages:].contiguous(), check=True)
+    for h in range(H):
+        expect = np.sort(np.lexsort((np.arange(L), -w[0, h, :L]))[:keep])
+        assert (kept[0, h].cpu().numpy() == expect).all()
+        assert (nw[0, h, :keep].cpu().numpy() == w[0, h, expect]).all()
+        at = torch.from_numpy(expect).cuda()
+        for c, sc in ((kc, ks), (vc, vs)):
+            old = c.flatten(0, 1)[at, h].view(torch.float8_e4m3fn).float()
+            new = c[pages:].flatten(0, 1)[:keep, h].view(torch.float8_e4m3fn).float()
+            scale = sc[pages:].flatten(0, 1)[:, h].repeat_interleave(64)[:keep, None]
+            assert torch.equal(old, new * scale)  # the new scale is at most 1: nothing is rounded
 
 
 def test_evict_many_sequences_and_pages():
