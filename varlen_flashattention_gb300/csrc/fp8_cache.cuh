@@ -85,8 +85,4 @@ __device__ __forceinline__ bool e4m3_any_nan(uint32_t codes) {
   return (((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
 }
 
-__device__ __forceinline__ void flag_bad_cache(int32_t* status, int32_t code) {
-  if (atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT) == JFA_OK) status[1] = code;
-}
-
 }  // namespace jfa
