@@ -407,8 +407,9 @@ typedef struct {
  *   weights_out[b][g][t] = decay * weights[b][g][t] + sum of P over the group's
  *   query heads and the q_len query tokens
  * (the first term is left out if weights is NULL); entries past L_b are not
- * written. weights and weights_out may be the same array. Codes that are NaN
- * make NaN of the rows that see them, and of no others. */
+ * written. weights and weights_out may be the same array. The workspace then
+ * holds a score of 4 bytes per query row and slot of the page table. Codes that are
+ * NaN make NaN of the rows that see them, and of no others. */
 typedef struct {
   const void* q;              /* bf16 [batch, q_len, q_heads, head_dim] */
   const void* k_cache;        /* e4m3 [num_pages, page_size, kv_heads, head_dim] */
