@@ -698,8 +698,9 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
 // in a fixed order; a sequence without tokens gets zeros and -inf. The last block
 // gathers the main kernel's findings into the status block.
 // Two shapes. kWide = false: a warp per output row, for many sequences of a dozen
-// parts or so: the lanes hold the parts' lse, and the first eight parts' rows are
-// on their way before the lse are there. A sequence of more than 64 parts among
+// parts or so: the lanes hold the parts' lse, and the first sixteen parts' rows are
+// on their way before the lse are there (24 x 37-4k tokens of head_dim 64, 25 parts
+// a sequence: 21.1 us the call, 21.9 with eight). A sequence of more than 64 parts among
 // them has its rows joined by the block's four warps, one row after the other.
 // kWide = true: a block per 32 columns of a row, its 32 groups of eight lanes
 // reading a part's 128-byte piece each, four ahead, so that a sequence cut into
@@ -773,9 +774,9 @@ __device__ __forceinline__ void join_rows(const Fp8DecodeParams& p) {
   const bool is_long = __syncthreads_or(row.count > 64);
   if (!is_long) {
     if (mine >= rows || row.count == 1) return;
-    float v[8][kPer], o[kPer];
+    float v[16][kPer], o[kPer];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 16; ++k)
       if (k < row.count) load(row, k, v[k]);
     float y[2];  // lane l: parts l and l + 32
 #pragma unroll
@@ -791,17 +792,17 @@ __device__ __forceinline__ void join_rows(const Fp8DecodeParams& p) {
     for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-    for (int i = 0; i < row.count; i += 8) {
+    for (int i = 0; i < row.count; i += 16) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 16; ++k) {
         if (i + k >= row.count) break;
         const float g = __shfl_sync(0xffffffffu, i < 32 ? f[0] : f[1], i + k);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) o[e] += g * v[k][e];
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i + 8 + k < row.count) load(row, i + 8 + k, v[k]);
+      for (int k = 0; k < 16; ++k)
+        if (i + 16 + k < row.count) load(row, i + 16 + k, v[k]);
     }
     const float inv = z == 0.f ? 0.f : 1.f / z;
     if constexpr (kPer == 4)
@@ -1057,7 +1058,7 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
     e = w ? launch_main<D, 2, true>(p, grid, stream) : launch_main<D, 2, false>(p, grid, stream);
   if (ev) cudaEventRecord(ev[1], stream);
   if (e != cudaSuccess) return e;
-  // parts a sequence has on average: past 32, the wide join
+  // parts a sequence has on average: past 32, the wide join (with 25, 24 x 37-4k tokens take 26 us against 21)
   const uint32_t rows = static_cast<uint32_t>(p.batch) * p.c.hkv * nrows;
   e = p.max_parts > 32 * p.batch
           ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p)
