@@ -239,15 +239,25 @@ struct F8Line {
   }
 };
 
-// The sequence that holds tile x (a warp's lanes look at 32 bounds at a time).
-__device__ __forceinline__ int f8_find_sequence(const int32_t* tile_base, int batch, int x) {
-  const int lane = threadIdx.x & 31;
-  for (int b0 = 0; b0 < batch; b0 += 32) {
-    const int b = b0 + lane;
-    const uint32_t m = __ballot_sync(0xffffffffu, b < batch && tile_base[b + 1] > x);
-    if (m) return b0 + __ffs(m) - 1;
+// The sequence that holds tile x, from sequence `from` on: the warp's lanes look at 32 bounds at a
+// time, first far apart, so that a batch padded with empty sequences costs little more than
+// without them (of 2048 sequences 8 with 0.5k-7k tokens: 53 us, 83 us one bound after the other).
+__device__ __forceinline__ int f8_find_sequence(const int32_t* tile_base, int batch, int x, int from) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = from, n = batch - from;
+  while (n > 32) {
+    const uint32_t step = (n + 31) >> 5, end = min(lo + (lane + 1) * step, static_cast<uint32_t>(batch));
+    const uint32_t m = __ballot_sync(0xffffffffu, tile_base[end] > x);
+    lo += (m ? __ffs(m) - 1 : 31) * step;
+    n = min(step, batch - lo);
   }
-  return batch - 1;
+  const uint32_t m = __ballot_sync(0xffffffffu, lane < n && tile_base[lo + lane + 1] > x);
+  return m ? static_cast<int>(lo) + __ffs(m) - 1 : batch - 1;
+}
+// The next sequence after b that holds tile x, most often b + 1.
+__device__ __forceinline__ int f8_next_sequence(const int32_t* tile_base, int batch, int x, int b) {
+  ++b;
+  return tile_base[b + 1] > x ? b : f8_find_sequence(tile_base, batch, x, b);
 }
 
 template <int D, int NR, bool WEIGHTS>
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
   for (int job = blockIdx.x * kF8Warps + warp; job < jobs; job += gridDim.x * kF8Warps) {
     const int part = fast_div(job, p.by_heads), h = job - part * hkv;
     const int x0 = line.begin(part), x1 = line.begin(part + 1);
-    int b = f8_find_sequence(tile_base, p.batch, x0);
+    int b = f8_find_sequence(tile_base, p.batch, x0, 0);
 
     // ---- producer: pages are looked up one tile before they are copied from
     int pb = b, pL = 0, pbase = 0, pend = 0;  // its sequence, length, first tile, end
@@ -317,8 +327,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
       slot = -1;
       if (x < x1) {
         if (x >= pend) {
-          do ++pb;
-          while (tile_base[pb + 1] <= x);
+          pb = f8_next_sequence(tile_base, p.batch, x, pb);
           enter();
         }
         const int tok = (x - pbase) * 16 + (lane & 15);
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
 
     for (int x = x0; x < x1;) {
       // ---- the sequence b, from tile t_lo on
-      while (tile_base[b + 1] <= x) ++b;
+      if (tile_base[b + 1] <= x) b = f8_next_sequence(tile_base, p.batch, x, b);
       const int L = length(b);
       const int base = tile_base[b], end = tile_base[b + 1];
       const int x_first = x, x_stop = min(end, x1);
@@ -978,9 +987,9 @@ __global__ void __launch_bounds__(32 * kF8WeightWarps) fp8_decode_weights_kernel
     const int part = fast_div(job, p.by_heads), h = job - part * hkv;
     int x = line.begin(part);
     const int x1 = line.begin(part + 1);
-    int b = f8_find_sequence(p.tile_base, p.batch, x);
+    int b = f8_find_sequence(p.tile_base, p.batch, x, 0);
     while (x < x1) {
-      while (p.tile_base[b + 1] <= x) ++b;
+      if (p.tile_base[b + 1] <= x) b = f8_next_sequence(p.tile_base, p.batch, x, b);
       bool bad;
       const int base = p.tile_base[b], stop = min(p.tile_base[b + 1], x1);
       const int end = min(f8_length(p, b, &bad), (stop - base) * 16);  // tokens of this part of the sequence
