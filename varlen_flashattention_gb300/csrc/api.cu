@@ -1012,8 +1012,10 @@ jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* a, void* ws, si
   if (a->batch > 0 && !aligned(a->new_offsets, 4)) return JFA_ERR_INVALID_ARG;
   if (a->batch > 0 && a->total_new > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return JFA_ERR_INVALID_ARG;
   if (a->weights && !aligned(a->weights, 4)) return JFA_ERR_INVALID_ARG;
-  // blocks of the grid: batch x chunks of 128 positions x heads, K and V
-  const double blocks = static_cast<double>(a->batch) * ((static_cast<int64_t>(a->max_new) + 126) / 128 + 1) * 2 * a->kv_heads;
+  // blocks of the grid: chunks of 128 positions x heads, K and V
+  const int64_t chunks = (static_cast<int64_t>(a->max_new) + 127) / 128 + 2;
+  const double blocks = std::max(static_cast<double>(a->batch) * chunks, a->total_new / 128 + 2.0 * a->batch) *
+                        2 * a->kv_heads;
   if (blocks >= 2147483647.0) return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
   if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;

@@ -19,10 +19,10 @@
 // bytes read, as much written, per kept token and head) and by the latency of
 // its passes for the selection.
 //
-// Both kernels that write codes give 128 consecutive positions of one head's K
-// or V to a block of threads: whole scale blocks (a power of two up to 128), the
-// values held in registers between the amax and the encoding, so every byte
-// is read once.
+// The kernels that write codes hold the values in registers between the amax and
+// the encoding, so every byte is read once: a scale block by a warp, or 128
+// consecutive positions of one head (whole scale blocks, a power of two up to
+// 128) by a block of threads.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -31,7 +31,7 @@
 
 namespace jfa {
 
-constexpr int kChunk = 128;    // positions of one block of threads
+constexpr int kChunkShift = 7, kChunk = 1 << kChunkShift;  // positions of one block of threads
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ append
@@ -44,8 +44,8 @@ struct Fp8AppendParams {
   const int32_t* page_table;
   const int32_t* seqlens;
   int32_t batch, max_pages, page_size, total_new, max_new;
-  int32_t chunks;            // of 128 positions a sequence can touch; 0: the blocks look their chunk up
-  FastDiv by_heads, by_chunks;  // division by 2 * hkv and by chunks
+  int32_t blocks;               // scale blocks a sequence can touch, 0: found in the offsets (the kernel of short blocks)
+  FastDiv by_heads, by_blocks;  // division by 2 * hkv and by `blocks`
   float* weights;
   int32_t* status;
 };
@@ -152,27 +152,72 @@ __device__ __forceinline__ bool append_range_ok(const Fp8AppendParams& p, int b,
 
 // One block checks the whole call, offsets, lengths and the pages written to, and
 // sets the status block; the others pass over what is wrong without a word.
-// That spares the launch that would have to clear the status block for them.
+// That spares the launch that would have to clear the status block for them. A
+// thread a sequence; the pages of those with many new ones are left to the warps
+// (512 sequences 7 us, a warp for each 32 us).
 __device__ void append_report(const Fp8AppendParams& p) {
-  const int lane = threadIdx.x & 31;
+  __shared__ int32_t s_left, s_b[kThreads], s_lo[kThreads], s_hi[kThreads];
+  const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
-  for (int b = threadIdx.x >> 5; b < p.batch; b += kThreads / 32) {
-    const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
-    if (!append_range_ok(p, b, o0, o1, L)) {
-      bad = true;
-    } else if (o1 > o0) {
-      const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-      const int last = fast_div(L - 1, p.c.page);
-#pragma unroll 4
-      for (int i = fast_div(L - (o1 - o0), p.c.page) + lane; i <= last; i += 32)
-        bad |= static_cast<uint32_t>(pt[i]) >= static_cast<uint32_t>(p.c.num_pages);
+  auto check = [&](int b, int i) {
+    const int32_t page = p.page_table[static_cast<int64_t>(b) * p.max_pages + i];
+    bad |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.num_pages);
+  };
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    if (tid == 0) s_left = 0;
+    __syncthreads();
+    const int b = b0 + tid;
+    if (b < p.batch) {
+      const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
+      if (!append_range_ok(p, b, o0, o1, L)) {
+        bad = true;
+      } else if (o1 > o0) {
+        const int lo = fast_div(L - (o1 - o0), p.c.page), hi = fast_div(L - 1, p.c.page);
+        if (hi - lo < 4) {
+          for (int i = lo; i <= hi; ++i) check(b, i);
+        } else {
+          const int at = atomicAdd(&s_left, 1);
+          s_b[at] = b;
+          s_lo[at] = lo;
+          s_hi[at] = hi;
+        }
+      }
     }
+    __syncthreads();
+    for (int j = tid >> 5; j < s_left; j += kThreads / 32) {
+      const int last = s_hi[j];
+#pragma unroll 4
+      for (int i = s_lo[j] + lane; i <= last; i += 32) check(s_b[j], i);
+    }
+    __syncthreads();
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x < kStatusBytes / 4)
-    p.status[threadIdx.x] = !bad ? 0 : (threadIdx.x == 0 ? JFA_ERR_BAD_INPUT : (threadIdx.x == 1 ? kSiteFp8Append : 0));
+  if (tid < kStatusBytes / 4)
+    p.status[tid] = !bad ? 0 : (tid == 0 ? JFA_ERR_BAD_INPUT : (tid == 1 ? kSiteFp8Append : 0));
 }
 
+// n consecutive positions touch at most n / c + 2 runs of c = 2^shift, so the runs of sequence b can be
+// numbered from offsets[b] / c + 2 b on, all distinct. This is the sequence of such a number: the last b
+// whose first one is not above it; the warp's lanes look at 32 at a time, first far apart. (Offsets that
+// do not rise give some sequence.)
+__device__ __forceinline__ int find_sequence(const int32_t* offsets, int batch, int shift, int number) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = 0, n = batch;
+  while (n > 1) {
+    const uint32_t step = (n + 31) >> 5, b = lo + lane * step;
+    const bool in = lane * step < n && (offsets[b] >> shift) + 2 * static_cast<int64_t>(b) <= number;
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    const uint32_t k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return static_cast<int>(lo);
+}
+
+// A block of threads a chunk of 128 positions of one head's K or V, for long runs in blocks too large for
+// a warp's registers or too small to fill them. Bound by HBM, at 78% of the copy rate (16 prompts of
+// 61 to 8192 tokens, 8 heads of 128: 77 us): the loads of a chunk are all in flight at once, four
+// blocks an SM; chunks of 64, 128 or 512 threads, and K and V by the same block took 74 to 100 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) fp8_append_kernel(const Fp8AppendParams p) {
   constexpr int kLanes = D / 8;              // threads of a row, 8 values each
@@ -194,48 +239,11 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_append_kernel(const Fp8Append
   const int hv = unit - chunk * 2 * hkv, h = hv >> 1;  // heads first: their rows are neighbours in memory
   const bool is_v = hv & 1;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  int b, ci, o0, L, f;  // sequence, its chunk, first row of its new tokens, length, first new position
-  if (p.chunks) {
-    b = fast_div(chunk, p.by_chunks);
-    ci = chunk - b * p.chunks;
-    o0 = p.new_offsets[b];
-    const int o1 = p.new_offsets[b + 1];
-    L = p.seqlens[b];
-    f = L - (o1 - o0);
-    if (!append_range_ok(p, b, o0, o1, L) || o1 == o0) return;
-  } else {
-    int before = 0;
-    for (b = lane;; b += 32) {
-      int o1 = 0, n = 0;
-      o0 = L = 0;
-      if (b < p.batch) {
-        o0 = p.new_offsets[b];
-        o1 = p.new_offsets[b + 1];
-        L = p.seqlens[b];
-        if (o1 > o0 && append_range_ok(p, b, o0, o1, L)) n = (L - 1) / kChunk - (L - (o1 - o0)) / kChunk + 1;
-      }
-      int x = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + x > chunk);
-      if (past) {
-        const int src = __ffs(past) - 1;
-        ci = __shfl_sync(0xffffffffu, chunk - before - x + n, src);
-        f = __shfl_sync(0xffffffffu, L - (o1 - o0), src);
-        L = __shfl_sync(0xffffffffu, L, src);
-        o0 = __shfl_sync(0xffffffffu, o0, src);
-        b = b - lane + src;
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, x, 31);
-      if (b - lane + 32 >= p.batch) return;
-    }
-  }
+  const int b = find_sequence(p.new_offsets, p.batch, kChunkShift, chunk);
+  const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
+  const int ci = chunk - (o0 / kChunk + 2 * b), f = L - (o1 - o0);  // the sequence's chunk, its first new position
+  if (ci < 0 || o1 == o0 || !append_range_ok(p, b, o0, o1, L) || ci > (L - 1) / kChunk - f / kChunk) return;
   const int p0 = ((f / kChunk) + ci) * kChunk;  // this block's positions: p0 .. p0 + 127
-  if (p0 >= L) return;
   const int bs = p.c.block_shift;
   const int old0 = (f >> bs) << bs;            // older tokens of f's block: old0 .. f - 1
   const int sub = tid % kLanes, r0 = tid / kLanes;
@@ -313,6 +321,77 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_append_kernel(const Fp8Append
   }
 }
 
+// A warp a scale block: its new rows, ROWS at most, stay in the warp's registers, and nothing but the
+// warp's own reduction lies between their loads and the stores, where the chunks' blocks of threads wait
+// at three barriers. Bound by HBM for prompts, by the chain of loads (offsets and length, page, old
+// scale) for a step's tokens.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS > 16 ? 2 : 4) fp8_append_warp_kernel(const Fp8AppendParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, 8 values each; rows of a warp
+  if (blockIdx.x == 0) {
+    append_report(p);
+    return;
+  }
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, r0 = lane / kLanes;
+  const int hkv = p.c.hkv, bs = p.c.block_shift;
+  const int job = (static_cast<int>(blockIdx.x) - 1) * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+  const int unit = fast_div(job, p.by_heads), hv = job - unit * 2 * hkv, h = hv >> 1;
+  const bool is_v = hv & 1;
+  const int b = p.blocks ? fast_div(unit, p.by_blocks) : find_sequence(p.new_offsets, p.batch, bs, unit);
+  if (b >= p.batch) return;
+  const int o0 = p.new_offsets[b], o1 = p.new_offsets[b + 1], L = p.seqlens[b];
+  const int f = L - (o1 - o0);  // the first new position
+  const int bi = unit - (p.blocks ? b * p.blocks : (o0 >> bs) + 2 * b);  // the sequence's block
+  if (o1 == o0 || bi < 0 || !append_range_ok(p, b, o0, o1, L) || bi > ((L - 1) >> bs) - (f >> bs)) return;
+  const int start = ((f >> bs) + bi) << bs;  // the block's first position
+  const int pg = fast_div(start, p.c.page);
+  const int64_t row_elems = static_cast<int64_t>(hkv) * D;
+  const int lo = max(start, f), hi = min(L, start + (1 << bs));  // its new positions
+  const __nv_bfloat16* src = (is_v ? p.v : p.k) + (static_cast<int64_t>(o0) + lo - f) * row_elems +
+                             static_cast<int64_t>(h) * D + 8 * sub;
+  constexpr int kMost = ROWS / kRows;  // passes over the new rows
+  uint4 raw[kMost];
+  uint32_t top = 0, odd = 0;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int i = k * kRows + r0;
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (lo + i < hi) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + i * row_elems));
+  }
+  const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + pg];
+  if (p.weights && !is_v && lane < hi - lo)
+    p.weights[(static_cast<int64_t>(b) * hkv + h) * (static_cast<int64_t>(p.max_pages) * p.page_size) + lo + lane] = 0.f;
+  if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.c.num_pages)) return;
+  const int row = page * p.page_size + (start - pg * p.page_size);  // of the block's first position
+  float* cell = (is_v ? p.c.vs : p.c.ks) + static_cast<int64_t>(row >> bs) * hkv + h;
+  const float old = start < f ? *cell : 0.f;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    bool finite;
+    top = max(top, amax8_bf16(raw[k], &finite));
+    if (!finite) odd |= 1u << k;
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const float s = fmaxf(e4m3_block_scale(__uint_as_float(top << 16)), old);
+  __syncwarp();  // every lane has read the cell
+  if (lane == 0) *cell = s;
+  const float inv = is_pow2(s) ? 1.f / s : 0.f;
+  uint8_t* codes = (is_v ? p.c.vc : p.c.kc) + row * row_elems + static_cast<int64_t>(h) * D + 8 * sub;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int pos = lo + k * kRows + r0;
+    if (pos < hi)
+      *reinterpret_cast<uint2*>(codes + (pos - start) * row_elems) =
+          inv != 0.f && !((odd >> k) & 1) ? encode8_pow2(raw[k], __float2bfloat162_rn(inv)) : encode8_bf16(raw[k], s);
+  }
+  if (start < f && s != old) {  // the older tokens of a block whose scale has grown
+    for (int pos = start + r0; pos < f; pos += kRows) {
+      uint2* dst = reinterpret_cast<uint2*>(codes + (pos - start) * row_elems);
+      *dst = recode8(*dst, old, s);
+    }
+  }
+}
+
 cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t* status, cudaStream_t stream) {
   Fp8AppendParams p{};
   p.k = static_cast<const __nv_bfloat16*>(a.k);
@@ -333,19 +412,37 @@ cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t*
   p.page_size = a.page_size;
   p.total_new = a.total_new;
   p.max_new = a.max_new;
-  // n consecutive positions touch at most (n + 126) / 128 + 1 chunks. With lengths as uneven as
-  // prompts' most blocks of batch x that many have nothing to do, so the blocks look up the
-  // chunk of their number instead, a warp over the sequences, where the batch is small:
-  // 16 prompts of 61 to 8192 tokens take 76 us, and 89 us with a fixed number each.
-  const int64_t fixed = (static_cast<int64_t>(a.max_new) + kChunk - 2) / kChunk + 1;
-  const int64_t most = a.total_new / kChunk + 2 * static_cast<int64_t>(a.batch);  // chunks of all sequences
-  const bool look_up = a.batch <= 128 && most < fixed * a.batch;
-  p.chunks = look_up ? 0 : static_cast<int32_t>(fixed);
   p.by_heads = make_fast_div(2 * a.kv_heads);
-  p.by_chunks = make_fast_div(static_cast<int32_t>(fixed));
   p.weights = a.weights;
   p.status = status;
-  const uint32_t grid = static_cast<uint32_t>((look_up ? most : fixed * a.batch) * 2 * a.kv_heads) + 1;
+  const int64_t heads = 2 * static_cast<int64_t>(a.kv_heads);
+  // A warp a scale block where the block's rows fit its registers and are not few among many: of 8 heads
+  // of 128, 16 prompts of 61 to 8192 tokens take 66 us with blocks of 16 tokens (77 by chunks), 75 with
+  // blocks of 32 (77), but 99 with blocks of 8 (76), a row or so a warp. Of few new tokens it is the faster one
+  // whatever the block: 512 x 1 token 6.9 us (66), 256 x 24 in blocks of 128 12.8 (46), 256 x 16 in
+  // blocks of 1 37 (40).
+  const int64_t fixed = (static_cast<int64_t>(a.max_new) + a.block_size - 2) / a.block_size + 1;
+  const int64_t most = a.total_new / a.block_size + 2 * static_cast<int64_t>(a.batch);
+  const int64_t jobs = std::min(fixed * a.batch, most) * heads;
+  const bool short_blocks = a.max_new <= 16 || (a.block_size >= 16 && std::min(a.max_new, a.block_size) <= 32);
+  if (short_blocks && jobs < (int64_t(1) << 31) - 64) {
+    p.blocks = fixed * a.batch <= most ? static_cast<int32_t>(fixed) : 0;
+    p.by_blocks = make_fast_div(std::max(p.blocks, 1));
+    const uint32_t grid = static_cast<uint32_t>((jobs + kThreads / 32 - 1) / (kThreads / 32)) + 1;
+    if (std::min(a.max_new, a.block_size) <= 16) {
+      if (a.head_dim == 128)
+        fp8_append_warp_kernel<128, 16><<<grid, kThreads, 0, stream>>>(p);
+      else
+        fp8_append_warp_kernel<64, 16><<<grid, kThreads, 0, stream>>>(p);
+    } else {
+      if (a.head_dim == 128)
+        fp8_append_warp_kernel<128, 32><<<grid, kThreads, 0, stream>>>(p);
+      else
+        fp8_append_warp_kernel<64, 32><<<grid, kThreads, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+  }
+  const uint32_t grid = static_cast<uint32_t>((a.total_new / kChunk + 2 * static_cast<int64_t>(a.batch)) * heads) + 1;
   if (a.head_dim == 128)
     fp8_append_kernel<128><<<grid, kThreads, 0, stream>>>(p);
   else
@@ -368,6 +465,7 @@ struct Fp8EvictParams {
   float* new_weights;    // [B, hkv, new_max_pages * page_size]
   uint8_t* page_ok;      // [B, new_max_pages]: the new page may be written
   int32_t bitmap_words;  // of the pages' bitmaps in shared memory
+  int32_t shrink;        // short sequences leave blocks of their clusters to others
   int32_t* status;
 };
 
@@ -408,23 +506,53 @@ struct alignas(16) SelShared {
   int32_t hits;              // how many there are
 };
 
-// Every sequence's first `used(b)` entries of a table, each once, by one block: a
-// warp a sequence, or all of them on one sequence after the other where there
-// are few. f(b, i, entry) is called by the thread that read the entry.
+// Every sequence's first `used(b)` entries of a table, each once, by one block: all threads on one
+// sequence after the other, or a warp a sequence, the lengths of 32 at once and the next one's first
+// entries on their way (512 sequences of up to 2k tokens 267 us the call, 294 one after the other);
+// whichever takes fewer steps where the rows are full (15 x 20k-32k tokens in pages of 16: a warp each
+// 29 us, all on each 40). f(b, i, entry) is called by the thread that read the entry.
 template <class Used, class F>
 __device__ __forceinline__ void for_entries(const int32_t* table, int batch, int width, Used used, F f) {
-  const bool few = batch < kSelWarps;
-  const int stride = few ? kSelThreads : 32, first = few ? threadIdx.x : threadIdx.x & 31;
-  for (int b = few ? 0 : threadIdx.x >> 5; b < batch; b += few ? 1 : kSelWarps) {
-    const int n = used(b);
+  const int lane = threadIdx.x & 31;
+  auto fetch = [&](int b, int n, int i0, int stride, int32_t (&v)[8]) {
     const int32_t* row = table + static_cast<int64_t>(b) * width;
-    for (int i0 = first; i0 < n; i0 += 8 * stride) {
-      int32_t v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = i0 + k * stride < n ? row[i0 + k * stride] : 0;
+    for (int k = 0; k < 8; ++k) v[k] = i0 + k * stride < n ? row[i0 + k * stride] : 0;
+  };
+  auto visit = [&](int b, int n, int i0, int stride, const int32_t (&v)[8]) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i0 + k * stride < n) f(b, i0 + k * stride, v[k]);
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * stride < n) f(b, i0 + k * stride, v[k]);
+  };
+  const int64_t steps_all = batch * static_cast<int64_t>(width / (8 * kSelThreads) + 1);
+  if (steps_all <= ((batch - 1) / kSelWarps + 1) * static_cast<int64_t>(width / 256 + 1)) {
+    for (int b = 0; b < batch; ++b) {
+      const int n = used(b);
+      for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kSelThreads) {
+        int32_t v[8];
+        fetch(b, n, i0, kSelThreads, v);
+        visit(b, n, i0, kSelThreads, v);
+      }
+    }
+    return;
+  }
+  for (int b0 = threadIdx.x >> 5; b0 < batch; b0 += 32 * kSelWarps) {
+    const int mine = b0 + lane * kSelWarps, many = min(32, (batch - b0 + kSelWarps - 1) / kSelWarps);
+    const int n_mine = mine < batch ? used(mine) : 0;
+    int n = __shfl_sync(0xffffffffu, n_mine, 0);
+    int32_t v[8], next[8];
+    fetch(b0, n, lane, 32, v);
+    for (int j = 0; j < many; ++j) {
+      const int b = b0 + j * kSelWarps, n_next = j + 1 < many ? __shfl_sync(0xffffffffu, n_mine, j + 1) : 0;
+      fetch(b + kSelWarps, n_next, lane, 32, next);
+      visit(b, n, lane, 32, v);
+      for (int i0 = lane + 256; i0 < n; i0 += 256) {
+        fetch(b, n, i0, 32, v);
+        visit(b, n, i0, 32, v);
+      }
+      n = n_next;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = next[k];
     }
   }
 }
@@ -495,25 +623,34 @@ __global__ void __launch_bounds__(kSelThreads, KEYS <= 16 ? 2 : 1)
     if (blockIdx.x == 0) evict_check(p, s_bitmap);
     return;
   }
-  reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);  // 512 threads: hist and sum
-  static_assert(kSelThreads * 16 == sizeof(sh.hist) + sizeof(sh.sum), "one int4 a thread clears both");
-  if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before the first addition
-  allow_next_grid();
-  const int rank = cluster > 1 ? static_cast<int>(blockIdx.x % cluster) : 0;
   const int seg = static_cast<int>(blockIdx.x) / cluster - 1;  // the first cluster's first block checks the call
   const int b = seg / p.c.hkv, h = seg % p.c.hkv;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int new_cap = p.new_max_pages * p.page_size;
-  const int wide = cluster * kSelThreads, wtid = rank * kSelThreads + tid;  // threads of the cluster
   int L = p.seqlens[b];
   if (L < 0 || L > cap || (L > 0 && p.c.num_pages == 0)) L = 0;
+  const bool choose = L > p.keep && p.keep > p.first + p.recent;
+  // The cluster is made for a full row of the table. Where not all clusters are on the device at
+  // once, a shorter sequence takes as many of the blocks as its keys (or the zeros behind what is
+  // kept) fill, and the others leave: 32 x 1k-8k tokens in rows of 131k 59 us, 137 us
+  // without. (Barriers of a cluster wait for the threads that have not left.)
+  const int rank = cluster > 1 ? static_cast<int>(blockIdx.x % cluster) : 0;
+  if (cluster > 1 && p.shrink) {
+    const int work = max(choose ? L - p.recent - p.first : 0, new_cap), each = KEYS * kSelThreads;
+    cluster = min(cluster, max(1, (work - 1) / each + 1));
+    if (rank >= cluster) return;
+  }
+  reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);  // 512 threads: hist and sum
+  static_assert(kSelThreads * 16 == sizeof(sh.hist) + sizeof(sh.sum), "one int4 a thread clears both");
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before the first addition
+  allow_next_grid();
+  const int wide = cluster * kSelThreads, wtid = rank * kSelThreads + tid;  // threads of the cluster
   const int n = min(L, p.keep);
   const float* w = p.weights + seg * cap;
   int32_t* kept = p.kept + static_cast<int64_t>(seg) * p.keep;
   float* nw = p.new_weights + static_cast<int64_t>(seg) * new_cap;
 
   // the candidates c0 .. c1 - 1, and this warp's run lo .. hi - 1 of them
-  const bool choose = L > p.keep && p.keep > p.first + p.recent;
   const int c0 = p.first, c1 = max(L - p.recent, c0);
   const int runs = cluster * kSelWarps;
   const int per_warp = choose ? ((c1 - c0 + runs - 1) / runs + 31) / 32 * 32 : 0;
@@ -764,7 +901,6 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
   __shared__ uint32_t s_amax[2][kChunk];
   __shared__ float s_new[2][kChunk];
 
-  wait_prior_grid();
   const int hkv = p.c.hkv, bs = p.c.block_shift, tid = threadIdx.x;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int64_t new_cap = static_cast<int64_t>(p.new_max_pages) * p.page_size;
@@ -776,6 +912,29 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
     h = job - chunk * hkv;
     b = fast_div(chunk, p.by_chunks);
     j0 = (chunk - b * p.chunks) * kChunk;
+  };
+  // This block's jobs that have rows, 32 looked at together, so that those of empty or short sequences
+  // cost next to nothing (512 sequences of which 8 hold 16k-32k tokens: 114 us the call, 446 us without).
+  const int step = gridDim.x;
+  int64_t scan = static_cast<int64_t>(blockIdx.x) - 32 * step;
+  uint32_t found = 0;  // among scan, scan + step, ...
+  auto next_job = [&]() -> int {
+    while (!found) {
+      scan += 32 * step;
+      if (scan >= jobs) return jobs;
+      const int64_t job = scan + (tid & 31) * step;
+      bool rows = false;
+      if (job < jobs) {
+        int b, j0, h;
+        place(static_cast<int>(job), b, j0, h);
+        const int L = p.seqlens[b];
+        rows = L > j0 && L <= cap;
+      }
+      found = __ballot_sync(0xffffffffu, rows);
+    }
+    const int i = __ffs(found) - 1;
+    found &= found - 1;
+    return static_cast<int>(scan) + i * step;
   };
   auto kept_of = [&](int job) -> int {  // old position of this thread's new one, -1: none
     if (job >= jobs || tid >= kChunk) return -1;
@@ -804,12 +963,12 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
     s_src[buf][tid] = src;
     s_dst[buf][tid] = dst;
   };
-  const int step = gridDim.x;
-  int t_next = kept_of(blockIdx.x);
-  look_up(blockIdx.x, t_next, 0);
-  t_next = kept_of(blockIdx.x + step);
-  int buf = 0;
-  for (int job = blockIdx.x; job < jobs; job += step, buf ^= 1) {
+  int job = next_job(), next = next_job();
+  wait_prior_grid();
+  int t_next = kept_of(job);
+  look_up(job, t_next, 0);
+  t_next = kept_of(next);
+  for (int buf = 0; job < jobs; buf ^= 1) {
     if (tid < kChunk) s_amax[0][tid] = s_amax[1][tid] = 0;
     __syncthreads();  // this chunk's rows are known
     int b, j0, h;
@@ -831,8 +990,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
         }
       }
     }
-    look_up(job + step, t_next, buf ^ 1);
-    t_next = kept_of(job + 2 * step);
+    look_up(next, t_next, buf ^ 1);
+    job = next;
+    next = next_job();
+    t_next = kept_of(next);
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
 #pragma unroll
@@ -888,9 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
 }
 
 template <int KEYS>
-static cudaError_t launch_select_keys(const Fp8EvictParams& p, int cluster, cudaStream_t stream) {
+static cudaError_t launch_select_keys(Fp8EvictParams& p, int cluster, int sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((static_cast<uint32_t>(p.batch) * p.c.hkv + 1) * cluster);
+  p.shrink = cfg.gridDim.x > static_cast<uint32_t>(sms) * (KEYS <= 16 ? 2 : 1);
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(p.bitmap_words) * 8;
   cfg.stream = stream;
@@ -912,13 +1074,13 @@ static cudaError_t launch_select_keys(const Fp8EvictParams& p, int cluster, cuda
 // By the candidates that a full row of the page table can hold: one block for up to 8192 (4 keys a
 // thread up to 2048, else 16), clusters of up to 8 blocks (the portable size) past that, and
 // 32 keys a thread past 65,536.
-static cudaError_t launch_select(const Fp8EvictParams& p, cudaStream_t stream) {
+static cudaError_t launch_select(Fp8EvictParams& p, int sms, cudaStream_t stream) {
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  if (cap <= 4 * kSelThreads) return launch_select_keys<4>(p, 1, stream);
+  if (cap <= 4 * kSelThreads) return launch_select_keys<4>(p, 1, sms, stream);
   int cluster = 1;
   while (cluster < 8 && cap > static_cast<int64_t>(cluster) * 16 * kSelThreads) cluster *= 2;
-  return cap <= static_cast<int64_t>(cluster) * 16 * kSelThreads ? launch_select_keys<16>(p, cluster, stream)
-                                                                 : launch_select_keys<32>(p, cluster, stream);
+  return cap <= static_cast<int64_t>(cluster) * 16 * kSelThreads ? launch_select_keys<16>(p, cluster, sms, stream)
+                                                                 : launch_select_keys<32>(p, cluster, sms, stream);
 }
 
 cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint8_t* page_ok, int32_t* status, int sms,
@@ -952,7 +1114,7 @@ cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint8_t* p
   p.page_ok = page_ok;
   p.bitmap_words = std::max(1, std::min((a.num_pages + 31) / 32, kMostBitmapWords));
   p.status = status;
-  const cudaError_t e = launch_select(p, stream);
+  const cudaError_t e = launch_select(p, sms, stream);
   if (e != cudaSuccess) return e;
   const int jobs = a.batch * p.chunks * a.kv_heads;
   const dim3 grid(std::min(jobs, sms * 4));
