@@ -163,6 +163,20 @@ def test_decode_many_sequences(B):
         jfa.jfa_decode_fp8(q.cuda(), *_cache(g), check=True)
 
 
+@pytest.mark.parametrize("B", [90, 512, 2100])
+def test_decode_padded_batch(B):
+    """Few sequences in use among many empty ones, at the ends and far apart: parts cross long runs of nothing."""
+    lens = [0] * B
+    for b, L in ((0, 700), (1, 33), (B // 3, 1900), (B // 3 + 40, 16), (B - 2, 5000), (B - 1, 1)):
+        lens[b] = L
+    c = _case(31, lens, 2, 64, 16, 16)
+    g = _gpu(c)
+    q = _bf16(c["rng"], B, 1, 6, 64)
+    w = torch.zeros(B, 2, c["cap"]).cuda()
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), weights_out=w, check=True)
+    check_decode(c, q, o, lse, 64 ** -0.5, None, w, np.zeros(w.shape, dtype=np.float32), what=f"B={B}")
+
+
 @pytest.mark.parametrize("H,lens", [(40, [700, 3]), (2700, [20, 0, 35])])
 def test_decode_many_heads(H, lens):
     """More heads than a part's warps, and than all warps."""
@@ -334,7 +348,7 @@ def test_append(d, P, block, old, new):
 
 @pytest.mark.parametrize("B,new_hi", [(200, 3), (150, 400), (40, 700)])
 def test_append_many_sequences(B, new_hi):
-    """Blocks with a fixed chunk each (batches past 128), and blocks that look theirs up."""
+    """Scale blocks with a fixed number each, and runs found in the offsets."""
     rng = np.random.default_rng(24)
     old, new = rng.integers(0, 40, B), rng.integers(0, new_hi + 1, B)
     new[3] = new_hi
@@ -345,6 +359,72 @@ def test_append_many_sequences(B, new_hi):
     offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     g = _gpu(c)
     jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.from_numpy(offs).cuda(), new_hi, check=True)
+    kvo.append(np64(k), np64(v), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, offs)
+    for x in ("kc", "vc"):
+        assert _same_codes(g[x].cpu().numpy(), c[x]), x
+    assert (g["ks"].cpu().numpy() == c["ks"]).all() and (g["vs"].cpu().numpy() == c["vs"]).all()
+
+
+@pytest.mark.parametrize("d,P,block,old,new", [
+    (128, 32, 32, [0, 5, 31, 32, 300, 9], [65, 1, 300, 32, 33, 0]),
+    (64, 96, 32, [0, 5, 31, 32, 300, 9], [65, 1, 300, 32, 33, 0]),
+    (128, 128, 128, [0, 120, 127, 128, 300, 9], [32, 17, 2, 31, 0, 25]),
+    (64, 128, 64, [0, 60, 63, 64, 300, 9], [17, 17, 17, 17, 1, 16]),
+    (128, 16, 16, [0, 15, 16, 1, 300, 9], [16, 2, 15, 17, 0, 400]),
+    (64, 8, 2, [0, 1, 2, 3, 300, 9], [16, 2, 15, 1, 0, 3]),
+    (128, 64, 64, [0, 60, 63, 64, 300, 9], [200, 1, 129, 64, 0, 65]),
+])
+def test_append_behind_scales_of_every_kind(d, P, block, old, new):
+    """Every number of rows a warp holds, and chunks, behind blocks whose scale is larger or smaller."""
+    lens = [a + b for a, b in zip(old, new)]
+    c = _case(32, lens, 2, d, P, block)
+    rng = c["rng"]
+    for x in ("ks", "vs"):
+        c[x][:] = rng.choice(np.float32([2.0 ** -20, 2.0 ** -9, 2.0 ** -6, 0.25, 4.0]), c[x].shape)
+    n = sum(new)
+    k, v = (_bf16(rng, n, 2, d) for _ in range(2))
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    g = _gpu(c)
+    jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.from_numpy(offs).cuda(), max(new), check=True)
+    kvo.append(np64(k), np64(v), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, offs)
+    for x in ("kc", "vc"):
+        assert _same_codes(g[x].cpu().numpy(), c[x]), x
+    assert (g["ks"].cpu().numpy() == c["ks"]).all() and (g["vs"].cpu().numpy() == c["vs"]).all()
+
+
+@pytest.mark.parametrize("d,P,block,new", [(128, 32, 32, 20), (64, 64, 64, 50), (128, 128, 128, 9)])
+def test_append_at_a_scale_that_is_no_power_of_two(d, P, block, new):
+    """A caller's scale of 0.3 has room for the new values (below 0.3 * 448) and stays. A code is then off by half
+    a step, 2^-4 of the value or 2^-10 of the scale, and the quotient's own rounding to fp32, 2^-24 of it."""
+    old = block - 3
+    c = _case(34, [old + new], 2, d, P, block)
+    c["ks"][:] = c["vs"][:] = 0.3
+    k, v = _bf16(c["rng"], new, 2, d), _bf16(c["rng"], new, 2, d)
+    g = _gpu(c)
+    jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.tensor([0, new], dtype=torch.int32).cuda(), new,
+                             check=True)
+    first = c["table"][0, old // P]
+    for x, sc, y in (("kc", "ks", k), ("vc", "vs", v)):
+        s = np.float64(np.float32(0.3))
+        assert (g[sc][first].cpu().numpy()[-1] == np.float32(0.3)).all()
+        got = kvo.e4m3_decode(g[x][first, P - 3:].cpu().numpy()) * s
+        want = np64(y)[:3]
+        assert (np.abs(got - want) <= 2.0 ** -4 * (1 + 2.0 ** -20) * np.abs(want) + 2.0 ** -10 * s).all()
+
+
+@pytest.mark.parametrize("B,long,block", [(1100, 500, 16), (1100, 500, 8), (33, 129, 64), (600, 32, 128)])
+def test_append_one_prompt_among_steps(B, long, block):
+    """One long run of new tokens among sequences that get one or none: its place is found in the offsets."""
+    rng = np.random.default_rng(33)
+    old, new = rng.integers(0, 40, B), rng.integers(0, 2, B)
+    new[B // 2], new[B - 1] = long, min(long, 33)
+    lens = [int(a + b) for a, b in zip(old, new)]
+    c = _case(33, lens, 1, 64, 128, block)
+    n = int(new.sum())
+    k, v = _bf16(rng, n, 1, 64), _bf16(rng, n, 1, 64)
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    g = _gpu(c)
+    jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.from_numpy(offs).cuda(), long, check=True)
     kvo.append(np64(k), np64(v), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, offs)
     for x in ("kc", "vc"):
         assert _same_codes(g[x].cpu().numpy(), c[x]), x
@@ -389,9 +469,19 @@ def test_evict_fills_the_card(lens, H, d, P, block, keep):
     _evict_case(lens, H, d, P, block, keep, 2, 5)
 
 
-def _evict_case(lens, H, d, P, block, keep, first, recent):
+@pytest.mark.parametrize("lens,H,d,P,block,keep,cap_pages", [
+    ([0, 3, 200, 41, 500, 20000, 1300], 24, 64, 128, 32, 100, 1100),
+    ([0, 3, 90, 41, 500, 1300] + [0] * 290 + [77, 0, 1, 300], 4, 64, 16, 16, 61, 700),
+    ([700, 3, 90, 41, 500, 1300, 9000], 2, 128, 8, 8, 300, 4100),
+])
+def test_evict_of_short_sequences_in_wide_tables(lens, H, d, P, block, keep, cap_pages):
+    """Rows of the page table far longer than most sequences, and batches mostly of empty ones."""
+    _evict_case(lens, H, d, P, block, keep, 2, 5, cap_pages)
+
+
+def _evict_case(lens, H, d, P, block, keep, first, recent, cap_pages=None):
     width = -(-keep // P)
-    c = _case(9, lens, H, d, P, block, spare=width * len(lens) + 1)
+    c = _case(9, lens, H, d, P, block, cap_pages, spare=width * len(lens) + 1)
     rng = c["rng"]
     w = np.exp(2 * rng.standard_normal((len(lens), H, c["cap"]))).astype(np.float32)
     w[rng.random(w.shape) < 0.3] = 0
