@@ -642,7 +642,7 @@ def jfa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k,
                   seqlens_k=seqlens_k, weights=weights, weights_out=weights_out, o=o, lse=lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     o = torch.empty_like(q) if o is None else o
-    lse = k_scale.new_empty((B, ql, Hq)) if lse is None else lse
+    lse = torch.empty((B, ql, Hq), dtype=torch.float32, device=dev) if lse is None else lse
     if stream is not None:  # new memory belongs to the current stream
         o.record_stream(stream)
         lse.record_stream(stream)
@@ -683,9 +683,10 @@ def jfa_cache_evict_fp8(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_
     dev = _device(k_cache=kc, v_cache=vc, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
                   seqlens_k=seqlens_k, weights=weights, new_page_table=new_page_table, kept=kept,
                   new_seqlens=new_seqlens, new_weights=new_weights)
-    kept = page_table.new_empty((B, Hkv, keep)) if kept is None else kept
+    kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev) if kept is None else kept
     new_seqlens = torch.empty_like(seqlens_k) if new_seqlens is None else new_seqlens
-    new_weights = weights.new_empty((B, Hkv, nmp * P)) if new_weights is None else new_weights
+    if new_weights is None:
+        new_weights = torch.empty((B, Hkv, nmp * P), dtype=torch.float32, device=dev)
     if stream is not None:  # new memory belongs to the current stream
         for t in (kept, new_seqlens, new_weights):
             t.record_stream(stream)
