@@ -198,6 +198,27 @@ def test_decode_one_long_among_short():
     check_decode(c, q, o, lse, 0.125, what="one long")
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,q_len,d", [
+    ([30] * 50 + [20000] + [20] * 39, 4, 1, 4, 128),     # thousands of parts: the weights behind the join
+    ([9, 16000] + [20] * 12, 16, 4, 3, 64),              # hundreds: beside it
+    ([12000, 0, 15, 14000] + [0, 33] * 10, 16, 8, 2, 128),
+    ([9000] + [0] * 598 + [7000], 6, 2, 1, 64),          # numbered by a kernel of its own
+])
+def test_decode_weights_of_long_sequences_among_short(lens, Hq, Hkv, q_len, d):
+    c = _case(35, lens, Hkv, d, 16, 16)
+    g = _gpu(c)
+    q = _bf16(c["rng"], len(lens), q_len, Hq, d)
+    w = c["rng"].random((len(lens), Hkv, c["cap"])).astype(np.float32)
+    out = torch.from_numpy(w).cuda()
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), weights=out, decay=0.5, check=True)
+    check_decode(c, q, o, lse, d ** -0.5, w, out, w, 0.5, what="long among short")
+    o2, lse2 = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), check=True)
+    again = torch.from_numpy(w).cuda()
+    o3, lse3 = jfa.jfa_decode_fp8(q.cuda(), *_cache(g), weights=again, decay=0.5, check=True)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3) and torch.equal(out, again)  # the same, whatever ran first
+    check_decode(c, q, o2, lse2, d ** -0.5, what="without weights")
+
+
 def test_decode_shared_pages():
     """Sequences that share a prefix's pages, and a sequence that holds a page twice."""
     c = _case(23, [64, 64, 100], 2, 64, 16, 8)

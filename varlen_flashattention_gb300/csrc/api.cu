@@ -251,7 +251,7 @@ Layout decode_layout(int64_t batch, int64_t q_heads, int64_t splits) {
 // 8-bit cache decode: findings, tile numbers, the parts' partial results and,
 // for the attention weights, the scores of every tile.
 struct Fp8DecodeLayout {
-  size_t errors = 0, tile_base = 0, part_o = 0, part_lse2 = 0, lse2 = 0, scores = 0, bytes = 0;
+  size_t errors = 0, tile_base = 0, long_list = 0, part_o = 0, part_lse2 = 0, lse2 = 0, scores = 0, bytes = 0;
 };
 Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
   Fp8DecodeLayout L;
@@ -265,6 +265,8 @@ Fp8DecodeLayout fp8_decode_layout(const jfa_decode_fp8_args& a) {
   off = align_up(off + kFp8MaxWarps + 4, 256);
   L.tile_base = off;
   off = align_up(off + 4 * (static_cast<size_t>(a.batch) + 1), 256);
+  L.long_list = off;
+  off += 4 * kFp8LongList;
   L.part_o = off;
   off = align_up(off + 4 * parts * rows * a.head_dim, 256);
   L.part_lse2 = off;
@@ -1043,6 +1045,7 @@ jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* a, void* ws, size_t ws_byte
   buf.status = reinterpret_cast<int32_t*>(w);
   buf.errors = w + L.errors;
   buf.tile_base = reinterpret_cast<int32_t*>(w + L.tile_base);
+  buf.long_list = reinterpret_cast<int32_t*>(w + L.long_list);
   buf.part_o = reinterpret_cast<float*>(w + L.part_o);
   buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);
   buf.lse2 = reinterpret_cast<float*>(w + L.lse2);

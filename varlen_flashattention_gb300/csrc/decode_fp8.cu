@@ -72,6 +72,7 @@ struct Fp8DecodeParams {
   int32_t batch, hq, group, q_len, max_pages, page_size;
   float scale_log2;
   int32_t* tile_base;  // [B + 1] 16-token tiles of the sequences before b
+  int32_t* long_list;  // how many sequences are cut into too many parts for a warp to join a row, and which
   int32_t max_parts;   // most parts of the line
   int32_t grid;        // blocks of the main kernel (four warps each)
   FastDiv by_heads;    // division by hkv
@@ -91,6 +92,7 @@ struct Fp8DecodeParams {
 constexpr int kF8Warps = 4;
 constexpr int kF8MinTiles = 1;    // fewest tiles of a part (a short sequence's time grows by 0.6 us a tile)
 constexpr int kF8ScanBatch = 512; // batches up to this number their tiles in every block
+constexpr int kF8RowParts = 62;   // parts that a warp joins a row of (two lse a lane, less two shared parts)
 // A score may pass its reference by this much before the reference moves.
 constexpr float kF8Slack = 8.f;
 // w's reference lies this far below the largest s + log2 vs when it is set.
@@ -213,13 +215,6 @@ __device__ __forceinline__ bool f8_number_tiles(const Fp8DecodeParams& p, int32_
   return __syncthreads_or(any);
 }
 
-// Large batches: one block numbers the tiles for all.
-__global__ void __launch_bounds__(1024) fp8_decode_plan_kernel(const Fp8DecodeParams p) {
-  allow_next_grid();
-  const bool bad = f8_number_tiles<1024>(p, p.tile_base);
-  if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.errors)[p.grid] = bad;
-}
-
 // The line of tiles, cut into parts of equal length.
 struct F8Line {
   int64_t total;  // tiles of all sequences
@@ -233,11 +228,35 @@ struct F8Line {
   __device__ __forceinline__ int part_of(int64_t x) const {
     return quotient(static_cast<uint64_t>((x + 1) * parts - 1), total);
   }
+  // A long sequence: of more than 62 parts (64 with what its ends share with others').
+  __device__ __forceinline__ bool is_long(int base, int end) const { return (end - base) * parts > kF8RowParts * total; }
   // n / d, in 32 bits where both fit (a 64-bit division is a hundred instructions)
   static __device__ __forceinline__ int quotient(uint64_t n, int64_t d) {
     return static_cast<int>(n >> 32 ? n / static_cast<uint64_t>(d) : static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
   }
 };
+
+// Lists the long sequences (fewer than 64: the parts are at most kFp8MaxWarps).
+static_assert(kFp8MaxWarps / kF8RowParts < kFp8LongList - 1, "the list holds them all");
+template <int THREADS>
+__device__ __forceinline__ void f8_list_long(const Fp8DecodeParams& p, const int32_t* base) {
+  __shared__ int32_t s_count;
+  if (threadIdx.x == 0) s_count = 0;
+  __syncthreads();
+  const F8Line line(base[p.batch], p.max_parts);
+  for (int b = threadIdx.x; b < p.batch; b += THREADS)
+    if (line.is_long(base[b], base[b + 1])) p.long_list[1 + atomicAdd(&s_count, 1)] = b;
+  __syncthreads();
+  if (threadIdx.x == 0) p.long_list[0] = s_count;
+}
+
+// Large batches: one block numbers the tiles for all.
+__global__ void __launch_bounds__(1024) fp8_decode_plan_kernel(const Fp8DecodeParams p) {
+  allow_next_grid();
+  const bool bad = f8_number_tiles<1024>(p, p.tile_base);
+  f8_list_long<1024>(p, p.tile_base);
+  if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.errors)[p.grid] = bad;
+}
 
 // The sequence that holds tile x, from sequence `from` on: the warp's lanes look at 32 bounds at a
 // time, first far apart, so that a batch padded with empty sequences costs little more than
@@ -275,6 +294,7 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
     if (blockIdx.x == 0) {
       for (int i = threadIdx.x; i <= p.batch; i += 128) p.tile_base[i] = s_base[i];
       if (threadIdx.x == 0) reinterpret_cast<uint32_t*>(p.errors)[p.grid] = bad;
+      f8_list_long<128>(p, s_base);
     }
     tile_base = s_base;
   } else {
@@ -709,8 +729,9 @@ __global__ void __launch_bounds__(128, F8Tile<D, NR>::kCtasPerSm) fp8_decode_ker
 // Two shapes. kWide = false: a warp per output row, for many sequences of a dozen
 // parts or so: the lanes hold the parts' lse, and the first sixteen parts' rows are
 // on their way before the lse are there (24 x 37-4k tokens of head_dim 64, 25 parts
-// a sequence: 21.1 us the call, 21.9 with eight). A sequence of more than 64 parts among
-// them has its rows joined by the block's four warps, one row after the other.
+// a sequence: 21.1 us the call, 21.9 with eight). The long sequences among them, which the
+// main kernel has listed, are joined by all blocks together, as in the other shape
+// (131k tokens and 79 x 500 of one KV head, 8 rows, with weights: 36 us, 171 us with one block a row).
 // kWide = true: a block per 32 columns of a row, its 32 groups of eight lanes
 // reading a part's 128-byte piece each, four ahead, so that a sequence cut into
 // hundreds of parts is joined by all SMs.
@@ -734,6 +755,7 @@ __device__ __forceinline__ void f8_report(const Fp8DecodeParams& p) {
 // Where the parts of an output row lie.
 struct F8Row {
   int count;         // parts; 0: the sequence is empty, 1: finished by its part
+  bool is_long;
   int step;          // rows from one part to the next
   const float* lse;  // of the first part
   const float* po;
@@ -746,6 +768,7 @@ struct F8Row {
     const F8Line line(__ldcg(p.tile_base + p.batch), p.max_parts);
     const int i0 = end > base ? line.part_of(base) : 0;
     count = end > base ? line.part_of(end - 1) - i0 + 1 : 0;
+    is_long = line.is_long(base, end);
     const int64_t first = ((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r;
     step = hkv * nrows;
     lse = p.part_lse2 + first;
@@ -762,31 +785,106 @@ __device__ __forceinline__ void f8_write_lse(const Fp8DecodeParams& p, const F8R
   if (p.w_out) p.lse2[row.w] = f8_weight_lse(lse2);
 }
 
-template <int D, int kAtOnce>
-__device__ __forceinline__ void join_rows(const Fp8DecodeParams& p, int block) {
-  constexpr int kPer = D / 32, kWarps = 4;  // output columns of a lane
-  __shared__ float s_m[kWarps], s_z[kWarps], s_o[kWarps][D];
+// 32 columns of a row by a block of threads.
+template <int D, int THREADS>
+__device__ __forceinline__ void join_slice(const Fp8DecodeParams& p, const F8Row& row, int slice) {
+  constexpr int kWarps = THREADS / 32, kGroups = THREADS / 8;
+  __shared__ float s_f[kFp8MaxWarps];
+  __shared__ float s_red[2][kWarps];
+  __shared__ float s_o[kWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = p.batch * p.c.hkv * p.group * p.q_len;
-  const int mine = block * kWarps + warp;
-  auto load = [&](const F8Row& row, int i, float (&v)[kPer]) {
-    const float* src = row.po + static_cast<int64_t>(i) * row.step * D;
-    if constexpr (kPer == 4) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-      const float2 a = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-      v[0] = a.x, v[1] = a.y;
-    }
+  const int group = threadIdx.x >> 3, sub = threadIdx.x & 7;
+  const int count = row.count, step = row.step;
+  const float *lse = row.lse, *po = row.po + 32 * slice;
+  auto load = [&](int i) {
+    return i < count ? __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * step * D) + sub)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
   };
+  float4 v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = load(group + kGroups * k);
+  float m = -INFINITY;
+  for (int i = threadIdx.x; i < count; i += THREADS) {
+    const float y = __ldcg(lse + static_cast<int64_t>(i) * step);
+    s_f[i] = y;
+    m = fmaxf(m, y);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) s_red[0][warp] = m;
+  __syncthreads();
+  float top = s_red[0][0];  // the largest lse (0 if every part is empty or NaN)
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_red[0][w]);
+  if (top == -INFINITY) top = 0.f;
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < count; i += THREADS) {
+    const float f = ptx::ex2(s_f[i] - top);
+    s_f[i] = f;
+    sum += f;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) s_red[1][warp] = sum;
+  __syncthreads();
+  float z = 0.f;  // sum of 2^(lse - top)
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) z += s_red[1][w];
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = group; i < count; i += 4 * kGroups) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = i + kGroups * k < count ? s_f[i + kGroups * k] : 0.f;
+      o.x += f * v[k].x;
+      o.y += f * v[k].y;
+      o.z += f * v[k].z;
+      o.w += f * v[k].w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = load(i + kGroups * (4 + k));
+  }
+#pragma unroll
+  for (int off = 8; off < 32; off <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+  }
+  if (lane < 8) *reinterpret_cast<float4*>(&s_o[warp][4 * sub]) = o;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) y += s_o[w][lane];
+    p.o[row.out * D + 32 * slice + lane] = __float2bfloat16(z == 0.f ? 0.f : y / z);
+    if (lane == 0 && slice == 0) f8_write_lse(p, row, top, z);
+  }
+}
+
+// A warp per row (`blocks` blocks of four, this one is `block`); the rows of long sequences by slices.
+template <int D, int kAtOnce>
+__device__ __forceinline__ void join_rows(const Fp8DecodeParams& p, int block, int blocks) {
+  constexpr int kPer = D / 32;  // output columns of a lane
+  const int lane = threadIdx.x & 31;
+  const int seq_rows = p.c.hkv * p.group * p.q_len, rows = p.batch * seq_rows;
+  const int mine = block * 4 + static_cast<int>(threadIdx.x >> 5);
+  const int many = __ldcg(p.long_list);
   const F8Row row(p, min(mine, rows - 1), D);
-  const bool is_long = __syncthreads_or(row.count > 64);
-  if (!is_long) {
-    if (mine >= rows || row.count == 1) return;
+  if (mine < rows && row.count != 1 && !row.is_long) {
+    auto load = [&](int i, float (&v)[kPer]) {
+      const float* src = row.po + static_cast<int64_t>(i) * row.step * D;
+      if constexpr (kPer == 4) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      } else {
+        const float2 a = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+        v[0] = a.x, v[1] = a.y;
+      }
+    };
     float v[kAtOnce][kPer], o[kPer];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k)
-      if (k < row.count) load(row, k, v[k]);
+      if (k < row.count) load(k, v[k]);
     float y[2];  // lane l: parts l and l + 32
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -811,7 +909,7 @@ __device__ __forceinline__ void join_rows(const Fp8DecodeParams& p, int block) {
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
-        if (i + kAtOnce + k < row.count) load(row, i + kAtOnce + k, v[k]);
+        if (i + kAtOnce + k < row.count) load(i + kAtOnce + k, v[k]);
     }
     const float inv = z == 0.f ? 0.f : 1.f / z;
     if constexpr (kPer == 4)
@@ -820,57 +918,14 @@ __device__ __forceinline__ void join_rows(const Fp8DecodeParams& p, int block) {
     else
       reinterpret_cast<uint32_t*>(p.o + row.out * D)[lane] = ptx::pack_bf16(o[0] * inv, o[1] * inv);
     if (lane == 0) f8_write_lse(p, row, m, z);
-    return;
   }
-  for (int j = 0; j < kWarps; ++j) {
-    const int job = block * kWarps + j;
-    if (job >= rows) return;
-    const F8Row r(p, job, D);
-    if (r.count == 1) continue;
-    const int lo = r.count * warp / kWarps, hi = r.count * (warp + 1) / kWarps;
-    float o[kPer], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-    for (int i = lo + lane; i < hi; i += 32) m = fmaxf(m, __ldcg(r.lse + static_cast<int64_t>(i) * r.step));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (m == -INFINITY) m = 0.f;
-    for (int i = lo; i < hi; i += 8) {
-      float f[8], v[8][kPer];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] = i + k < hi ? ptx::ex2(__ldcg(r.lse + static_cast<int64_t>(i + k) * r.step) - m) : 0.f;
-        if (i + k < hi) load(r, i + k, v[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (i + k >= hi) break;
-        sum += f[k];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += f[k] * v[k][e];
-      }
+  const int items = seq_rows * (D / 32);
+  for (int j = 0; j < many; ++j) {
+    const int b = __ldcg(p.long_list + 1 + j);
+    for (int item = block; item < items; item += blocks) {
+      __syncthreads();  // the last slice is done with
+      join_slice<D, 128>(p, F8Row(p, b * seq_rows + item / (D / 32), D), item % (D / 32));
     }
-    if (lane == 0) {
-      s_m[warp] = sum == 0.f ? -INFINITY : m;  // nothing in it: counts for nothing
-      s_z[warp] = sum;
-    }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = o[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-      if (top == -INFINITY) top = 0.f;
-      float z = 0.f, y = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ptx::ex2(s_m[w] - top);
-        z += s_z[w] * f;
-        y += s_o[w][threadIdx.x] * f;
-      }
-      p.o[r.out * D + threadIdx.x] = __float2bfloat16(z == 0.f ? 0.f : y / z);
-      if (threadIdx.x == 0) f8_write_lse(p, r, top, z);
-    }
-    __syncthreads();
   }
 }
 
@@ -881,92 +936,12 @@ __global__ void __launch_bounds__(kWide ? kF8WideThreads : 128) fp8_decode_join_
   allow_next_grid();
   if (blockIdx.x == gridDim.x - 1) {
     f8_report<kWide ? kF8WideThreads : 128>(p);
-    return;
+  } else if constexpr (kWide) {
+    const F8Row row(p, static_cast<int>(blockIdx.x / (D / 32)), D);
+    if (row.count != 1) join_slice<D, kF8WideThreads>(p, row, static_cast<int>(blockIdx.x % (D / 32)));
+  } else {
+    join_rows<D, 16>(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x) - 1);
   }
-  if constexpr (!kWide) {
-    join_rows<D, 16>(p, static_cast<int>(blockIdx.x));
-    return;
-  }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slice = static_cast<int>(blockIdx.x % (D / 32));
-  const F8Row row(p, static_cast<int>(blockIdx.x / (D / 32)), D);
-  const int count = row.count, step = row.step;
-  if (count == 1) return;
-  const float *lse = row.lse, *po = row.po + 32 * slice;
-  float top, z;  // largest lse and sum of 2^(lse - top) (top: 0 if every part is empty or NaN)
-
-  {
-    __shared__ float s_f[kFp8MaxWarps];
-    __shared__ float s_red[2][8];
-    __shared__ float s_o[8][32];
-    const int group = threadIdx.x >> 3, sub = threadIdx.x & 7;
-    float4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = group + 32 * k;
-      v[k] = i < count ? __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * step * D) + sub)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < count; i += kF8WideThreads) {
-      const float y = __ldcg(lse + static_cast<int64_t>(i) * step);
-      s_f[i] = y;
-      m = fmaxf(m, y);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) s_red[0][warp] = m;
-    __syncthreads();
-    top = s_red[0][0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_red[0][w]);
-    if (top == -INFINITY) top = 0.f;
-    float sum = 0.f;
-    for (int i = threadIdx.x; i < count; i += kF8WideThreads) {
-      const float f = ptx::ex2(s_f[i] - top);
-      s_f[i] = f;
-      sum += f;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) s_red[1][warp] = sum;
-    __syncthreads();
-    z = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) z += s_red[1][w];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = group; i < count; i += 128) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = i + 32 * k < count ? s_f[i + 32 * k] : 0.f;
-        o.x += f * v[k].x;
-        o.y += f * v[k].y;
-        o.z += f * v[k].z;
-        o.w += f * v[k].w;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = i + 128 + 32 * k;
-        v[k] = j < count ? __ldcg(reinterpret_cast<const float4*>(po + static_cast<int64_t>(j) * step * D) + sub)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-#pragma unroll
-    for (int off = 8; off < 32; off <<= 1) {
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
-      o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
-      o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
-    }
-    if (lane < 8) *reinterpret_cast<float4*>(&s_o[warp][4 * sub]) = o;
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
-    float y = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) y += s_o[w][lane];
-    p.o[row.out * D + 32 * slice + lane] = __float2bfloat16(z == 0.f ? 0.f : y / z);
-  }
-  if (threadIdx.x == 0 && slice == 0) f8_write_lse(p, row, top, z);
 }
 
 // The rows' lse of a sequence and head, joined from its parts once more (the join's own may not be
@@ -982,19 +957,19 @@ __device__ __forceinline__ void f8_join_lse(const Fp8DecodeParams& p, int b, int
   } else {
     const float* lse = p.part_lse2 + ((static_cast<int64_t>(i0) + b) * hkv + h) * nrows + r;
     const int64_t step = static_cast<int64_t>(hkv) * nrows;
-    constexpr int kStride = 32 / kRows;
+    constexpr int kStride = 32 / kRows, kLoads = kRows < 4 ? kRows : 4;  // parts a round: kStride * kLoads
     float m = kF8NoRef, sum = 0.f;
-    for (int i = lane / kRows; i < count; i += 4 * kStride) {
-      float x[4], top = m;
+    for (int i = lane / kRows; i < count; i += kStride * kLoads) {
+      float x[kLoads], top = m;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kLoads; ++k) {
         x[k] = i + k * kStride < count && r < nrows ? __ldcg(lse + (i + k * kStride) * step) : -INFINITY;
         top = fmaxf(top, x[k]);
       }
       sum *= ptx::ex2(m - top);
       m = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum += ptx::ex2(x[k] - m);
+      for (int k = 0; k < kLoads; ++k) sum += ptx::ex2(x[k] - m);
     }
 #pragma unroll
     for (int off = kRows; off < 32; off <<= 1) {
@@ -1065,7 +1040,7 @@ __device__ __forceinline__ void add_weights(const Fp8DecodeParams& p, int max_pa
   }
 }
 
-// The weights by themselves, behind the wide join.
+// The weights by themselves, behind the join.
 constexpr int kF8WeightWarps = 8;
 template <int kAhead, int kRows>
 __global__ void __launch_bounds__(32 * kF8WeightWarps) fp8_decode_weights_kernel(const Fp8DecodeParams p, int max_parts) {
@@ -1086,7 +1061,7 @@ __global__ void __launch_bounds__(128) fp8_decode_finish_kernel(const Fp8DecodeP
   else if (blockIdx.x == gridDim.x - 1)
     f8_report<128>(p);
   else
-    join_rows<D, 8>(p, block - blocks);
+    join_rows<D, 8>(p, block - blocks, static_cast<int>(gridDim.x) - 1 - blocks);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -1136,19 +1111,23 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
   // parts a sequence has on average: past 32, the wide join (with 25, 24 x 37-4k tokens take 26 us against 21)
   const uint32_t rows = static_cast<uint32_t>(p.batch) * p.c.hkv * nrows, join_blocks = (rows + 3) / 4 + 1;
   const bool wide = p.max_parts > 32 * p.batch;
-  if (!w)
+  auto join = [&] {
     return wide ? launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p)
                 : launch_after(fp8_decode_join_kernel<D, false>, dim3(join_blocks), dim3(128), 0, stream, p);
-  const int weight_warps = wide ? sms * 4 * kF8WeightWarps : sms * 5 * 4;
+  };
+  if (!w) return join();
+  // The weights beside the join read a sequence's parts again in every warp: not where there can be thousands.
+  const bool beside = !wide && p.max_parts <= 640;
+  const int weight_warps = beside ? sms * 5 * 4 : sms * 4 * kF8WeightWarps;
   const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(weight_warps / p.c.hkv, tiles)));
-  if (!wide) {
+  if (beside) {
     const int blocks = weight_warps / 4;  // five of the six blocks that fit an SM: the join runs beside them
     const dim3 g(blocks + join_blocks), block(128);
     if (nrows <= 4) return launch_after(fp8_decode_finish_kernel<D, 4, 4>, g, block, 0, stream, p, parts, blocks);
     if (nrows <= 8) return launch_after(fp8_decode_finish_kernel<D, 2, 8>, g, block, 0, stream, p, parts, blocks);
     return launch_after(fp8_decode_finish_kernel<D, 1, 16>, g, block, 0, stream, p, parts, blocks);
   }
-  e = launch_after(fp8_decode_join_kernel<D, true>, dim3(rows * (D / 32) + 1), dim3(kF8WideThreads), 0, stream, p);
+  e = join();
   if (e != cudaSuccess) return e;
   const dim3 g(sms * 4), block(32 * kF8WeightWarps);
   if (nrows <= 4) return launch_after(fp8_decode_weights_kernel<4, 4>, g, block, 0, stream, p, parts);
@@ -1177,6 +1156,7 @@ cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffe
   p.page_size = a.page_size;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.tile_base = w.tile_base;
+  p.long_list = w.long_list;
   p.errors = w.errors;
   p.part_o = w.part_o;
   p.part_lse2 = w.part_lse2;

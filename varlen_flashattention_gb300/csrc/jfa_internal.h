@@ -231,10 +231,12 @@ cudaError_t launch_decode_general(const DecodeLaunch& a, float* part_o, float* p
                                   cudaStream_t stream);
 // 8-bit paged cache: decode, append, evict.
 constexpr int kFp8MaxWarps = 2560;  // most warps of the decode's main kernel
+constexpr int kFp8LongList = 64;    // a count, and sequences of more parts than a warp joins
 struct Fp8DecodeBuffers {
   int32_t* status;
   uint8_t* errors;     // [kFp8MaxWarps + 4]
   int32_t* tile_base;  // [B + 1]
+  int32_t* long_list;  // [kFp8LongList]
   float* part_o;       // [parts + B][kv_heads][rows][D]
   float* part_lse2;    // [parts + B][kv_heads][rows]
   float* lse2;         // [B * kv_heads][rows] (weights only)
