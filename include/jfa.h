@@ -377,8 +377,8 @@ typedef struct {
  * the maximum over the finite new values; the block's scale becomes need, or, if
  * it holds older tokens, s' = max(its scale s, need), their codes being rewritten
  * as e4m3(e4m3(code) * s / s') where s' > s. New codes are e4m3(x / scale),
- * rounded to nearest even; infinities and NaN become NaN. Sequences of one call
- * must not share a block that receives tokens. If weights is set, the entries
+ * rounded to nearest even; infinities and NaN become NaN. A block that receives
+ * tokens must belong to one sequence, once. If weights is set, the entries
  * at the new positions become 0. */
 typedef struct {
   const void* k;              /* bf16 [total_new, kv_heads, head_dim] */
