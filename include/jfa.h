@@ -409,7 +409,8 @@ typedef struct {
  * (the first term is left out if weights is NULL); entries past L_b are not
  * written. weights and weights_out may be the same array. The workspace then
  * holds a score of 4 bytes per query row and slot of the page table. Codes that are
- * NaN make NaN of the rows that see them, and of no others. */
+ * NaN make NaN of the rows that see them, and of no others; a row that is NaN makes
+ * NaN of the weights of the tokens it sees, and of no others. */
 typedef struct {
   const void* q;              /* bf16 [batch, q_len, q_heads, head_dim] */
   const void* k_cache;        /* e4m3 [num_pages, page_size, kv_heads, head_dim] */

@@ -1005,7 +1005,7 @@ __device__ __forceinline__ void add_weights(const Fp8DecodeParams& p, int max_pa
       if (p.tile_base[b + 1] <= x) b = f8_next_sequence(p.tile_base, p.batch, x, b);
       bool bad;
       const int base = p.tile_base[b], stop = min(p.tile_base[b + 1], x1);
-      const int end = min(f8_length(p, b, &bad), (stop - base) * 16);  // tokens of this part of the sequence
+      const int L = f8_length(p, b, &bad), end = min(L, (stop - base) * 16);  // tokens of this part of the sequence
       const int64_t seg = static_cast<int64_t>(b) * hkv + h;
       float z[kRows];
       if constexpr (kJoined) {
@@ -1030,8 +1030,10 @@ __device__ __forceinline__ void add_weights(const Fp8DecodeParams& p, int max_pa
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           sum[k] *= p.decay;
+          // The first `hidden` rows do not see this token: they add nothing, a NaN lse of theirs neither.
+          const int hidden = max(t + 32 * k - (L - p.q_len), 0) * p.group;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) sum[k] += ptx::ex2(v[k][r] - z[r]);
+          for (int r = 0; r < kRows; ++r) sum[k] += r < hidden ? 0.f : ptx::ex2(v[k][r] - z[r]);
           if (t + 32 * k < end) out[t + 32 * k] = sum[k];
         }
       }
