@@ -10,7 +10,7 @@ import torch
 import varlen_flashattention_gb300 as jfa
 from oracle import kv_cache as kvo
 from tests.parity import np64
-from tests.test_gpu_fp8_cache import _bf16, _cache, _case, _gpu
+from tests.test_gpu_fp8_cache import _bf16, _cache, _case, _gpu, _same_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,109 @@ def test_weights_of_tokens_that_a_nan_row_does_not_see(lens, G, ql, what):
         assert (got[b, :, L:] == -7.0).all()
     if what != "key":  # the newest token is seen by the last query token alone
         assert not np.isnan(got[0, 0, lens[0] - 1]) and np.isnan(got[0, 0, :lens[0] - ql + 1]).all()
+
+
+# ------------------------------------------------------------------ one rounding
+
+def _tie_scales(values):
+    """Pairs of one of `values` and a scale whose product is next to the middle of two e4m3 values, nearer
+    than fp32 can tell: rounded to fp32 it is the middle."""
+    mid = (kvo.E4M3[8:126] + kvo.E4M3[9:127]) / 2
+    mid = mid[(mid > 1) & (mid < 4)]
+    x, t = (a.ravel() for a in np.meshgrid(np.asarray(values, dtype=np.float64), mid))
+    s = (t / x).astype(np.float32)
+    p = x * s.astype(np.float64)
+    good = (p != t) & (p.astype(np.float32) == t.astype(np.float32)) & (s < 2)
+    assert good.sum() > 20
+    return x[good], s[good]
+
+
+def _tie_cache(c, rng, block):
+    """Codes and scales of the cache replaced by ones whose values lie next to e4m3's middles."""
+    x, s = _tie_scales(kvo.E4M3[56:64])
+    code = {float(v): i for i, v in enumerate(kvo.E4M3)}
+    codes = np.array([code[float(v)] for v in x], dtype=np.uint8)
+    for n, sc in (("kc", "ks"), ("vc", "vs")):
+        pick = rng.integers(0, len(s), c[sc].shape)
+        c[sc][:] = s[pick]
+        hit = np.repeat(codes[pick], block, 1)[..., None] | (rng.integers(0, 2, c[n].shape).astype(np.uint8) << 7)
+        low = rng.integers(0, 80, c[n].shape).astype(np.uint8)
+        c[n][:] = np.where(rng.random(c[n].shape) < 0.5, hit, low)
+
+
+def _evict_equals(c, keep, first=0, recent=0, what=""):
+    lens, P = c["lens"], c["P"]
+    B, width = len(lens), -(-keep // P)
+    w = c["rng"].random((B, c["H"], c["cap"])).astype(np.float32)
+    new = np.full((B, width), -1, dtype=np.int32)
+    at = 0
+    for b, L in enumerate(lens):
+        n = -(-min(int(L), keep) // P)
+        new[b, :n] = c["free"][at:at + n]
+        at += n
+    g = _gpu(c)
+    kept, nl, nw = jfa.jfa_cache_evict_fp8(*_cache(g), torch.from_numpy(w).cuda(), keep, torch.from_numpy(new).cuda(),
+                                           first=first, recent=recent, check=True)
+    k2, l2, w2 = kvo.evict(c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, w, keep, new, first, recent)
+    assert (kept.cpu().numpy() == k2).all() and (nl.cpu().numpy() == l2).all() and (nw.cpu().numpy() == w2).all()
+    for x in ("ks", "vs"):
+        assert (g[x].cpu().numpy() == c[x]).all(), f"{what}: {x}"
+    for x in ("kc", "vc"):
+        assert _same_codes(g[x].cpu().numpy(), c[x]), f"{what}: {x}"
+
+
+LAYOUTS = [(128, 16, 16), (64, 16, 8), (128, 1, 1), (64, 24, 8), (128, 128, 64)]
+
+
+@pytest.mark.parametrize("d,P,block", LAYOUTS)
+def test_evict_rounds_once(d, P, block):
+    """Values a hair from the middle of two e4m3 values at the new scale go to the nearer one."""
+    c = _case(42, [300, 40, 7, 129], 2, d, P, block, spare=300)
+    _tie_cache(c, c["rng"], block)
+    _evict_equals(c, 90, 2, 5)
+
+
+def _append_equals(c, old, new, k, v):
+    lens = [a + b for a, b in zip(old, new)]
+    assert list(c["lens"]) == lens
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    g = _gpu(c)
+    jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.from_numpy(offs).cuda(), max(new), check=True)
+    kvo.append(np64(k), np64(v), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, offs)
+    for x in ("ks", "vs"):
+        assert (g[x].cpu().numpy() == c[x]).all(), x
+    for x in ("kc", "vc"):
+        assert _same_codes(g[x].cpu().numpy(), c[x]), x
+
+
+# a warp a scale block with 16 or 32 rows, and chunks
+GROWN = [(128, 16, 16, [5, 1, 15, 8, 20], [1, 2, 1, 3, 5]), (64, 32, 32, [5, 1, 31, 8, 40], [20, 21, 1, 30, 22]),
+         (128, 128, 128, [5, 100, 127, 64, 200], [60, 1, 1, 300, 40]), (64, 24, 8, [3, 1, 7, 12, 20], [40, 1, 1, 2, 30])]
+
+
+@pytest.mark.parametrize("d,P,block,old,new", GROWN)
+@pytest.mark.parametrize("growth", [2.0, 4.0])
+def test_append_rewrites_older_codes_with_one_rounding(d, P, block, old, new, growth):
+    """Older codes under a scale that is no power of two and grows two- to eightfold."""
+    c = _case(45, [a + b for a, b in zip(old, new)], 3, d, P, block)
+    _tie_cache(c, c["rng"], block)
+    n = sum(new)
+    k, v = (_bf16(c["rng"], n, 3, d) for _ in range(2))
+    at = 0
+    for m in new:  # every sequence's first new token sets the scale
+        k[at, :, 0] = v[at, :, d - 1] = 448 * growth
+        at += m
+    _append_equals(c, old, new, k, v)
+
+
+@pytest.mark.parametrize("d,P,block,old,new", GROWN)
+@pytest.mark.parametrize("odd", [1.0, 1.5])
+def test_append_rewrites_the_largest_older_codes(d, P, block, old, new, odd):
+    """Older values at the end of bf16's range, under scales of 2^118 to 1.5 * 2^119 that grow to 2^120."""
+    c = _case(46, [a + b for a, b in zip(old, new)], 2, d, P, block)
+    for x in ("ks", "vs"):
+        c[x][:] = np.float32(odd) * np.exp2(c["rng"].integers(118, 120, c[x].shape)).astype(np.float32)
+    n = sum(new)
+    k, v = (_bf16(c["rng"], n, 2, d) for _ in range(2))
+    k[:, :, 1] = v[:, :, 2] = 3.38e38
+    _append_equals(c, old, new, k, v)

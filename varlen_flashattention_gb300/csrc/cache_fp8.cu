@@ -67,22 +67,32 @@ __device__ __noinline__ uint2 encode8(const float* x, float s) {
   return make_uint2(r[0], r[1]);
 }
 
-// Eight codes from the scale `from` to the scale `to`.
+// Eight codes from the scale `from` to the scale `to`, a power of two, with one
+// rounding: the ratio of the scales is exact, and its product with a code, 4 by 24
+// bits, is cut to 24 with its last bit set where anything was cut ("round to odd"),
+// which the rounding to 4 bits cannot mistake for a tie. Out of line like encode8.
 __device__ __noinline__ uint2 recode8(uint2 codes, float from, float to) {
-  float x[8];
+  // Above 2^20 there are no codes but 0 (the others would pass 448); below 2^-40 nothing is left of any.
+  const uint32_t u = __float_as_uint(from);
+  const int e = static_cast<int>(u >> 23) - static_cast<int>(__float_as_uint(to) >> 23);
+  const float ratio = __uint_as_float((static_cast<uint32_t>(min(max(e, -40), 20) + 127) << 23) | (u & 0x7FFFFFu));
   const uint32_t w[2] = {codes.x, codes.y};
+  uint32_t r[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t lo, hi;
     e4m3x4_to_f16(w[i], lo, hi);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    x[4 * i] = a.x * from;
-    x[4 * i + 1] = a.y * from;
-    x[4 * i + 2] = b.x * from;
-    x[4 * i + 3] = b.y * from;
+    float x[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float y = __fmul_rz(x[k], ratio);
+      x[k] = __uint_as_float(__float_as_uint(y) | (fmaf(x[k], ratio, -y) != 0.f ? 1u : 0u));
+    }
+    r[i] = f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16);
   }
-  return encode8(x, to);
+  return make_uint2(r[0], r[1]);
 }
 
 // Eight finite bf16 values divided by a power of two (inv: its inverse). The
