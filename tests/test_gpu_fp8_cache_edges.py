@@ -157,3 +157,32 @@ def test_append_rewrites_the_largest_older_codes(d, P, block, old, new, odd):
     k, v = (_bf16(c["rng"], n, 2, d) for _ in range(2))
     k[:, :, 1] = v[:, :, 2] = 3.38e38
     _append_equals(c, old, new, k, v)
+
+
+@pytest.mark.parametrize("d,P,block,old,new", GROWN)
+def test_append_new_codes_with_one_rounding(d, P, block, old, new):
+    """New values whose quotient by an older scale, no power of two, is a hair from the middle of two codes."""
+    c = _case(47, [a + b for a, b in zip(old, new)], 3, d, P, block)
+    rng = c["rng"]
+    values = (1 + np.arange(128) / 128.0)[3::7]  # bf16
+    mid = (kvo.E4M3[8:126] + kvo.E4M3[9:127]) / 2
+    mid = mid[(mid > 1) & (mid < 4)]
+    x, t = (a.ravel() for a in np.meshgrid(values, mid))
+    s = (x / t).astype(np.float32)
+    y = x / s.astype(np.float64)
+    good = (y != t) & ((x.astype(np.float32) / s) == t.astype(np.float32))
+    x, s = x[good], s[good]
+    assert len(x) > 100
+    n, H = sum(new), 3
+    k, v = (torch.zeros(n, H, d) for _ in range(2))
+    for y, sc in ((k, "ks"), (v, "vs")):
+        at = 0
+        for b, m in enumerate(new):
+            f = old[b]
+            page, cell = c["table"][b, f // P], f % P // block
+            for h in range(H):
+                i = rng.integers(0, len(x))
+                c[sc][page, cell, h] = s[i]
+                y[at:at + m, h] = torch.from_numpy(x[i] * rng.choice([1.0, -1.0, 0.5, 2.0, 64.0], (m, d))).float()
+            at += m
+    _append_equals(c, old, new, k.to(torch.bfloat16), v.to(torch.bfloat16))

@@ -52,17 +52,27 @@ struct Fp8AppendParams {
 
 __device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0; }
 
-// e4m3 codes of eight values divided by s, the rounded quotient whatever s is.
-// (Kept out of line, like recode8: the usual paths below must stay small, the
-// kernels were losing time to instruction fetches with these inlined.)
+// e4m3 codes of eight values divided by s, the quotient rounded once whatever s is:
+// it is cut to fp32 with its last bit set where the division leaves a remainder, which
+// fmaf gives exactly ("round to odd"), and then rounded to 4 bits. (Kept out of line,
+// like recode8: the usual paths below must stay small, the kernels were losing time to
+// instruction fetches with these inlined.)
 __device__ __noinline__ uint2 encode8(const float* x, float s) {
+  const uint32_t u = __float_as_uint(s);
+  const int e = 127 - static_cast<int>(u >> 23);
+  const float m = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);  // s = m 2^-e, 1 <= m < 2
   uint32_t r[2] = {0, 0};
 #pragma unroll 1
   for (int i = 0; i < 8; i += 2) {
-    // infinities and NaN become NaN
-    const float a = fabsf(x[i]) < INFINITY ? __fdiv_rn(x[i], s) : __int_as_float(0x7fffffff);
-    const float b = fabsf(x[i + 1]) < INFINITY ? __fdiv_rn(x[i + 1], s) : __int_as_float(0x7fffffff);
-    r[i >> 2] |= f32x2_to_e4m3x2(a, b) << (8 * (i & 2));
+    float q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float y = scalbnf(x[i + k], e);  // exact but for numbers far below e4m3's smallest
+      const float z = __fdiv_rz(y, m);
+      const uint32_t odd = __float_as_uint(z) | (fmaf(-z, m, y) != 0.f ? 1u : 0u);
+      q[k] = fabsf(x[i + k]) < INFINITY ? __uint_as_float(odd) : __int_as_float(0x7fffffff);  // infinities and NaN become NaN
+    }
+    r[i >> 2] |= f32x2_to_e4m3x2(q[0], q[1]) << (8 * (i & 2));
   }
   return make_uint2(r[0], r[1]);
 }
