@@ -365,8 +365,8 @@ typedef struct {
  * block_size is 1, 2, 4, ..., 128 and divides page_size (1 = a scale per token);
  * num_pages * page_size < 2^31. Token t of sequence b lives in page
  * page_table[b][t / page_size], slot t % page_size. Scales must be positive
- * normal numbers; those that jfa_cache_append_fp8 and jfa_cache_evict_fp8 write are powers of
- * two. head_dim is 64 or 128. Slots of a page past a sequence's length are never
+ * normal numbers up to 2^127; those that jfa_cache_append_fp8 and
+ * jfa_cache_evict_fp8 write are powers of two. head_dim is 64 or 128. Slots of a page past a sequence's length are never
  * read and, but for codes of a block whose scale changes, never written.
  *
  * jfa_cache_append_fp8: the new tokens' K and V, packed by offsets, become the

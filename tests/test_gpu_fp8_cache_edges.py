@@ -113,6 +113,19 @@ def test_evict_rounds_once(d, P, block):
     _evict_equals(c, 90, 2, 5)
 
 
+@pytest.mark.parametrize("e", [118, 119, 120, 121, 127])
+@pytest.mark.parametrize("odd", [False, True])
+def test_evict_largest_scales(e, odd):
+    """Values past fp32's largest number, which a code and its scale can hold, keep their size."""
+    c = _case(44, [100, 33], 2, 64, 16, 8, spare=30)
+    rng = c["rng"]
+    for sc in ("ks", "vs"):
+        c[sc][:] = 2.0 ** rng.integers(e - 3, e + 1, c[sc].shape)
+        if odd:
+            c[sc] *= rng.uniform(0.5, 1.0, c[sc].shape).astype(np.float32)
+    _evict_equals(c, 40, 2, 5)
+
+
 def _append_equals(c, old, new, k, v):
     lens = [a + b for a, b in zip(old, new)]
     assert list(c["lens"]) == lens

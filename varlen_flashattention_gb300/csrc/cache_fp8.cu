@@ -1029,14 +1029,15 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_evict_move_kernel(const Fp8Ev
         float a = __half2float(__hmax(__low2half(top), __high2half(top)));
 #pragma unroll
         for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-        if (sub == 0)
-          atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(fminf(a * sc[v][k], 3.4028234e38f)));
+        // in units of 2^8, which keeps values past fp32's range (a scale of 2^127 holds 448 * 2^127), rounded up:
+        // never past 1.75 times a power of two, the border of e4m3_block_scale_from_256th
+        if (sub == 0) atomicMax(&s_amax[v][(k * kRowsPerPass + r0) >> bs], __float_as_uint(__fmul_ru(a * 0x1p-8f, sc[v][k])));
       }
     }
     __syncthreads();
     if (tid < 2 * blocks) {
       const int v = tid >= blocks, i = tid - v * blocks;
-      const float s = e4m3_block_scale(__uint_as_float(s_amax[v][i]));
+      const float s = e4m3_block_scale_from_256th(__uint_as_float(s_amax[v][i]));
       s_new[v][i] = s;
       const int dst = s_dst[buf][i << bs];
       if (dst >= 0) scales[v][static_cast<int64_t>(dst >> bs) * hkv] = s;

@@ -11,7 +11,7 @@
 // of two costs no precision against amax / 448 (only up to one binade of its
 // 18-binade range), dividing by it is exact, and codes move from one scale to
 // another unchanged unless they fall into the subnormals. Readers take any
-// positive scale.
+// positive normal scale up to 2^127.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -73,12 +73,14 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 }
 
 // The smallest power of two s >= 2^-126 with amax / s <= 448 = 1.75 * 2^8, for
-// finite amax >= 0: amax = (1 + f) 2^e takes 2^(e - 8), one more if 1 + f > 1.75.
-__device__ __forceinline__ float e4m3_block_scale(float amax) {
+// finite amax >= 0: amax / 2^8 = (1 + f) 2^e takes 2^e, one more if 1 + f > 1.75. (What
+// is below 2^-126 there, where a division may round, takes 2^-126.)
+__device__ __forceinline__ float e4m3_block_scale_from_256th(float amax) {
   const uint32_t u = __float_as_uint(amax);
-  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
 }
+__device__ __forceinline__ float e4m3_block_scale(float amax) { return e4m3_block_scale_from_256th(amax * 0x1p-8f); }
 
 // Any e4m3 NaN (0x7F or 0xFF) among four codes.
 __device__ __forceinline__ bool e4m3_any_nan(uint32_t codes) {
