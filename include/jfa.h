@@ -379,7 +379,8 @@ typedef struct {
  * as e4m3(e4m3(code) * s / s') where s' > s. New codes are e4m3(x / scale),
  * rounded to nearest even; infinities and NaN become NaN. A block that receives
  * tokens must belong to one sequence, once. If weights is set, the entries
- * at the new positions become 0. */
+ * at the new positions become 0. (total_new / 128 + 2 batch) x kv_heads must be
+ * below 2^29; max_new may be any bound. */
 typedef struct {
   const void* k;              /* bf16 [total_new, kv_heads, head_dim] */
   const void* v;              /* bf16 [total_new, kv_heads, head_dim] */

@@ -194,6 +194,17 @@ def test_append_and_evict_arguments_are_refused(lib):
             _abi.JFA_ERR_INVALID_ARG, bad
 
 
+def test_append_takes_any_bound_on_new_tokens(lib):
+    """max_new, a bound, does not decide what is refused; an empty workspace ends the calls before any CUDA work."""
+    call = lib.jfa_cache_append_fp8
+    for good in (dict(max_new=2 ** 31 - 1), dict(batch=16384, kv_heads=64, total_new=16383 + 131072, max_new=131072),
+                 dict(batch=1 << 20, kv_heads=128, total_new=1 << 20, max_new=1 << 20)):
+        assert call(ctypes.byref(_append_args(**good)), FAKE, 0, None) == _abi.JFA_ERR_WORKSPACE_TOO_SMALL, good
+    for bad in (dict(batch=1 << 25, max_new=1), dict(batch=1 << 20, kv_heads=256, total_new=1 << 20),
+                dict(kv_heads=32767, total_new=2 ** 31 - 1, max_new=2 ** 31 - 1)):
+        assert call(ctypes.byref(_append_args(**bad)), FAKE, 0, None) == _abi.JFA_ERR_INVALID_ARG, bad
+
+
 # ------------------------------------------------------------------ the binding
 
 def _t(B=3, P=16, block=8, H=2, d=64, pages=10, mp=4):

@@ -199,3 +199,23 @@ def test_append_new_codes_with_one_rounding(d, P, block, old, new):
                 y[at:at + m, h] = torch.from_numpy(x[i] * rng.choice([1.0, -1.0, 0.5, 2.0, 64.0], (m, d))).float()
             at += m
     _append_equals(c, old, new, k.to(torch.bfloat16), v.to(torch.bfloat16))
+
+
+# ------------------------------------------------------------------ sizes
+
+@pytest.mark.parametrize("B,H,block", [(40, 2, 16), (40, 2, 8), (3, 40, 128)])
+def test_append_with_a_loose_bound_on_new_tokens(B, H, block):
+    """max_new is a bound: one that is far above every sequence's count changes nothing."""
+    rng = np.random.default_rng(48)
+    old, new = rng.integers(0, 40, B), rng.integers(0, 30, B)
+    lens = [int(a + b) for a, b in zip(old, new)]
+    c = _case(48, lens, H, 64, 128, block)
+    n = int(new.sum())
+    k, v = _bf16(rng, n, H, 64), _bf16(rng, n, H, 64)
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    g = _gpu(c)
+    jfa.jfa_cache_append_fp8(k.cuda(), v.cuda(), *_cache(g), torch.from_numpy(offs).cuda(), 2 ** 31 - 1, check=True)
+    kvo.append(np64(k), np64(v), c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, offs)
+    for x in ("kc", "vc"):
+        assert _same_codes(g[x].cpu().numpy(), c[x]), x
+    assert (g["ks"].cpu().numpy() == c["ks"]).all() and (g["vs"].cpu().numpy() == c["vs"]).all()

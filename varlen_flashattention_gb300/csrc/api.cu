@@ -1014,11 +1014,10 @@ jfa_status jfa_cache_append_fp8(const jfa_cache_append_fp8_args* a, void* ws, si
   if (a->batch > 0 && !aligned(a->new_offsets, 4)) return JFA_ERR_INVALID_ARG;
   if (a->batch > 0 && a->total_new > 0 && (!aligned(a->k, 16) || !aligned(a->v, 16))) return JFA_ERR_INVALID_ARG;
   if (a->weights && !aligned(a->weights, 4)) return JFA_ERR_INVALID_ARG;
-  // blocks of the grid: chunks of 128 positions x heads, K and V
-  const int64_t chunks = (static_cast<int64_t>(a->max_new) + 127) / 128 + 2;
-  const double blocks = std::max(static_cast<double>(a->batch) * chunks, a->total_new / 128 + 2.0 * a->batch) *
-                        2 * a->kv_heads;
-  if (blocks >= 2147483647.0) return JFA_ERR_INVALID_ARG;
+  // Chunks of 128 positions that the new tokens can touch, x heads, K and V: the largest grid, whatever
+  // max_new is. (As many sequences x heads as the evict call takes, 2^28, or 2^36 new rows.)
+  const int64_t chunks = a->total_new / 128 + 2 * static_cast<int64_t>(a->batch);
+  if (chunks * 2 * a->kv_heads >= int64_t(1) << 30) return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
   if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
   int32_t* status = static_cast<int32_t*>(ws);
