@@ -106,11 +106,34 @@ LAYOUTS = [(128, 16, 16), (64, 16, 8), (128, 1, 1), (64, 24, 8), (128, 128, 64)]
 
 
 @pytest.mark.parametrize("d,P,block", LAYOUTS)
+def test_evict_scales_that_are_no_powers_of_two(d, P, block):
+    c = _case(41, [300, 40, 7, 129], 2, d, P, block, spare=300)
+    for x in ("ks", "vs"):
+        c[x] *= c["rng"].uniform(0.5, 1.5, c[x].shape).astype(np.float32)
+    _evict_equals(c, 90, 2, 5)
+
+
+@pytest.mark.parametrize("d,P,block", LAYOUTS)
 def test_evict_rounds_once(d, P, block):
     """Values a hair from the middle of two e4m3 values at the new scale go to the nearer one."""
     c = _case(42, [300, 40, 7, 129], 2, d, P, block, spare=300)
     _tie_cache(c, c["rng"], block)
     _evict_equals(c, 90, 2, 5)
+
+
+@pytest.mark.parametrize("powers", [15, 16, 17, 20])
+@pytest.mark.parametrize("odd", [False, True])
+def test_evict_tiny_codes_under_large_scales(powers, odd):
+    """Blocks of which only the smallest codes are in use, or none, get a scale up to 2^17 times smaller."""
+    c = _case(43, [300, 77], 2, 64, 16, 8, spare=300)
+    rng = c["rng"]
+    top = 8 >> max(0, powers - 14)  # codes 1 .. 7: e4m3's subnormals
+    for n, sc in (("kc", "ks"), ("vc", "vs")):
+        c[n][:] = rng.integers(0, top + 1, c[n].shape) | (rng.integers(0, 2, c[n].shape) << 7)
+        c[sc][:] = 2.0 ** rng.integers(-3, 4, c[sc].shape)
+        if odd:
+            c[sc] *= rng.uniform(0.5, 1.5, c[sc].shape).astype(np.float32)
+    _evict_equals(c, 61, 1, 3)
 
 
 @pytest.mark.parametrize("e", [118, 119, 120, 121, 127])
@@ -219,3 +242,22 @@ def test_append_with_a_loose_bound_on_new_tokens(B, H, block):
     for x in ("kc", "vc"):
         assert _same_codes(g[x].cpu().numpy(), c[x]), x
     assert (g["ks"].cpu().numpy() == c["ks"]).all() and (g["vs"].cpu().numpy() == c["vs"]).all()
+
+
+# ------------------------------------------------------------------ the same again
+
+@pytest.mark.parametrize("lens,Hkv,G,ql,d", [([3000, 1, 0, 700], 2, 4, 1, 128), ([5000], 1, 4, 4, 64),
+                                             ([40000] + [300] * 70, 1, 8, 1, 128)])
+def test_decode_repeats_itself(lens, Hkv, G, ql, d):
+    """The same inputs give the same bits, whatever the workspace held before."""
+    c = _case(49, lens, Hkv, d, 16, 16)
+    g, q = _gpu(c), _bf16(c["rng"], len(lens), ql, Hkv * G, d).cuda()
+    w = torch.from_numpy(c["rng"].random((len(lens), Hkv, c["cap"])).astype(np.float32)).cuda()
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    runs = []
+    for fill in (0, 0xA5, 0xFF):
+        ws.fill_(fill)
+        out = torch.zeros_like(w)
+        runs.append((*jfa.jfa_decode_fp8(q, *_cache(g), weights=w, weights_out=out, workspace=ws, check=True), out))
+    for r in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], r))
