@@ -1030,10 +1030,21 @@ __device__ __forceinline__ void add_weights(const Fp8DecodeParams& p, int max_pa
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           sum[k] *= p.decay;
-          // The first `hidden` rows do not see this token: they add nothing, a NaN lse of theirs neither.
-          const int hidden = max(t + 32 * k - (L - p.q_len), 0) * p.group;
+          float all = sum[k];
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) sum[k] += r < hidden ? 0.f : ptx::ex2(v[k][r] - z[r]);
+          for (int r = 0; r < kRows; ++r) all += ptx::ex2(v[k][r] - z[r]);
+          // The first `hidden` rows do not see this token: they add nothing, a NaN lse of theirs neither.
+          // (A branch that few warps take: with a test of every row the loads no longer go out together,
+          // 36 against 41 us for 87 x 2k-8k tokens of one KV head, 8 rows, behind the join.)
+          const int newer = t + 32 * k - (L - p.q_len);
+          if (newer > 0) {
+            const int hidden = newer * p.group;
+            all = sum[k];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+              if (r >= hidden) all += ptx::ex2(v[k][r] - z[r]);
+          }
+          sum[k] = all;
           if (t + 32 * k < end) out[t + 32 * k] = sum[k];
         }
       }
