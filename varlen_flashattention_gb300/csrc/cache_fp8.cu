@@ -174,7 +174,9 @@ __device__ __forceinline__ bool append_range_ok(const Fp8AppendParams& p, int b,
 // sets the status block; the others pass over what is wrong without a word.
 // That spares the launch that would have to clear the status block for them. A
 // thread a sequence; the pages of those with many new ones are left to the warps
-// (512 sequences 7 us, a warp for each 32 us).
+// (512 sequences 7 us, a warp for each 32 us). A warp reads 128 entries at a time, which the
+// call waits for where pages hold one token: one prompt of 32k tokens 90 us, 43 in pages of 16
+// (with blocks of one token in both).
 __device__ void append_report(const Fp8AppendParams& p) {
   __shared__ int32_t s_left, s_b[kThreads], s_lo[kThreads], s_hi[kThreads];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -437,10 +439,12 @@ cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t*
   p.status = status;
   const int64_t heads = 2 * static_cast<int64_t>(a.kv_heads);
   // A warp a scale block where the block's rows fit its registers and are not few among many: of 8 heads
-  // of 128, 16 prompts of 61 to 8192 tokens take 66 us with blocks of 16 tokens (77 by chunks), 75 with
-  // blocks of 32 (77), but 99 with blocks of 8 (76), a row or so a warp. Of few new tokens it is the faster one
-  // whatever the block: 512 x 1 token 6.9 us (66), 256 x 24 in blocks of 128 12.8 (46), 256 x 16 in
-  // blocks of 1 37 (40).
+  // of 128, 16 prompts of 61 to 8192 tokens take 67 us with blocks of 16 tokens (77 by chunks), 75 with
+  // blocks of 32 (77), but 100 with blocks of 8 (77), a row or so a warp. The same of one head 9.8 (12.0),
+  // 11.6 (12.0) and 14.1 (12.0), and of head_dim 64, where a warp covers four rows a pass instead of two: 8 heads
+  // 44 (49), 49 (50) and 69 (49), one head 7.1 (7.5), 7.5 (7.7) and 10.1 (7.9). Of few new tokens it is the
+  // faster one whatever the block: 512 x 1 token 6.9 us (66), 256 x 32 in blocks of 128 12.4 (35; of head_dim
+  // 64 8.7 and 26; of one head 5.4 and 7.6), 256 x 16 in blocks of 1 37 (35 to 40; one head 7.0 and 7.4).
   const int64_t fixed = (static_cast<int64_t>(a.max_new) + a.block_size - 2) / a.block_size + 1;
   const int64_t most = a.total_new / a.block_size + 2 * static_cast<int64_t>(a.batch);
   const int64_t jobs = std::min(fixed * a.batch, most) * heads;
@@ -530,7 +534,9 @@ struct alignas(16) SelShared {
 // sequence after the other, or a warp a sequence, the lengths of 32 at once and the next one's first
 // entries on their way (512 sequences of up to 2k tokens 267 us the call, 294 one after the other);
 // whichever takes fewer steps where the rows are full (15 x 20k-32k tokens in pages of 16: a warp each
-// 29 us, all on each 40). f(b, i, entry) is called by the thread that read the entry.
+// 29 us, all on each 40). f(b, i, entry) is called by the thread that read the entry. One block is enough
+// for pages of 16 tokens; with pages of one token the call waits for it (32 x 1k-32k tokens cut to 2k
+// 701 us, 89 in pages of 16 with blocks of one token; one of 131k cut to 16k 96 and 29).
 template <class Used, class F>
 __device__ __forceinline__ void for_entries(const int32_t* table, int batch, int width, Used used, F f) {
   const int lane = threadIdx.x & 31;

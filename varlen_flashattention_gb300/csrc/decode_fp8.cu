@@ -90,8 +90,10 @@ struct Fp8DecodeParams {
 };
 
 constexpr int kF8Warps = 4;
-constexpr int kF8MinTiles = 1;    // fewest tiles of a part (a short sequence's time grows by 0.6 us a tile)
-constexpr int kF8ScanBatch = 512; // batches up to this number their tiles in every block
+// Batches up to this number their tiles in every block, larger ones in a kernel before: 512 x 100-1000
+// tokens of one KV head of 64 18.1 against 19.8 us, 256 x 13.9 against 16.1; 1024 x 27.4 against 27.6,
+// for 4 KB more of shared memory.
+constexpr int kF8ScanBatch = 512;
 constexpr int kF8RowParts = 62;   // parts that a warp joins a row of (two lse a lane, less two shared parts)
 // A score may pass its reference by this much before the reference moves.
 constexpr float kF8Slack = 8.f;
@@ -101,9 +103,10 @@ constexpr float kF8NoRef = -3.0e38f;  // a reference before the first visible to
 
 template <int D, int NR>
 struct F8Tile {
-  // By the registers: 128 a thread, or 255 with 16 rows. (16 rows at head_dim 128 in 168 registers
-  // spill, 88 us against 67 us for 16 x 0.5k-8k tokens with 4 query tokens of 4 heads; with Q
-  // in shared memory instead of 32 of the registers they take 70 us.)
+  // By the registers: 128 a thread, or 255 with 16 rows; at head_dim 128 one to three of them
+  // spill (4 to 12 bytes). (16 rows at head_dim 128 in 168 registers spill far more, 88 us against
+  // 67 us for 16 x 0.5k-8k tokens with 4 query tokens of 4 heads; with Q in shared memory instead
+  // of 32 of the registers they take 70 us.)
   static constexpr int kCtasPerSm = NR == 1 ? 4 : 2;
   // Tiles computed together. 16 rows leave 8 warps an SM, too few to cover the chain of a tile's
   // steps by each other's work: two tiles give each warp two such chains.
@@ -221,7 +224,7 @@ struct F8Line {
   int64_t parts;  // parts in use
   __device__ __forceinline__ F8Line(int32_t tiles, int max_parts) {
     total = tiles;
-    parts = min(static_cast<int64_t>(max_parts), (total + kF8MinTiles - 1) / kF8MinTiles);
+    parts = min(static_cast<int64_t>(max_parts), total);
   }
   __device__ __forceinline__ int begin(int64_t i) const { return quotient(static_cast<uint64_t>(i * total), parts); }
   // the part that holds tile x: the last i with floor(i total / parts) <= x
@@ -1063,8 +1066,8 @@ __global__ void __launch_bounds__(32 * kF8WeightWarps) fp8_decode_weights_kernel
 }
 
 // The weights beside the join of a warp per row: the first `blocks` blocks add weights, the others join
-// rows, the last one reports. One launch less, and neither waits for the other: 32 x 1k-32k tokens 208.5 ->
-// 206.6 us, 24 x 37-4k of head_dim 64 21.1 -> 20.2, and 3 us less on the host.
+// rows, the last one reports. One launch less, and neither waits for the other: 32 x 1k-32k tokens 206.4 ->
+// 204.8 us, 24 x 37-4k of head_dim 64 21.3 -> 19.3, and 3 us less on the host.
 template <int D, int kAhead, int kRows>
 __global__ void __launch_bounds__(128) fp8_decode_finish_kernel(const Fp8DecodeParams p, int max_parts, int blocks) {
   wait_prior_grid();
@@ -1121,7 +1124,11 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
     e = w ? launch_main<D, 2, true>(p, grid, stream) : launch_main<D, 2, false>(p, grid, stream);
   if (ev) cudaEventRecord(ev[1], stream);
   if (e != cudaSuccess) return e;
-  // parts a sequence has on average: past 32, the wide join (with 25, 24 x 37-4k tokens take 26 us against 21)
+  // The wide join past 32 parts a sequence on average, half of what a warp joins: lengths differ. With
+  // 25 parts, 24 x 37-4k tokens of head_dim 64 take 26 us by it and 21 by rows; with 6 to 28 parts, 8 KV heads,
+  // 51 x 10k 185 and 154, 11 x 32k 121 and 114. With 34 to 61 parts even lengths would take less by rows
+  // still (9 x 8k 37 and 32, 5 x 8k 25 and 24), mixed ones more: 5 x 1k-32k 37 and 50, 41 x 1k-32k of one KV
+  // head 42 and 82, one of 131k with four of 500 52 and 62. With 101 parts 3 x 32k take 39 and 76.
   const uint32_t rows = static_cast<uint32_t>(p.batch) * p.c.hkv * nrows, join_blocks = (rows + 3) / 4 + 1;
   const bool wide = p.max_parts > 32 * p.batch;
   auto join = [&] {
@@ -1129,12 +1136,16 @@ static cudaError_t launch_dim(Fp8DecodeParams& p, void* events, int sms, cudaStr
                 : launch_after(fp8_decode_join_kernel<D, false>, dim3(join_blocks), dim3(128), 0, stream, p);
   };
   if (!w) return join();
-  // The weights beside the join read a sequence's parts again in every warp: not where there can be thousands.
+  // The weights beside the join read the lse of a sequence's parts again in every warp: not where there can
+  // be thousands. Even lengths take less beside it whatever the parts (11 to 87 x 2k-8k 32 us against 34, and
+  // 3 less on the host), one sequence of 65k among 500s more: with 304 parts 48 against 44 (4 rows), 53
+  // against 42 (16 rows, 4 KV heads), with 608 39 against 32 and 66 against 32, with 1216 36 against 30 and
+  // 96 against 32.
   const bool beside = !wide && p.max_parts <= 640;
   const int weight_warps = beside ? sms * 5 * 4 : sms * 4 * kF8WeightWarps;
   const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(weight_warps / p.c.hkv, tiles)));
   if (beside) {
-    const int blocks = weight_warps / 4;  // five of the six blocks that fit an SM: the join runs beside them
+    const int blocks = weight_warps / 4;  // five of the six or seven blocks that fit an SM: the join runs beside them
     const dim3 g(blocks + join_blocks), block(128);
     if (nrows <= 4) return launch_after(fp8_decode_finish_kernel<D, 4, 4>, g, block, 0, stream, p, parts, blocks);
     if (nrows <= 8) return launch_after(fp8_decode_finish_kernel<D, 2, 8>, g, block, 0, stream, p, parts, blocks);
