@@ -409,7 +409,8 @@ typedef struct {
  *   query heads and the q_len query tokens
  * (the first term is left out if weights is NULL); entries past L_b are not
  * written. weights and weights_out may be the same array. The workspace then
- * holds a score of 4 bytes per query row and slot of the page table. Codes that are
+ * holds a score of 4 bytes per query row and slot of the page table, whatever the
+ * lengths are (512 rows of 131,072 slots and 32 query heads: 8.6 GB). Codes that are
  * NaN make NaN of the rows that see them, and of no others; a row that is NaN makes
  * NaN of the weights of the tokens it sees, and of no others. */
 typedef struct {

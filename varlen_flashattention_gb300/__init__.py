@@ -621,7 +621,8 @@ def jfa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens_k,
     weights (optional, fp32 [B, Hkv, max_pages * page_size]): weights_out = decay * weights + each
     cached token's attention weight, summed over the group's query heads and the query tokens, for
     the tokens of each sequence; weights is updated in place if weights_out is not given, and
-    weights_out alone receives the sums. Returns O bf16 [B, q_len, Hq, d], LSE fp32 [B, q_len, Hq]."""
+    weights_out alone receives the sums. With either the workspace holds 4 bytes per query row and
+    slot of page_table, whatever the lengths are. Returns O bf16 [B, q_len, Hq, d], LSE fp32 [B, q_len, Hq]."""
     kc, vc, (num_pages, P, block, Hkv, d, B, mp) = _fp8_cache_inputs(k_cache, v_cache, k_scale, v_scale, page_table,
                                                                      seqlens_k)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
