@@ -366,8 +366,9 @@ typedef struct {
  * num_pages * page_size < 2^31. Token t of sequence b lives in page
  * page_table[b][t / page_size], slot t % page_size. Scales must be positive
  * normal numbers up to 2^127; those that jfa_cache_append_fp8 and
- * jfa_cache_evict_fp8 write are powers of two. head_dim is 64 or 128. Slots of a page past a sequence's length are never
- * read and, but for codes of a block whose scale changes, never written.
+ * jfa_cache_evict_fp8 write are powers of two. head_dim is 64 or 128. Slots of a
+ * page past a sequence's length are never read and, but for codes of a block whose
+ * scale changes, never written.
  *
  * jfa_cache_append_fp8: the new tokens' K and V, packed by offsets, become the
  * last tokens of their sequences: seqlens_k counts them already, so sequence b's
@@ -402,8 +403,10 @@ typedef struct {
  * attend to it as in jfa_decode_smallq (query token i sees keys
  * j <= L_b - q_len + i; a row that sees no key gets O = 0, LSE = -inf), over the
  * values that the codes and scales stand for. q_len x (q_heads / kv_heads) must
- * be <= 16; the group may be any number up to that. The work is split evenly over
- * the device whatever the lengths; there is no split count to choose.
+ * be <= 16; the group may be any number up to that. Scores are held in fp32: the
+ * largest |q| of a row times a K scale times `scale` must stay within its range.
+ * The work is split evenly over the device whatever the lengths; there is no split
+ * count to choose.
  * Attention weights: with weights_out set, for every t < L_b and KV head g
  *   weights_out[b][g][t] = decay * weights[b][g][t] + sum of P over the group's
  *   query heads and the q_len query tokens

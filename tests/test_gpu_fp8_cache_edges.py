@@ -10,7 +10,7 @@ import torch
 import varlen_flashattention_gb300 as jfa
 from oracle import kv_cache as kvo
 from tests.parity import np64
-from tests.test_gpu_fp8_cache import _bf16, _cache, _case, _gpu, _same_codes
+from tests.test_gpu_fp8_cache import _bf16, _cache, _case, _gpu, _same_codes, check_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -196,6 +196,19 @@ def test_append_rewrites_the_largest_older_codes(d, P, block, old, new, odd):
 
 
 @pytest.mark.parametrize("d,P,block,old,new", GROWN)
+@pytest.mark.parametrize("scale", [2.0 ** -126, 2.0 ** -125, 2.0 ** 126, 2.0 ** 127, 1.5 * 2.0 ** -126, 1.5 * 2.0 ** 126])
+def test_append_behind_the_smallest_and_largest_scales(d, P, block, old, new, scale):
+    """New values of the scale's own size, which keep it, and much smaller ones."""
+    c = _case(50, [a + b for a, b in zip(old, new)], 2, d, P, block)
+    c["ks"][:] = c["vs"][:] = scale
+    n = sum(new)
+    size = 2.0 ** c["rng"].integers(-12, 1, (n, 2, 1)) * min(scale * 100, 2.0 ** 125)
+    k, v = ((_bf16(c["rng"], n, 2, d).double() * torch.from_numpy(size)).to(torch.bfloat16) for _ in range(2))
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+    _append_equals(c, old, new, k, v)
+
+
+@pytest.mark.parametrize("d,P,block,old,new", GROWN)
 def test_append_new_codes_with_one_rounding(d, P, block, old, new):
     """New values whose quotient by an older scale, no power of two, is a hair from the middle of two codes."""
     c = _case(47, [a + b for a, b in zip(old, new)], 3, d, P, block)
@@ -222,6 +235,22 @@ def test_append_new_codes_with_one_rounding(d, P, block, old, new):
                 y[at:at + m, h] = torch.from_numpy(x[i] * rng.choice([1.0, -1.0, 0.5, 2.0, 64.0], (m, d))).float()
             at += m
     _append_equals(c, old, new, k.to(torch.bfloat16), v.to(torch.bfloat16))
+
+
+# ------------------------------------------------------------------ scales at both ends
+
+@pytest.mark.parametrize("ks,q_size", [(126, -122), (127, -120), (-126, 120), (100, -98)])
+@pytest.mark.parametrize("vs", [126, 120, -126])
+@pytest.mark.parametrize("lens,ql", [([33, 4000], 1), ([1203], 4)])
+def test_decode_largest_and_smallest_scales(ks, q_size, vs, lens, ql):
+    """Keys and queries whose product is of usual size, values near fp32's ends: small codes, so that O is a bf16."""
+    c = _case(51, lens, 1, 128, 16, 16)
+    for n in ("kc", "vc"):
+        c[n][:] = c["rng"].integers(0, 49, c[n].shape) | (c["rng"].integers(0, 2, c[n].shape) << 7)
+    c["ks"][:], c["vs"][:] = 2.0 ** ks, 2.0 ** vs
+    q = (_bf16(c["rng"], len(lens), ql, 4, 128).double() * 2.0 ** q_size).to(torch.bfloat16)
+    o, lse = jfa.jfa_decode_fp8(q.cuda(), *_cache(_gpu(c)), scale=0.25, check=True)
+    check_decode(c, q, o, lse, 0.25, what="ends")
 
 
 # ------------------------------------------------------------------ sizes
