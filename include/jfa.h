@@ -469,6 +469,101 @@ typedef struct {
   float* new_weights;         /* out: fp32 [batch, kv_heads, new_max_pages * page_size] (not weights itself) */
 } jfa_cache_evict_fp8_args;
 
+/* ------------------------------------------------------------------ speculative decoding
+ * Three calls around the bf16 paged cache of jfa_decode_splitkv ([INF] PR
+ * 1993: few query rows, e.g. speculative decoding; PR 1999/2104: paging. The
+ * pages name neither trees nor how a cache is filled; the readings here are
+ * this library's): new tokens enter the cache, trees of drafted tokens attend
+ * to it, and the drafts that were accepted stay. head_dim is 64 or 128 and
+ * page_size any number; num_pages * page_size < 2^31. The new tokens of sequence
+ * b are the rows offsets[b] .. offsets[b+1]-1 of the packed tensors (n_b of them, maybe
+ * none) and the last n_b of the seqlens_k[b] = L_b tokens of its cache.
+ * offsets[batch] may be below the tensors' rows: the rows behind the last
+ * sequence are neither read nor written.
+ *
+ * jfa_cache_append_rope: K and V of the new tokens are written to positions
+ * L_b - n_b .. L_b - 1, K rotated on the way, and Q rotated into q_out. Token i of
+ * a sequence turns by row p of the tables, p = L_b - n_b + i or, if positions is
+ * set, its entry there (drafts of a tree: tokens before + depth); a pair (x, y)
+ * of columns becomes
+ *   x' = x cos[p][j] - y sin[p][j],   y' = y cos[p][j] + x sin[p][j],
+ * in fp32, rounded to bf16 once. Pair j < rot_dim / 2 is columns (j, j +
+ * rot_dim / 2), or (2j, 2j + 1) if interleaved; columns from rot_dim on are copied,
+ * as V is. rot_dim is a multiple of 16 up to head_dim, or 0: nothing turns (the
+ * tables may then be NULL). The rows of Q, K and V may lie apart (strides in
+ * elements, multiples of 8: views of a fused projection's output). A slot that
+ * receives a token must belong to one sequence, once. */
+typedef struct {
+  const void* q;              /* optional: bf16 rows of [q_heads, head_dim], q_stride apart */
+  const void* k;              /* bf16 rows of [kv_heads, head_dim], k_stride apart */
+  const void* v;              /* as k, v_stride apart */
+  const int32_t* new_offsets; /* int32 [batch+1], device, new_offsets[batch] <= total_new */
+  const int32_t* positions;   /* optional: int32 [total_new], 0 <= p < table_rows */
+  const float* cos_table;     /* fp32 [table_rows, rot_dim / 2] */
+  const float* sin_table;     /* as cos_table */
+  void* q_out;                /* out (with q): bf16 [total_new, q_heads, head_dim]; may be q itself if its rows touch */
+  void* k_cache;              /* in/out: bf16 [num_pages, page_size, kv_heads, head_dim] */
+  void* v_cache;              /* in/out: as k_cache */
+  const int32_t* page_table;  /* int32 [batch, max_pages]; entries past ceil(L_b/page_size) are not read */
+  const int32_t* seqlens_k;   /* int32 [batch], new tokens included, <= max_pages*page_size */
+  int64_t q_stride, k_stride, v_stride; /* >= heads * head_dim, multiples of 8 */
+  int32_t batch, q_heads, kv_heads, head_dim; /* q_heads is not used without q */
+  int32_t rot_dim, interleaved, table_rows;
+  int32_t page_size, num_pages, max_pages;
+  int32_t total_new;          /* host: rows of q, k and v */
+} jfa_cache_append_rope_args;
+
+/* jfa_decode_tree: attention of the new tokens over their sequence's cache, which
+ * already holds them. Row i of sequence b sees every token before the new ones and,
+ * of those, token j iff bit j of its word of tree_mask is set (a tree's ancestors and
+ * itself; any mask is taken, bits from n_b on are ignored). Without tree_mask
+ * it sees j <= i, the chain of jfa_decode_smallq; n_b = 1 is jfa_decode_splitkv.
+ *   S = scale q K^T over the visible tokens, P = softmax(S), O = P V, LSE = ln sum exp S;
+ * a row that sees none gets O = 0, LSE = -inf. Infinities and NaN in K or V reach the rows
+ * that see their token and no others. n_b <= max_q <= 64; q_heads / kv_heads may be any
+ * number up to 128. The work is split evenly over the device whatever the lengths; there
+ * is no split count to choose. A sequence whose length or offsets are out of range gets
+ * O = 0, LSE = -inf (its rows of total_q), and the call reports it. */
+typedef struct {
+  const void* q;              /* bf16 [total_q, q_heads, head_dim] */
+  const void* k_cache;        /* bf16 [num_pages, page_size, kv_heads, head_dim] */
+  const void* v_cache;        /* as k_cache */
+  const int32_t* page_table;  /* int32 [batch, max_pages]; entries past ceil(L_b/page_size) are not read */
+  const int32_t* seqlens_k;   /* int32 [batch], n_b <= L_b <= max_pages*page_size */
+  const int32_t* q_offsets;   /* int32 [batch+1], device, q_offsets[batch] <= total_q */
+  const uint64_t* tree_mask;  /* optional: uint64 [total_q] */
+  int32_t batch, q_heads, kv_heads, head_dim;
+  int32_t page_size, num_pages, max_pages;
+  int32_t total_q;            /* host: rows of q */
+  int32_t max_q;              /* host: >= every n_b, 1 .. 64 */
+  float scale;
+  void* o;                    /* out: bf16 [total_q, q_heads, head_dim] */
+  float* lse;                 /* out: fp32 [total_q, q_heads] */
+  void* main_kernel_events;   /* optional cudaEvent_t[2] around the main kernel */
+} jfa_decode_tree_args;
+
+/* jfa_cache_accept: the K and V rows of the accepted new tokens move to the places
+ * behind the earlier tokens: with C_b = L_b - n_b, the row of position C_b + k becomes
+ * what that of C_b + accepted[b][k] was, for k < counts[b] (all rows are read before
+ * any is written; the order is the caller's), and
+ *   new_seqlens[b] = C_b + counts[b].
+ * Rows turned by jfa_cache_append_rope with positions by depth need no other turn. A
+ * sequence with a count, index, length or page out of range is left as it is and gets
+ * C_b, or L_b where the length or the offsets are what is wrong; the call reports it. */
+typedef struct {
+  void* k_cache;              /* in/out: bf16 [num_pages, page_size, kv_heads, head_dim] */
+  void* v_cache;              /* in/out: as k_cache */
+  const int32_t* page_table;  /* int32 [batch, max_pages] */
+  const int32_t* seqlens_k;   /* int32 [batch], new tokens included */
+  const int32_t* q_offsets;   /* int32 [batch+1], device */
+  const int32_t* accepted;    /* int32 [batch, width], 0 <= accepted[b][k] < n_b for k < counts[b] */
+  const int32_t* counts;      /* int32 [batch], 0 <= counts[b] <= min(width, n_b) */
+  int32_t batch, kv_heads, head_dim;
+  int32_t page_size, num_pages, max_pages;
+  int32_t width;              /* 0 .. 64 */
+  int32_t* new_seqlens;       /* out: int32 [batch] (not seqlens_k itself) */
+} jfa_cache_accept_args;
+
 /* Workspace sizes in bytes (0 only when args is NULL). */
 JFA_API size_t jfa_fwd_workspace_size(const jfa_fwd_args* args);
 JFA_API size_t jfa_bwd_workspace_size(const jfa_bwd_args* args);
@@ -483,6 +578,9 @@ JFA_API size_t jfa_fp8_quantize_v_workspace_size(const jfa_fp8_quantize_v_args* 
 JFA_API size_t jfa_cache_append_fp8_workspace_size(const jfa_cache_append_fp8_args* args);
 JFA_API size_t jfa_decode_fp8_workspace_size(const jfa_decode_fp8_args* args);
 JFA_API size_t jfa_cache_evict_fp8_workspace_size(const jfa_cache_evict_fp8_args* args);
+JFA_API size_t jfa_cache_append_rope_workspace_size(const jfa_cache_append_rope_args* args);
+JFA_API size_t jfa_decode_tree_workspace_size(const jfa_decode_tree_args* args);
+JFA_API size_t jfa_cache_accept_workspace_size(const jfa_cache_accept_args* args);
 /* Bytes of the V blocks for a batch (an upper bound: (ceil(total/128) + batch) x heads x 16384). */
 JFA_API size_t jfa_fp8_vt_bytes(int32_t batch, int32_t heads, int32_t total);
 
@@ -513,6 +611,12 @@ JFA_API jfa_status jfa_decode_fp8(const jfa_decode_fp8_args* args, void* workspa
                           cudaStream_t stream);
 JFA_API jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* args, void* workspace, size_t workspace_bytes,
                                cudaStream_t stream);
+JFA_API jfa_status jfa_cache_append_rope(const jfa_cache_append_rope_args* args, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+JFA_API jfa_status jfa_decode_tree(const jfa_decode_tree_args* args, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+JFA_API jfa_status jfa_cache_accept(const jfa_cache_accept_args* args, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
 
 /* Paged split-KV decode that allocates nothing. The pages have no
  * counterpart for this entry point; it exists for callers that cannot

@@ -19,6 +19,9 @@ kernels; there is no CPU or PyTorch fallback.
     jfa_cache_append_fp8  new tokens' K and V quantized into an 8-bit paged cache (block scales)
     jfa_decode_fp8        decode over the 8-bit paged cache, with accumulated attention weights -> (O, LSE)
     jfa_cache_evict_fp8   the tokens of the largest accumulated weights moved to new pages
+    jfa_cache_append_rope new tokens' K and V written to a bf16 paged cache, Q and K rotated on the way
+    jfa_decode_tree       attention of drafted trees (or chains) of up to 64 tokens over the paged cache -> (O, LSE)
+    jfa_cache_accept      the accepted drafts moved to the places behind the earlier tokens
     jfa_trace_enable      registers a per-role event trace buffer (JFA_TRACE builds; see trace.py)
     jfa_trace_compiled    1 if the loaded library records traces
     jagged_attention      autograd wrapper of jfa_fwd / jfa_bwd
@@ -39,6 +42,7 @@ __all__ = [
     "varlen_attention", "jfa_decode_smallq", "jfa_selftest_wait_timeout", "jfa_fwd_fp8",
     "jfa_trace_enable", "jfa_trace_compiled", "jfa_fp8_quantize_v",
     "jfa_cache_append_fp8", "jfa_decode_fp8", "jfa_cache_evict_fp8",
+    "jfa_cache_append_rope", "jfa_decode_tree", "jfa_cache_accept",
 ]
 
 
@@ -696,6 +700,156 @@ def jfa_cache_evict_fp8(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_
                                first, recent, _ptr(kept), _ptr(new_seqlens), _ptr(new_weights))
     _run("jfa_cache_evict_fp8", "jfa_cache_evict_fp8_workspace_size", a, dev, workspace, stream, check)
     return kept, new_seqlens, new_weights
+
+
+# ---------------------------------------------------------------- speculative decoding
+
+def _paged_inputs(k_cache, v_cache, page_table, seqlens_k, offsets, offsets_name):
+    """Shapes of a bf16 paged cache and of the batch over it: (num_pages, page size, KV heads,
+    head dim, batch, max_pages)."""
+    try:  # the usual case in one test; what follows it names what is wrong
+        num_pages, P, Hkv, d = shape = k_cache.shape
+        B, mp = page_table.shape
+        bf16, i32 = torch.bfloat16, torch.int32
+        if (k_cache.dtype is bf16 and v_cache.dtype is bf16 and page_table.dtype is i32 and seqlens_k.dtype is i32 and
+                offsets.dtype is i32 and v_cache.shape == shape and seqlens_k.shape == (B,) and
+                offsets.shape == (B + 1,) and k_cache.is_contiguous() and v_cache.is_contiguous() and
+                page_table.is_contiguous() and seqlens_k.is_contiguous() and offsets.is_contiguous()):
+            return num_pages, P, Hkv, d, B, mp
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    num_pages, P, Hkv, d = k_cache.shape
+    _need(v_cache, "v_cache", torch.bfloat16, k_cache.shape)
+    _need(seqlens_k, "seqlens_k", torch.int32, 1)
+    _need(page_table, "page_table", torch.int32, 2)
+    B, mp = page_table.shape
+    _need(page_table, "page_table", torch.int32, (seqlens_k.numel(), mp))
+    _need(offsets, offsets_name, torch.int32, (B + 1,))
+    return num_pages, P, Hkv, d, B, mp
+
+
+def _need_rows(t, name, heads, d, rows):
+    """bf16 [rows, heads, d] whose rows may lie apart (a view of a fused projection's
+    output); returns the row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1:] != (heads, d) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have shape {('rows' if rows is None else rows, heads, d)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return heads * d
+    stride, inner, last = t.stride()
+    if last != 1 or (heads > 1 and inner != d) or (t.shape[0] > 1 and (stride < heads * d or stride % 8 != 0)):
+        raise ValueError(f"{name}: a row's heads must be contiguous and its stride a multiple of 8, got {t.stride()}")
+    return stride if t.shape[0] > 1 else heads * d
+
+
+def jfa_cache_append_rope(q, k, v, k_cache, v_cache, page_table, seqlens_k, new_offsets, cos, sin, positions=None,
+                          interleaved=False, q_out=None, workspace=None, stream=None, check=False):
+    """Writes the K and V rows of new tokens into a bf16 paged cache, K rotated by its position on the
+    way, and rotates Q (see include/jfa.h). q: bf16 [total_new, Hq, d] or None; k, v: bf16 [total_new,
+    Hkv, d]; the rows of the three may be strided (views of a fused projection's output). Sequence b's
+    rows new_offsets[b] .. new_offsets[b+1]-1 (int32 [B+1]) become its last tokens (seqlens_k, int32 [B],
+    counts them already); caches bf16 [num_pages, page_size, Hkv, d] with d 64 or 128; page_table int32 [B,
+    max_pages]. cos, sin: fp32 [positions, rot_dim / 2] with rot_dim a multiple of 16 up to d, or both
+    None (nothing turns). positions (optional, int32 [total_new]): the tables' rows, by default the
+    tokens' places in their sequences. Pairs are columns (j, j + rot_dim / 2), or neighbours if
+    interleaved. Returns the rotated Q (q_out, which may be q itself; None without q); its rows behind
+    new_offsets[B] are not written."""
+    num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, new_offsets, "new_offsets")
+    ks = _need_rows(k, "k", Hkv, d, None)
+    total = k.shape[0]
+    vs = _need_rows(v, "v", Hkv, d, total)
+    Hq = qs = 0
+    if q is not None:
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        qs = _need_rows(q, "q", Hq, d, total)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rows = rot = 0
+    if cos is not None or sin is not None:
+        _need(cos, "cos", torch.float32, 2)
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        _need(sin, "sin", torch.float32, cos.shape)
+        if rot > d or rot % 16 != 0:
+            raise ValueError(f"cos must hold a multiple of 8 up to {d // 2} columns, got {cos.shape[1]}")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, (total,))
+    if q_out is not None:
+        _need(q_out, "q_out", torch.bfloat16, q.shape)
+    dev = _device(k=k, v=v, q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k,
+                  new_offsets=new_offsets, cos=cos, sin=sin, positions=positions, q_out=q_out)
+    if q is not None and q_out is None:
+        q_out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=dev)
+        if stream is not None:  # new memory belongs to the current stream
+            q_out.record_stream(stream)
+    a = _abi.CacheAppendRopeArgs(_ptr(q), _ptr(k), _ptr(v), _ptr(new_offsets), _ptr(positions), _ptr(cos), _ptr(sin),
+                                 _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens_k), qs, ks,
+                                 vs, B, Hq, Hkv, d, rot, int(bool(interleaved)), rows, P, num_pages, mp, total)
+    _run("jfa_cache_append_rope", "jfa_cache_append_rope_workspace_size", a, dev, workspace, stream, check)
+    return q_out
+
+
+def jfa_decode_tree(q, k_cache, v_cache, page_table, seqlens_k, q_offsets, tree_mask=None, max_q=64, scale=None, o=None,
+                    lse=None, workspace=None, stream=None, events=None, check=False):
+    """Attention of each sequence's new tokens over its bf16 paged cache, which holds them already (see
+    include/jfa.h). q: bf16 [total_q, Hq, d], sequence b's rows q_offsets[b] .. q_offsets[b+1]-1 (int32
+    [B+1]), at most max_q <= 64 of them; the cache as in jfa_cache_append_rope, seqlens_k counting the new
+    tokens. A row sees all tokens before the new ones and new token j iff bit j of its tree_mask (int64 or
+    uint64 [total_q]) is set: its ancestors in the tree and itself; without tree_mask j <= i. Returns O bf16
+    [total_q, Hq, d] and LSE fp32 [total_q, Hq]; rows behind q_offsets[B] are not written."""
+    num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, q_offsets, "q_offsets")
+    _need(q, "q", torch.bfloat16, 3)
+    total, Hq, _ = q.shape
+    _need(q, "q", torch.bfloat16, (total, Hq, d))
+    if tree_mask is not None:
+        mask_type = torch.uint64 if isinstance(tree_mask, torch.Tensor) and tree_mask.dtype == torch.uint64 else torch.int64
+        _need(tree_mask, "tree_mask", mask_type, (total,))
+    if o is not None:
+        _need(o, "o", torch.bfloat16, q.shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (total, Hq))
+    dev = _device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k,
+                  q_offsets=q_offsets, tree_mask=tree_mask, o=o, lse=lse)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((total, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    if stream is not None:  # new memory belongs to the current stream
+        o.record_stream(stream)
+        lse.record_stream(stream)
+    a = _abi.DecodeTreeArgs(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens_k), _ptr(q_offsets),
+                            _ptr(tree_mask), B, Hq, Hkv, d, P, num_pages, mp, total, int(max_q), scale, _ptr(o),
+                            _ptr(lse), None)
+    if events is not None:
+        a.main_kernel_events, _keep = _events(events)
+    _run("jfa_decode_tree", "jfa_decode_tree_workspace_size", a, dev, workspace, stream, check)
+    return o, lse
+
+
+def jfa_cache_accept(k_cache, v_cache, page_table, seqlens_k, q_offsets, accepted, counts, new_seqlens=None,
+                     workspace=None, stream=None, check=False):
+    """Keeps the accepted ones of each sequence's new tokens in a bf16 paged cache: the K and V rows of new
+    tokens accepted[b][k], k < counts[b] (int32 [B, width <= 64] and [B]; 0 .. n_b - 1, n_b = q_offsets[b+1] -
+    q_offsets[b]), move to the places behind the tokens before the new ones, in that order. Returns
+    new_seqlens int32 [B] = seqlens_k - n_b + counts."""
+    num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, q_offsets, "q_offsets")
+    width = accepted.shape[1] if isinstance(accepted, torch.Tensor) and accepted.dim() == 2 else 0
+    _need(accepted, "accepted", torch.int32, (B, width))
+    _need(counts, "counts", torch.int32, (B,))
+    if new_seqlens is not None:
+        _need(new_seqlens, "new_seqlens", torch.int32, (B,))
+    dev = _device(k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k, q_offsets=q_offsets,
+                  accepted=accepted, counts=counts, new_seqlens=new_seqlens)
+    if new_seqlens is None:
+        new_seqlens = torch.empty_like(seqlens_k)
+        if stream is not None:  # new memory belongs to the current stream
+            new_seqlens.record_stream(stream)
+    a = _abi.CacheAcceptArgs(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens_k), _ptr(q_offsets),
+                             _ptr(accepted), _ptr(counts), B, Hkv, d, P, num_pages, mp, width, _ptr(new_seqlens))
+    _run("jfa_cache_accept", "jfa_cache_accept_workspace_size", a, dev, workspace, stream, check)
+    return new_seqlens
 
 
 # ---------------------------------------------------------------- autograd

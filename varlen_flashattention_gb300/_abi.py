@@ -17,6 +17,7 @@ VARIANT_ENV = "JFA_LIBRARY_VARIANT"
 
 c_void_p = ctypes.c_void_p
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_f32 = ctypes.c_float
 
 JFA_OK = 0
@@ -136,6 +137,33 @@ class CacheEvictFp8Args(ctypes.Structure):
                 ("kept", c_void_p), ("new_seqlens", c_void_p), ("new_weights", c_void_p)]
 
 
+class CacheAppendRopeArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("new_offsets", c_void_p),
+                ("positions", c_void_p), ("cos_table", c_void_p), ("sin_table", c_void_p), ("q_out", c_void_p),
+                ("k_cache", c_void_p), ("v_cache", c_void_p), ("page_table", c_void_p), ("seqlens_k", c_void_p),
+                ("q_stride", c_i64), ("k_stride", c_i64), ("v_stride", c_i64),
+                ("batch", c_i32), ("q_heads", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("rot_dim", c_i32), ("interleaved", c_i32), ("table_rows", c_i32),
+                ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("total_new", c_i32)]
+
+
+class DecodeTreeArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("page_table", c_void_p),
+                ("seqlens_k", c_void_p), ("q_offsets", c_void_p), ("tree_mask", c_void_p),
+                ("batch", c_i32), ("q_heads", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("total_q", c_i32),
+                ("max_q", c_i32), ("scale", c_f32), ("o", c_void_p), ("lse", c_void_p),
+                ("main_kernel_events", c_void_p)]
+
+
+class CacheAcceptArgs(ctypes.Structure):
+    _fields_ = [("k_cache", c_void_p), ("v_cache", c_void_p), ("page_table", c_void_p), ("seqlens_k", c_void_p),
+                ("q_offsets", c_void_p), ("accepted", c_void_p), ("counts", c_void_p),
+                ("batch", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("width", c_i32),
+                ("new_seqlens", c_void_p)]
+
+
 # (name, argtypes, restype) of every exported symbol declared in include/jfa.h
 SIGNATURES = [
     ("jfa_fwd_workspace_size", [ctypes.POINTER(FwdArgs)], ctypes.c_size_t),
@@ -151,6 +179,9 @@ SIGNATURES = [
     ("jfa_cache_append_fp8_workspace_size", [ctypes.POINTER(CacheAppendFp8Args)], ctypes.c_size_t),
     ("jfa_decode_fp8_workspace_size", [ctypes.POINTER(DecodeFp8Args)], ctypes.c_size_t),
     ("jfa_cache_evict_fp8_workspace_size", [ctypes.POINTER(CacheEvictFp8Args)], ctypes.c_size_t),
+    ("jfa_cache_append_rope_workspace_size", [ctypes.POINTER(CacheAppendRopeArgs)], ctypes.c_size_t),
+    ("jfa_decode_tree_workspace_size", [ctypes.POINTER(DecodeTreeArgs)], ctypes.c_size_t),
+    ("jfa_cache_accept_workspace_size", [ctypes.POINTER(CacheAcceptArgs)], ctypes.c_size_t),
     ("jfa_fp8_vt_bytes", [c_i32, c_i32, c_i32], ctypes.c_size_t),
     ("jfa_fwd", [ctypes.POINTER(FwdArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_bwd", [ctypes.POINTER(BwdArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
@@ -165,6 +196,9 @@ SIGNATURES = [
     ("jfa_cache_append_fp8", [ctypes.POINTER(CacheAppendFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_decode_fp8", [ctypes.POINTER(DecodeFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_cache_evict_fp8", [ctypes.POINTER(CacheEvictFp8Args), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
+    ("jfa_cache_append_rope", [ctypes.POINTER(CacheAppendRopeArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
+    ("jfa_decode_tree", [ctypes.POINTER(DecodeTreeArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
+    ("jfa_cache_accept", [ctypes.POINTER(CacheAcceptArgs), c_void_p, ctypes.c_size_t, c_void_p], c_i32),
     ("jfa_decode_splitkv_noalloc", [ctypes.POINTER(DecodeArgs), c_void_p], c_i32),
     ("jfa_decode_noalloc_status", [c_void_p, ctypes.POINTER(c_i32)], c_i32),
     ("jfa_read_device_status", [c_void_p, c_void_p, ctypes.POINTER(c_i32)], c_i32),

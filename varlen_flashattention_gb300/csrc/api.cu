@@ -114,6 +114,20 @@ bool make_tmap_f32_acc(CUtensorMap* m, const void* base, uint64_t rows, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D bf16 view [rows, heads, d] read in boxes of 64 columns x `group` heads x `nodes` rows, 128-byte swizzle.
+bool make_tmap_bf16_heads(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads, uint64_t d, uint32_t group,
+                          uint32_t nodes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d, heads, rows};
+  const cuuint64_t strides[2] = {d * 2, heads * d * 2};
+  const cuuint32_t box[3] = {64, group, nodes};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool good_dim(int d) { return d == 64 || d == 128 || d == 192; }
 
 // Which forward kernel runs: head_dim 128 takes the flat-stream kernel, 64
@@ -286,7 +300,46 @@ size_t fp8_evict_bytes(int64_t batch, int64_t new_max_pages) {
   return align_up(kStatusBytes + static_cast<size_t>(batch) * new_max_pages, 256);
 }
 
+// Tree decode: status, findings and records of the CTAs, the partial results of two items each.
+struct TreeLayoutBytes {
+  size_t total = 0, cta_status = 0, records = 0, part_lse2 = 0, part_o = 0, bytes = 0;
+  int32_t row_tiles = 1;
+};
+TreeLayoutBytes tree_layout(const jfa_decode_tree_args& a, int sms) {
+  TreeLayoutBytes L;
+  const int group = a.kv_heads > 0 ? std::min(std::max(a.q_heads / a.kv_heads, 1), kTile) : 1;
+  L.row_tiles = a.max_q > tree_nodes_per_tile(group) ? 2 : 1;
+  const size_t tiles = static_cast<size_t>(sms) * 2 * L.row_tiles, d = a.head_dim == 64 ? 64 : 128;
+  size_t off = kStatusBytes;
+  L.total = off;
+  off += 256;
+  L.cta_status = off;
+  off = align_up(off + 8 * static_cast<size_t>(sms), 256);
+  L.records = off;
+  off = align_up(off + 32 * static_cast<size_t>(sms), 256);
+  L.part_lse2 = off;
+  off += tiles * kTile * 4;
+  L.part_o = off;
+  L.bytes = off + tiles * kTile * d * 4;
+  return L;
+}
+
 // ------------------------------------------------------------------ validation
+
+// What the calls on the bf16 paged cache of speculative decoding have in common.
+jfa_status check_paged_cache(const void* kc, const void* vc, const int32_t* table, const int32_t* seqlens,
+                             const int32_t* offsets, int32_t batch, int32_t kv_heads, int32_t head_dim,
+                             int32_t page_size, int32_t num_pages, int32_t max_pages) {
+  if (batch < 0 || kv_heads < 1 || page_size < 1 || num_pages < 0 || max_pages < 0) return JFA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return JFA_ERR_UNSUPPORTED;
+  if (kv_heads > 32767) return JFA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * page_size >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_pages) * page_size >= (int64_t(1) << 31) - 16384) return JFA_ERR_INVALID_ARG;
+  if (batch > 0 && num_pages > 0 && (!aligned(kc, 16) || !aligned(vc, 16))) return JFA_ERR_INVALID_ARG;
+  if (batch > 0 && (!aligned(seqlens, 4) || !aligned(offsets, 4) || (max_pages > 0 && !aligned(table, 4))))
+    return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
 
 // What the three calls on the 8-bit cache have in common: the cache's own sizes and pointers.
 jfa_status check_fp8_cache(const void* kc, const void* vc, const float* ks, const float* vs, const int32_t* table,
@@ -1082,6 +1135,108 @@ jfa_status jfa_cache_evict_fp8(const jfa_cache_evict_fp8_args* a, void* ws, size
   const int sms = sm_count();
   if (sms <= 0) return JFA_ERR_CUDA;
   return cuda_status(launch_cache_evict_fp8(*a, static_cast<uint8_t*>(ws) + kStatusBytes, status, sms, stream));
+}
+
+size_t jfa_cache_append_rope_workspace_size(const jfa_cache_append_rope_args* a) { return a ? kStatusBytes : 0; }
+
+jfa_status jfa_cache_append_rope(const jfa_cache_append_rope_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!a) return JFA_ERR_INVALID_ARG;
+  const jfa_status st = check_paged_cache(a->k_cache, a->v_cache, a->page_table, a->seqlens_k, a->new_offsets, a->batch,
+                                          a->kv_heads, a->head_dim, a->page_size, a->num_pages, a->max_pages);
+  if (st != JFA_OK) return st;
+  if (a->total_new < 0 || a->total_new == INT32_MAX || (a->batch == 0 && a->total_new > 0)) return JFA_ERR_INVALID_ARG;
+  if (a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 16 != 0 || a->table_rows < 0)
+    return JFA_ERR_INVALID_ARG;
+  if (a->interleaved != 0 && a->interleaved != 1) return JFA_ERR_INVALID_ARG;
+  if (a->q && (a->q_heads < 1 || a->q_heads > 32767)) return JFA_ERR_INVALID_ARG;
+  const auto stride_ok = [&](int64_t s, int64_t heads) { return s >= heads * a->head_dim && s % 8 == 0; };
+  if (a->total_new > 0) {
+    if (!aligned(a->k, 16) || !aligned(a->v, 16) || !stride_ok(a->k_stride, a->kv_heads) ||
+        !stride_ok(a->v_stride, a->kv_heads))
+      return JFA_ERR_INVALID_ARG;
+    if (a->q) {
+      if (!aligned(a->q, 16) || !aligned(a->q_out, 16) || !stride_ok(a->q_stride, a->q_heads)) return JFA_ERR_INVALID_ARG;
+      // in place only if a row of q_out is the same row of q
+      if (a->q_out == a->q && a->q_stride != static_cast<int64_t>(a->q_heads) * a->head_dim) return JFA_ERR_INVALID_ARG;
+    }
+    if (a->rot_dim > 0 && a->table_rows > 0 && (!aligned(a->cos_table, 16) || !aligned(a->sin_table, 16)))
+      return JFA_ERR_INVALID_ARG;
+    if (a->positions && !aligned(a->positions, 4)) return JFA_ERR_INVALID_ARG;
+  }
+  if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  int32_t* status = static_cast<int32_t*>(ws);
+  if (a->batch == 0) return cuda_status(launch_status_clear(status, stream));
+  return cuda_status(launch_cache_append_rope(*a, status, stream));
+}
+
+size_t jfa_decode_tree_workspace_size(const jfa_decode_tree_args* a) {
+  return a ? tree_layout(*a, std::max(sm_count(), 1)).bytes : 0;
+}
+
+jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!a) return JFA_ERR_INVALID_ARG;
+  const jfa_status st = check_paged_cache(a->k_cache, a->v_cache, a->page_table, a->seqlens_k, a->q_offsets, a->batch,
+                                          a->kv_heads, a->head_dim, a->page_size, a->num_pages, a->max_pages);
+  if (st != JFA_OK) return st;
+  if (a->q_heads < 1 || a->q_heads % a->kv_heads != 0 || a->total_q < 0 || a->max_q < 1) return JFA_ERR_INVALID_ARG;
+  if (a->max_q > kTreeMaxNodes || a->q_heads / a->kv_heads > kTile) return JFA_ERR_UNSUPPORTED;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return JFA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->total_q) * a->q_heads >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
+  const bool work = a->batch > 0 && a->total_q > 0;
+  if (work && (!aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4))) return JFA_ERR_INVALID_ARG;
+  if (a->tree_mask && !aligned(a->tree_mask, 8)) return JFA_ERR_INVALID_ARG;
+  if (!aligned(ws, 256) || !events_ok(a->main_kernel_events)) return JFA_ERR_INVALID_ARG;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  if (!work) {
+    if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
+    return cuda_status(launch_status_clear(reinterpret_cast<int32_t*>(w), stream));
+  }
+  const int sms = sm_count();
+  if (sms <= 0) return JFA_ERR_CUDA;
+  const TreeLayoutBytes L = tree_layout(*a, sms);
+  if (ws_bytes < L.bytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  TreeBuffers buf{};
+  buf.status = reinterpret_cast<int32_t*>(w);
+  buf.total = reinterpret_cast<int64_t*>(w + L.total);
+  buf.cta_status = reinterpret_cast<int32_t*>(w + L.cta_status);
+  buf.records = reinterpret_cast<int4*>(w + L.records);
+  buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);
+  buf.part_o = reinterpret_cast<float*>(w + L.part_o);
+  buf.row_tiles = L.row_tiles;
+  // Boxes of tokens that lie side by side in a page, whole swizzle atoms of 8 rows; in pages that 8 does not
+  // divide, rows are gathered four at a time through boxes one row high.
+  int box = a->page_size & -a->page_size;
+  box = box < 8 ? 1 : std::min(box, kTile);
+  const int group = a->q_heads / a->kv_heads;
+  const uint64_t rows = static_cast<uint64_t>(a->num_pages) * a->page_size;
+  const uint64_t cols = static_cast<uint64_t>(a->kv_heads) * a->head_dim;
+  CUtensorMap tq, tk, tv;  // without pages no tile is loaded; the maps must still be valid
+  if (!make_tmap_bf16_heads(&tq, a->q, a->total_q, a->q_heads, a->head_dim, group, tree_nodes_per_tile(group)) ||
+      !make_tmap_bf16(&tk, rows ? a->k_cache : a->q, rows, cols, box) ||
+      !make_tmap_bf16(&tv, rows ? a->v_cache : a->q, rows, cols, box))
+    return JFA_ERR_CUDA;
+  return cuda_status(launch_decode_tree(*a, buf, tq, tk, tv, box, wait_budget_ns(), sms, stream));
+}
+
+size_t jfa_cache_accept_workspace_size(const jfa_cache_accept_args* a) { return a ? kStatusBytes : 0; }
+
+jfa_status jfa_cache_accept(const jfa_cache_accept_args* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!a) return JFA_ERR_INVALID_ARG;
+  const jfa_status st = check_paged_cache(a->k_cache, a->v_cache, a->page_table, a->seqlens_k, a->q_offsets, a->batch,
+                                          a->kv_heads, a->head_dim, a->page_size, a->num_pages, a->max_pages);
+  if (st != JFA_OK) return st;
+  if (a->width < 0) return JFA_ERR_INVALID_ARG;
+  if (a->width > kTreeMaxNodes) return JFA_ERR_UNSUPPORTED;
+  if (a->batch > 0 && (!aligned(a->counts, 4) || !aligned(a->new_seqlens, 4) || (a->width > 0 && !aligned(a->accepted, 4))))
+    return JFA_ERR_INVALID_ARG;
+  if (a->batch > 0 && a->new_seqlens == a->seqlens_k) return JFA_ERR_INVALID_ARG;  // other blocks still read them
+  if (static_cast<int64_t>(a->batch) * a->kv_heads >= int64_t(1) << 29) return JFA_ERR_INVALID_ARG;  // blocks of the grid
+  if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
+  int32_t* status = static_cast<int32_t*>(ws);
+  if (a->batch == 0) return cuda_status(launch_status_clear(status, stream));
+  return cuda_status(launch_cache_accept(*a, status, stream));
 }
 
 jfa_status jfa_selftest_wait_timeout(int32_t budget_us, void* ws, cudaStream_t stream) {

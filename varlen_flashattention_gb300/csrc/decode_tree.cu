@@ -1,0 +1,946 @@
+// Attention of a sequence's newest tokens, drafts of a tree or a plain chain,
+// over its paged bf16 cache (jfa_decode_tree).
+//
+// Rows are (node i, head of the group) pairs of one KV head; row (i, g) sees
+// every token t < C = L - n before the drafts and draft j iff bit j of mask_i:
+//   S = scale q K^T, P = softmax(S) over the visible, O = P V, LSE = ln sum exp S.
+//
+// A K and a V row of one KV head serve all rows of that head: 4 D bytes for
+// 4 D flops a row, so 64 rows are 64 flop per byte and 256 rows 256, against
+// 288 at which the tensor cores and HBM take the same time. Below that the
+// cache is read once at HBM's rate whatever the number of rows; the products
+// run on tcgen05 with the rows as M = 128.
+//
+// A CTA holds up to two tiles of 128 rows (a row group) and works as two
+// streams, each with its own score tile and accumulator in TMEM and its own
+// four softmax warps. With two row tiles a stream is a row tile and both read
+// every K / V tile; with one they take the K / V tiles in turn and are joined
+// at the end like two parts. So one stream's softmax runs while the other's
+// products do, and no stream ever waits for the other's maxima.
+//
+// All (sequence, KV head, row group) lines of 128-token tiles form one long
+// line, which is cut evenly into one range per CTA; a line that was cut leaves
+// partial results (normalised O, LSE) that a second kernel joins.
+//
+// Tiles are gathered by TMA through the page table: boxes of as many tokens as
+// lie side by side (the largest power of two that divides the page size), or,
+// for pages that 8 does not divide, four single rows at a time (gather4).
+// Drafts are the last tokens, so only a line's last one or two tiles have a
+// mask. In those V rows that some row may not see are checked first: what is
+// not finite there becomes 0 for the product, since 0 * NaN would reach every
+// row, and is added to the rows that do see it at the end.
+//
+// Roles (352 threads): warps 0-3 and 4-7 the streams' softmax and epilogue,
+// warp 8 K / V producer, warp 9 MMA issuer, warp 10 Q loads.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "jfa_internal.h"
+#include "ptx.cuh"
+
+namespace jfa {
+
+namespace {
+
+constexpr int kTreeThreads = 352;
+constexpr int kWarpKV = 8, kWarpMma = 9, kWarpQ = 10;
+constexpr float kLn2f = 0.6931471805599453f;
+
+struct TreeParams {
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  const int32_t* q_offsets;
+  const uint64_t* mask;  // may be null: a chain
+  const __nv_bfloat16* v_cache;
+  __nv_bfloat16* o;
+  float* lse;
+  TreeBuffers w;
+  int32_t batch, hq, hkv, group, page_size, num_pages, max_pages, total_q, max_q;
+  int32_t nodes_per_tile;  // nodes whose rows fit a tile: 128 / group
+  int32_t box;             // tokens of a box, or 1: rows are gathered
+  float scale_log2;
+  uint64_t budget_ns;
+};
+
+template <int D>
+struct TreeLayout {
+  static constexpr int kTileBytes = kTile * D * 2;  // a Q, K or V tile
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffSlots = 2 * kTileBytes;
+  static constexpr int kOffMl = kOffSlots + kSlots * kTileBytes;  // float2 (m, l) per stream and row
+  static constexpr int kOffBars = kOffMl + 2 * kTile * 8;
+  // slot_full[S], slot_empty[S], q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free, ml_full[2], drain
+  static constexpr int kNumBars = 2 * kSlots + 2 + 6 + 1 + 2 + 1;
+  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
+  static constexpr int kBytes = kOffMisc + 256;
+  static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // S: 128 columns a stream, O: D
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+// A CTA's share of one line.
+struct TreeItem {
+  int b, h, rg;
+  int t0, t1;      // tiles of the line
+  int nt;          // tiles of the whole line
+  int q0, n, L;    // first row of q, nodes, tokens
+  int two;         // two row tiles
+};
+
+// The sequence's new tokens and length; false where they are out of range (reported by the numbering).
+__device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, int& q0, int& n, int& L) {
+  q0 = p.q_offsets[b];
+  const int q1 = p.q_offsets[b + 1];
+  L = p.seqlens[b];
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_q && q1 - q0 <= p.max_q && L >= q1 - q0 &&
+                  L <= static_cast<int64_t>(p.num_pages ? p.max_pages : 0) * p.page_size && (b > 0 || q0 == 0);
+  n = ok ? q1 - q0 : 0;
+  return ok;
+}
+__device__ __forceinline__ int row_tiles(const TreeParams& p, int n) {
+  return (n + p.nodes_per_tile - 1) / p.nodes_per_tile;
+}
+// Tiles of all the sequence's lines.
+__device__ __forceinline__ int64_t seq_work(const TreeParams& p, int n, int L) {
+  if (n == 0) return 0;
+  return static_cast<int64_t>(p.hkv) * ((row_tiles(p, n) + 1) >> 1) * ((L + kTile - 1) / kTile);
+}
+
+// Walks the items of a range of the long line; a whole warp calls it.
+struct TreeWalk {
+  int b, h, rg, t, q0, n, L, nt, groups;
+  int64_t left;
+  __device__ __forceinline__ void open(const TreeParams& p, int b0, int64_t pos, int64_t len) {
+    left = len;
+    b = b0;
+    if (left <= 0) return;
+    seq(p);
+    const int64_t line = pos / nt;
+    t = static_cast<int>(pos % nt);
+    h = static_cast<int>(line / groups);
+    rg = static_cast<int>(line % groups);
+  }
+  __device__ __forceinline__ void seq(const TreeParams& p) {
+    tree_seq(p, b, q0, n, L);
+    nt = (L + kTile - 1) / kTile;
+    groups = (row_tiles(p, n) + 1) >> 1;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, TreeItem& I) {
+    if (left <= 0) return false;
+    I.b = b;
+    I.h = h;
+    I.rg = rg;
+    I.t0 = t;
+    I.nt = nt;
+    I.t1 = static_cast<int>(min(static_cast<int64_t>(nt), t + left));
+    I.q0 = q0;
+    I.n = n;
+    I.L = L;
+    I.two = row_tiles(p, n) - 2 * rg >= 2;
+    left -= I.t1 - I.t0;
+    if (left > 0) {
+      t = 0;
+      if (++rg == groups) {
+        rg = 0;
+        if (++h == p.hkv) {
+          h = 0;
+          // the next sequence with new tokens, 32 looked at together (there is one: tiles are left)
+          for (int from = b + 1;; from += 32) {
+            const int at = from + static_cast<int>(threadIdx.x & 31);
+            int aq = 0, an = 0, al = 0;
+            const bool some = at < p.batch && tree_seq(p, at, aq, an, al) && an > 0;
+            const uint32_t m = __ballot_sync(0xffffffffu, some);
+            if (m) {
+              const int src = __ffs(m) - 1;
+              b = from + src;
+              q0 = __shfl_sync(0xffffffffu, aq, src);
+              n = __shfl_sync(0xffffffffu, an, src);
+              L = __shfl_sync(0xffffffffu, al, src);
+              nt = (L + kTile - 1) / kTile;
+              groups = (row_tiles(p, n) + 1) >> 1;
+              break;
+            }
+            if (from >= p.batch) {  // only if the arrays changed under the call
+              left = 0;
+              break;
+            }
+          }
+        }
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          ptx::smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Four rows of the map's 2-D tensor (box one row high), side by side in shared memory.
+__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                            const int (&y)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5, %6, %7}], [%2];" ::"r"(ptx::smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+      : "memory");
+}
+
+// Eight bf16 values without infinities and NaN; the values of a word that are finite, 0 for the others.
+__device__ __forceinline__ bool all_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
+  return ok;
+}
+__device__ __forceinline__ uint32_t keep_finite(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Adds the non-finite values of the flagged drafts that a row sees to 32 of its columns
+// (rare: kept out of line).
+__device__ __noinline__ void add_not_finite(const TreeParams& p, const TreeItem& I, uint64_t flags, int D, int col,
+                                            float* o) {
+  while (flags) {
+    const int j = __ffsll(static_cast<long long>(flags)) - 1;
+    flags &= flags - 1;
+    const int t = I.L - I.n + j;
+    const int page = p.page_table[static_cast<int64_t>(I.b) * p.max_pages + t / p.page_size];
+    const int64_t row = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)
+                            ? static_cast<int64_t>(page) * p.page_size + t % p.page_size
+                            : t % p.page_size;
+    const __nv_bfloat16* v = p.v_cache + (row * p.hkv + I.h) * D + col;
+    for (int e = 0; e < 32; ++e) {
+      const float x = __bfloat162float(v[e]);
+      if (!(fabsf(x) < INFINITY)) o[e] += x;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    decode_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
+  using Lay = TreeLayout<D>;
+  constexpr int kSlots = Lay::kSlots;
+  constexpr int kAtoms = D / 64;  // 64-column atoms of a tile
+  constexpr int kHalf = D / 2;
+  constexpr uint32_t kIdS = ptx::idesc_bf16(kTile, kTile, false, false);  // S = Q K^T
+  constexpr uint32_t kIdPV = ptx::idesc_bf16(kTile, D, false, true);      // O += P V, P from TMEM
+
+  extern __shared__ uint8_t smem[];
+  uint64_t* slot_full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBars);
+  uint64_t* slot_empty = slot_full + kSlots;
+  uint64_t* q_full = slot_empty + kSlots;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* o_free = o_full + 2;
+  uint64_t* ml_full = o_free + 1;
+  uint64_t* drain = ml_full + 2;
+  float2* ml = reinterpret_cast<float2*>(smem + Lay::kOffMl);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc);
+  ptx::CtaCtl* ctl = reinterpret_cast<ptx::CtaCtl*>(smem + Lay::kOffMisc + 8);
+  int32_t* s_first = reinterpret_cast<int32_t*>(smem + Lay::kOffMisc + 16);     // first sequence of the range
+  int64_t* s_pos = reinterpret_cast<int64_t*>(smem + Lay::kOffMisc + 24);       // where in its lines the range begins
+  unsigned long long* s_flags = reinterpret_cast<unsigned long long*>(smem + Lay::kOffMisc + 32);  // [4]
+  int64_t* s_sum = reinterpret_cast<int64_t*>(smem + Lay::kOffMisc + 64);       // [kTreeThreads / 32] and the total
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  int32_t* status = p.w.cta_status + 2 * cta;
+  allow_next_grid();
+  if ((ptx::smem_u32(smem) & 1023) != 0) {  // not aligned enough for the layout
+    if (tid == 0) {
+      status[0] = JFA_ERR_UNSUPPORTED;
+      status[1] = 0;
+      if (cta == 0) *p.w.total = 0;
+    }
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(slot_full + i, 1);
+      ptx::mbar_init(slot_empty + i, 1);
+    }
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(s_full + i, 1);
+      ptx::mbar_init(p_full + i, 4);  // the stream's softmax warps
+      ptx::mbar_init(o_full + i, 1);
+      ptx::mbar_init(ml_full + i, 4);
+    }
+    ptx::mbar_init(o_free, 8);
+    ptx::mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) s_flags[i] = 0;
+    ctl->abort = 0;
+    status[0] = 0;
+    status[1] = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == kWarpKV && lane == 0) {
+    ptx::prefetch_tmap(&tm_q);
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+  }
+  if (warp == kWarpMma) {
+    ptx::tmem_alloc(tmem_slot, Lay::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  __syncthreads();  // the status words are cleared
+
+  // ---------------------------------------------------------------- numbering
+  // All tiles of all lines are summed, then the sequence in which this CTA's range begins is found.
+  int64_t total = 0;
+  {
+    int64_t mine = 0;
+    for (int b = tid; b < p.batch; b += kTreeThreads) {
+      int q0, n, L;
+      if (!tree_seq(p, b, q0, n, L)) {  // its rows are empty, a share of them a CTA
+        atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
+        atomicCAS(status + 1, 0, kSiteTreeInput);
+        const int64_t q1 = min(p.q_offsets[b + 1], p.total_q);
+        for (int64_t i = static_cast<int64_t>(max(q0, 0)) * p.hq + cta; i < q1 * p.hq; i += gridDim.x) {
+          p.lse[i] = -INFINITY;
+          for (int c = 0; c < D; c += 8) ptx::st_v4(p.o + i * D + c, 0, 0, 0, 0);
+        }
+      }
+      mine += seq_work(p, n, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTreeThreads / 32; ++i) total += s_sum[i];
+  }
+  // one range a CTA; with fewer tiles than CTAs the last ones have none
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  const int64_t begin = cta < ctas ? total * cta / ctas : total;
+  const int64_t end = cta < ctas ? total * (cta + 1) / ctas : total;
+  if (cta == 0 && tid == 0) *p.w.total = total;
+  if (begin < end) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kTreeThreads) {
+      int q0, n = 0, L = 0;
+      if (b0 + tid < p.batch) tree_seq(p, b0 + tid, q0, n, L);
+      const int64_t v = seq_work(p, n, L);
+      int64_t incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int i = 0; i < kTreeThreads / 32; ++i) {
+        if (i == warp) incl += base + all;
+        all += s_sum[i];
+      }
+      if (begin < incl && begin >= incl - v) {
+        *s_first = b0 + tid;
+        *s_pos = begin - (incl - v);
+      }
+      base += all;
+      if (base > begin) break;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint64_t budget = p.budget_ns;
+  TreeWalk walk;
+  walk.open(p, begin < end ? *s_first : 0, begin < end ? *s_pos : 0, end - begin);
+  if (tid == 0 && begin < end) {  // where this CTA's range begins, for the join
+    p.w.records[2 * cta] = make_int4(walk.b, walk.h, walk.rg, walk.t);
+    p.w.records[2 * cta + 1] =
+        make_int4(walk.nt, walk.q0, walk.n, row_tiles(p, walk.n) - 2 * walk.rg >= 2);
+  }
+  TreeItem I{};
+
+  if (warp == kWarpKV) {
+    // ------------------------------------------------------------ K / V producer
+    uint32_t pos = 0;
+    bool ok = true, bad = false;
+    const int box = p.box, boxes = kTile / box;
+    // rows of the [num_pages * page_size, hkv * D] view at which this lane's pieces of a tile begin
+    auto row_of = [&](int t) -> int {
+      const int pg = t / p.page_size;
+      int page = p.page_table[static_cast<int64_t>(I.b) * p.max_pages + pg];
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) {
+        bad = true;
+        page = 0;
+      }
+      return page * p.page_size + (t - pg * p.page_size);
+    };
+    auto load = [&](const CUtensorMap* map, int tile) -> bool {
+      const int tok = tile * kTile, valid = min(kTile, I.L - tok);
+      const uint32_t slot = pos % kSlots, round = pos / kSlots;
+      uint8_t* dst = smem + Lay::kOffSlots + slot * Lay::kTileBytes;
+      int y[4] = {0, 0, 0, 0};
+      int pieces;
+      if (box > 1) {  // boxes of `box` tokens, a lane a box and atom (what lies past the end in the last is masked)
+        pieces = (valid + box - 1) / box;
+        if ((lane & 15) < pieces) y[0] = row_of(tok + (lane & 15) * box);
+      } else {  // four tokens a lane; past the end the last token again
+        pieces = (valid + 3) / 4;
+        if (lane < pieces) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = row_of(min(tok + 4 * lane + e, I.L - 1));
+        }
+      }
+      if (!(ok = ptx::warp_all(
+                ptx::mbar_wait(slot_empty + slot, (round & 1) ^ 1, ctl, status, kSiteTreeProdSlot, budget))))
+        return false;
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(slot_full + slot, static_cast<uint32_t>(pieces * (box > 1 ? box : 4) * 128 * kAtoms));
+      __syncwarp();
+      if (box > 1) {
+        // boxes <= 16, so a half warp an atom
+        const int i = lane & 15, a = lane >> 4;
+        if (a < kAtoms && i < pieces && i < boxes)
+          ptx::tma_load_2d(dst + a * 16384 + i * box * 128, map, slot_full + slot, I.h * D + 64 * a, y[0]);
+      } else if (lane < pieces) {
+#pragma unroll
+        for (int a = 0; a < kAtoms; ++a)
+          tma_gather4(dst + a * 16384 + lane * 512, map, slot_full + slot, I.h * D + 64 * a, y);
+      }
+      __syncwarp();
+      ++pos;
+      return true;
+    };
+    while (ok && walk.next(p, I)) {
+      const int nt = I.t1 - I.t0, lead = I.two ? 1 : 2;
+      for (int t = 0; ok && t < min(lead, nt); ++t) load(&tm_k, I.t0 + t);
+      for (int t = 0; ok && t < nt; ++t) {
+        load(&tm_v, I.t0 + t);
+        if (ok && t + lead < nt) load(&tm_k, I.t0 + t + lead);
+      }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) {
+      atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
+      atomicCAS(status + 1, 0, kSiteTreeInput);
+    }
+    // after an abort some loads may have no consumer: none may be in flight when the CTA exits
+    if (lane == 0) {
+      ptx::CtaCtl no_abort{0, 0};
+      for (uint32_t i = pos > kSlots ? pos - kSlots : 0; i < pos; ++i)
+        ptx::mbar_wait(slot_full + i % kSlots, (i / kSlots) & 1, &no_abort, nullptr, kSiteTreeDrain, budget);
+    }
+    __syncwarp();
+  } else if (warp == kWarpQ) {
+    // ------------------------------------------------------------ Q loads
+    uint32_t it = 0;
+    const uint32_t bytes = static_cast<uint32_t>(p.nodes_per_tile * p.group) * 128 * kAtoms;
+    while (walk.next(p, I)) {
+      if (!ptx::warp_all(ptx::mbar_wait(q_empty, (it & 1) ^ 1, ctl, status, kSiteTreeProdQ, budget))) break;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(q_full, bytes * (I.two ? 2 : 1));
+        for (int m = 0; m < (I.two ? 2 : 1); ++m)
+#pragma unroll
+          for (int a = 0; a < kAtoms; ++a)
+            tma_load_3d(smem + Lay::kOffQ + m * Lay::kTileBytes + a * 16384, &tm_q, q_full, 64 * a, I.h * p.group,
+                        I.q0 + (2 * I.rg + m) * p.nodes_per_tile);
+      }
+      __syncwarp();
+      ++it;
+    }
+    if (lane == 0 && it > 0) {
+      ptx::CtaCtl no_abort{0, 0};
+      ptx::mbar_wait(q_full, (it - 1) & 1, &no_abort, nullptr, kSiteTreeDrain, budget);
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop; one elected lane issues.
+    uint32_t pos = 0, it = 0, np[2] = {0, 0};
+    bool ok = true;
+    auto slot_wait = [&]() -> uint32_t {
+      const uint32_t slot = pos % kSlots, round = pos / kSlots;
+      ok = ptx::warp_all(ptx::mbar_wait(slot_full + slot, round & 1, ctl, status, kSiteTreeMmaSlot, budget));
+      ptx::tc_fence_after();
+      ++pos;
+      return slot;
+    };
+    // S of stream g over the K tile in `slot`; free_slot and free_q: its last readers
+    auto issue_s = [&](int g, int qtile, uint32_t slot, bool free_slot, bool free_q) {
+      const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffQ + qtile * Lay::kTileBytes), 16, 1024);
+      const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffSlots + slot * Lay::kTileBytes), 16, 1024);
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          ptx::mma_ss(tmem + Lay::kColS + g * kTile, q_desc + (off >> 4), k_desc + (off >> 4), kIdS, kk > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(s_full + g);
+        if (free_slot) ptx::mma_commit(slot_empty + slot);
+        if (free_q) ptx::mma_commit(q_empty);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int g, uint32_t slot, bool first, bool last, bool free_slot) {
+      if (first && it > 0)  // the item before has been read out of the accumulators
+        ok = ptx::warp_all(ptx::mbar_wait(o_free, (it - 1) & 1, ctl, status, kSiteTreeMmaOFree, budget));
+      if (!ok) return;
+      ok = ptx::warp_all(ptx::mbar_wait(p_full + g, np[g] & 1, ctl, status, kSiteTreeMmaP, budget));
+      if (!ok) return;
+      ++np[g];
+      ptx::tc_fence_after();
+      const uint64_t v_desc =
+          ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffSlots + slot * Lay::kTileBytes), 16384, 1024);
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          ptx::mma_ts(tmem + Lay::kColO + g * D, tmem + Lay::kColS + g * kTile + kk * 8, v_desc + ((kk * 2048) >> 4),
+                      kIdPV, (!first || kk > 0) ? 1u : 0u);
+        if (free_slot) ptx::mma_commit(slot_empty + slot);
+        if (last) ptx::mma_commit(o_full + g);
+      }
+      __syncwarp();
+    };
+    while (ok && walk.next(p, I)) {
+      const int nt = I.t1 - I.t0;
+      ok = ptx::warp_all(ptx::mbar_wait(q_full, it & 1, ctl, status, kSiteTreeMmaQ, budget));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      uint32_t slot = slot_wait();
+      if (!ok) break;
+      if (I.two) {
+        issue_s(0, 0, slot, false, false);
+        issue_s(1, 1, slot, true, nt == 1);
+        for (int t = 0; ok && t < nt; ++t) {
+          const bool more = t + 1 < nt;
+          const uint32_t vs = slot_wait();
+          if (!ok) break;
+          issue_pv(0, vs, t == 0, !more, false);
+          if (!ok) break;
+          uint32_t ks = 0;
+          if (more) {
+            ks = slot_wait();
+            if (!ok) break;
+            issue_s(0, 0, ks, false, false);
+          }
+          issue_pv(1, vs, t == 0, !more, true);
+          if (!ok) break;
+          if (more) issue_s(1, 1, ks, true, t + 2 == nt);
+        }
+      } else {
+        issue_s(0, 0, slot, true, nt == 1);
+        if (nt > 1) {
+          slot = slot_wait();
+          if (!ok) break;
+          issue_s(1, 0, slot, true, nt == 2);
+        }
+        for (int t = 0; ok && t < nt; ++t) {
+          const uint32_t vs = slot_wait();
+          if (!ok) break;
+          issue_pv(t & 1, vs, t < 2, t + 2 >= nt, true);
+          if (ok && t + 2 < nt) {
+            slot = slot_wait();
+            if (!ok) break;
+            issue_s(t & 1, 0, slot, true, t + 3 == nt);
+          }
+        }
+      }
+      ++it;
+    }
+    if (ptx::elect_one()) ptx::mma_commit(drain);
+    __syncwarp();
+    ptx::CtaCtl no_abort{0, 0};
+    ptx::mbar_wait(drain, 0, &no_abort, nullptr, kSiteTreeDrain, budget);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and epilogue (warps 0-7)
+    const int g = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_base + Lay::kColS + g * kTile;
+    const uint32_t o_tmem = tmem + lane_base + Lay::kColO;
+    const int row_node = r / p.group, row_head = r % p.group;  // of this row in its tile
+    const float sl = p.scale_log2;
+    const uint64_t sl2 = ptx::f2_packf(sl, sl);
+    uint32_t ring = 0, ns = 0, it = 0;
+    uint32_t no0 = 0, no1 = 0, nml0 = 0, nml1 = 0;  // phases of o_full and ml_full so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t phase, int site) -> bool {  // the warp agrees, so that votes below are whole
+      return ok = ptx::warp_all(ptx::mbar_wait(bar, phase & 1, ctl, status, site, budget));
+    };
+    while (ok && walk.next(p, I)) {
+      const int nt = I.t1 - I.t0, C = I.L - I.n;
+      const int node = (2 * I.rg + (I.two ? g : 0)) * p.nodes_per_tile + row_node;
+      const bool row_ok = row_node < p.nodes_per_tile && node < I.n;
+      const bool active = __any_sync(0xffffffffu, row_ok);
+      uint64_t bits = 0;  // the drafts that this row sees
+      if (row_ok) {
+        bits = p.mask ? p.mask[I.q0 + node] : (~uint64_t(0) >> (63 - node));
+        bits &= ~uint64_t(0) >> (64 - I.n);
+      }
+      if (g == 0 && tid == 0) s_flags[(it + 2) & 3] = 0;
+      float m = -INFINITY, l = 0.f;
+      const int step = I.two ? 1 : 2;
+      for (int t = I.two ? 0 : g; t < nt; t += step) {
+        const int tok = (I.t0 + t) * kTile;
+        const bool masked = tok + kTile > C;
+        if (!wait(s_full + g, ns, kSiteTreeSoftS)) break;
+        ++ns;
+        ptx::tc_fence_after();
+        if (active) {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ptx::tmem_ld32(s_tmem + 32 * u, s[u]);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ptx::reg_fence32(s[u]);
+          if (masked) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int at = tok + 32 * u - C;  // draft number of the first of these columns
+              const uint32_t sees = at >= 64    ? 0u
+                                    : at >= 0   ? static_cast<uint32_t>(bits >> at)
+                                    : at <= -32 ? 0xffffffffu
+                                                : (static_cast<uint32_t>(bits << -at) | ((1u << -at) - 1u));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(sees >> e & 1)) s[u][e] = 0xff800000u;  // -inf
+            }
+          }
+          float mx8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mx8[(e >> 1) & 7] = ptx::fmax3(mx8[(e >> 1) & 7], __uint_as_float(s[u][e]), __uint_as_float(s[u][e + 1]));
+          const float mnew = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
+                                   ptx::fmax3(ptx::fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])) * sl;
+          if (t < step) {
+            m = mnew;
+          } else {
+            // O is rescaled only when the running maximum grows by more than 2^8; otherwise the
+            // old one stays the reference and P stays below 2^8.
+            const bool need = row_ok && mnew > m + 8.0f;
+            if (__any_sync(0xffffffffu, need)) {  // S of this tile is complete, so P V of the last one is
+              const float mm = need ? mnew : m;
+              const float f = need ? ptx::ex2(m - mm) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                ptx::tmem_ld32(o_tmem + g * D + 32 * c, ov);
+                ptx::tmem_ld_wait();
+                ptx::reg_fence32(ov);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+                ptx::tmem_st32(o_tmem + g * D + 32 * c, ov);
+              }
+              l *= f;
+              m = mm;
+            }
+          }
+          const float mu = m == -INFINITY ? 0.f : m;  // a row with no visible key yet keeps P = 0
+          const uint64_t nmu2 = ptx::f2_packf(-mu, -mu);
+          uint64_t ls2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[u][2 * e], s[u][2 * e + 1]), sl2, nmu2), x0, x1);
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              ls2[e & 3] = ptx::f2_add(ls2[e & 3], ptx::f2_packf(p0, p1));
+              pk[e] = ptx::pack_bf16(p0, p1);  // off by up to 2^-8 of a weight; the sum takes it unrounded
+            }
+            ptx::tmem_st16(s_tmem + 16 * u, pk);
+          }
+          float a0, a1;
+          ptx::f2_unpack(ptx::f2_add(ptx::f2_add(ls2[0], ls2[1]), ptx::f2_add(ls2[2], ls2[3])), a0, a1);
+          l += a0 + a1;
+        }
+        // V of a tile with drafts, by one stream's 128 threads: a token a thread
+        if (masked && !(I.two && g)) {
+          const uint32_t at = ring + min(t + (I.two ? 1 : 2), nt) + t;  // the ring position of this V
+          const uint32_t slot = at % kSlots;
+          if (!wait(slot_full + slot, at / kSlots, kSiteTreeSoftV)) break;
+          const int draft = tok + r - C;
+          if (draft >= 0) {
+            uint8_t* row = smem + Lay::kOffSlots + slot * Lay::kTileBytes + r * 128;
+            bool found = false;
+#pragma unroll
+            for (int a = 0; a < kAtoms; ++a)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {  // the swizzle only orders the eight chunks of a row: all are looked at
+                uint4* at16 = reinterpret_cast<uint4*>(row + a * 16384 + ((c ^ (r & 7)) << 4));
+                uint4 v = *at16;
+                if (!all_finite(v)) {
+                  if (!found && draft < I.n) atomicOr(s_flags + (it & 3), 1ull << draft);
+                  found = true;
+                  v.x = keep_finite(v.x);
+                  v.y = keep_finite(v.y);
+                  v.z = keep_finite(v.z);
+                  v.w = keep_finite(v.w);
+                  *at16 = v;
+                }
+              }
+            if (found) ptx::fence_proxy_async_smem();
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full + g);
+      }
+      if (!ok) break;
+      ring += 2 * nt;
+      // -------------------------------------------------------- the item's end
+      const bool whole = I.t0 == 0 && I.t1 == I.nt;
+      const int slot = 2 * cta + (I.t0 > 0 ? 0 : 1);  // a CTA's first item may continue a line, its last one be cut
+      const int mt = I.two ? g : 0;
+      const int64_t out_row = row_ok ? static_cast<int64_t>(I.q0 + node) * p.hq + I.h * p.group + row_head : 0;
+      float f0 = 0.f, f1 = 0.f, lse2 = -INFINITY;
+      const bool both = !I.two && nt > 1;  // one row tile, two streams to join
+      if ((I.two || g == 0 || both) && !wait(o_full + g, g ? no1 : no0, kSiteTreeSoftO)) break;
+      if (I.two) {
+        f0 = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
+        lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+      } else {
+        if (both || g == 0) {
+          ml[g * kTile + r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ml_full + g);
+        }
+        float2 o0 = make_float2(m, l), o1 = make_float2(-INFINITY, 0.f);
+        if (both || g == 1) {
+          const int og = 1 - g;
+          if (!wait(o_full + og, og ? no1 : no0, kSiteTreeSoftO)) break;
+          if (!wait(ml_full + og, og ? nml1 : nml0, kSiteTreeSoftMl)) break;
+          const float2 other = ml[og * kTile + r];
+          if (g == 0) {
+            o1 = other;
+          } else {
+            o1 = both ? o0 : o1;
+            o0 = other;
+          }
+        }
+        ++nml0;
+        if (both) ++nml1;
+        const float M = fmaxf(o0.x, o1.x), Mu = M == -INFINITY ? 0.f : M;
+        const float w0 = ptx::ex2(o0.x - Mu), w1 = ptx::ex2(o1.x - Mu);
+        const float sum = o0.y * w0 + o1.y * w1;
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        f0 = w0 * inv;
+        f1 = w1 * inv;
+        lse2 = sum == 0.f ? -INFINITY : M + log2f(sum);
+      }
+      ++no0;
+      if (I.two || both) ++no1;
+      ptx::tc_fence_after();
+      const uint64_t flagged = static_cast<uint64_t>(I.t1) * kTile > C ? (s_flags[it & 3] & bits) : 0;
+      // two row tiles: a stream reads its own accumulator; else both halves of the columns are shared out
+      const int c_begin = I.two ? 0 : g * kHalf, c_end = I.two ? D : c_begin + kHalf;
+      if (active) {
+#pragma unroll 1
+        for (int c = c_begin; c < c_end; c += 32) {
+          uint32_t ov[32];
+          ptx::tmem_ld32(o_tmem + (I.two ? g * D : 0) + c, ov);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(ov);
+          float of[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) of[e] = f0 == 0.f ? 0.f : __uint_as_float(ov[e]) * f0;
+          if (both) {
+            ptx::tmem_ld32(o_tmem + D + c, ov);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) of[e] += f1 == 0.f ? 0.f : __uint_as_float(ov[e]) * f1;
+          }
+          if (flagged) {
+            float tmp[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) tmp[e] = of[e];
+            add_not_finite(p, I, flagged, D, c, tmp);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) of[e] = tmp[e];
+          }
+          if (row_ok) {
+            if (whole) {
+              __nv_bfloat16* out = p.o + out_row * D + c;
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                ptx::st_v4(out + e, ptx::pack_bf16(of[e], of[e + 1]), ptx::pack_bf16(of[e + 2], of[e + 3]),
+                           ptx::pack_bf16(of[e + 4], of[e + 5]), ptx::pack_bf16(of[e + 6], of[e + 7]));
+            } else {  // [slot][row tile][D / 4][128 rows] of four columns: neighbouring lanes side by side
+              float4* out = reinterpret_cast<float4*>(p.w.part_o) +
+                            ((static_cast<int64_t>(slot) * p.w.row_tiles + mt) * (D / 4) + c / 4) * kTile + r;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                out[(e / 4) * kTile] = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
+            }
+          }
+        }
+        if (row_ok && (I.two || g == 0)) {
+          if (whole)
+            p.lse[out_row] = lse2 * kLn2f;
+          else
+            p.w.part_lse2[(static_cast<int64_t>(slot) * p.w.row_tiles + mt) * kTile + r] = lse2;
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(o_free);
+      ++it;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, Lay::kTmemCols);
+  }
+}
+
+// Joins the parts of the lines that were cut: lse = log2 sum 2^lse_p, O = sum 2^(lse_p - lse) O_p.
+// Block column x looks at the border between the ranges of CTA x and x + 1: if it is the first one
+// inside its line, the blocks (x, y) join that line, a thread eight columns of a row. The first
+// block also gathers the CTAs' findings.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_tree_join_kernel(const TreeParams p, int ctas_launched) {
+  wait_prior_grid();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+    int code = 0, site = 0;
+    for (int c = threadIdx.x; c < ctas_launched; c += 32)
+      if (code == 0 && p.w.cta_status[2 * c] != 0) {
+        code = p.w.cta_status[2 * c];
+        site = p.w.cta_status[2 * c + 1];
+      }
+    const uint32_t any = __ballot_sync(0xffffffffu, code != 0);
+    const int src = any ? __ffs(any) - 1 : 0;
+    code = __shfl_sync(0xffffffffu, code, src);
+    site = __shfl_sync(0xffffffffu, site, src);
+    for (int i = threadIdx.x; i < static_cast<int>(kStatusBytes / 4); i += 32)
+      p.w.status[i] = i == 0 ? code : (i == 1 ? site : 0);
+  }
+  const int64_t total = *p.w.total;
+  const int64_t ctas = min(static_cast<int64_t>(ctas_launched), total);
+  const int c = blockIdx.x + 1;
+  if (c >= ctas) return;
+  const int4 first = p.w.records[2 * c], rest = p.w.records[2 * c + 1];
+  const int t0 = first.w;
+  if (t0 == 0) return;  // a line begins at the border
+  const int64_t start = total * c / ctas, line = start - t0, line_end = line + rest.x;
+  if (total * (c - 1) / ctas > line) return;  // an earlier border lies inside this line
+  const int two = rest.w, rg = first.z, q0 = rest.y, n = rest.z;
+  const int item = blockIdx.y * kJoinThreads + threadIdx.x;  // [row tile][D / 8][128 rows]
+  const int r = item & (kTile - 1), chunk = (item >> 7) % (D / 8), mt = (item >> 7) / (D / 8);
+  if (mt > two) return;
+  const int row_node = r / p.group;
+  const int node = (2 * rg + mt) * p.nodes_per_tile + row_node;
+  if (row_node >= p.nodes_per_tile || node >= n) return;
+  // the parts: the last item of CTA c - 1, then the first ones of c, c + 1, .. up to the line's end
+  int last = c;
+  while (last + 1 < ctas && total * (last + 1) / ctas < line_end) ++last;
+  const int parts = last - c + 2;
+  auto slot_of = [&](int i) { return (i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * static_cast<int64_t>(p.w.row_tiles) + mt; };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) M = fmaxf(M, p.w.part_lse2[slot_of(i) * kTile + r]);
+  const float Mu = M == -INFINITY ? 0.f : M;
+  float sum = 0.f, acc[8] = {};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const int64_t slot = slot_of(i);
+    const float w = ptx::ex2(p.w.part_lse2[slot * kTile + r] - Mu);
+    const float4* o = reinterpret_cast<const float4*>(p.w.part_o) + (slot * (D / 4) + 2 * chunk) * kTile + r;
+    const float4 a = o[0], b = o[kTile];
+    sum += w;
+    if (w != 0.f) {
+      acc[0] += w * a.x;
+      acc[1] += w * a.y;
+      acc[2] += w * a.z;
+      acc[3] += w * a.w;
+      acc[4] += w * b.x;
+      acc[5] += w * b.y;
+      acc[6] += w * b.z;
+      acc[7] += w * b.w;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t row = static_cast<int64_t>(q0 + node) * p.hq + first.y * p.group + r % p.group;
+  ptx::st_v4(p.o + row * D + 8 * chunk, ptx::pack_bf16(acc[0] * inv, acc[1] * inv),
+             ptx::pack_bf16(acc[2] * inv, acc[3] * inv), ptx::pack_bf16(acc[4] * inv, acc[5] * inv),
+             ptx::pack_bf16(acc[6] * inv, acc[7] * inv));
+  if (chunk == 0) p.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2f;
+}
+
+template <int D>
+cudaError_t launch_tree_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                          int grid, void* events, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(decode_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TreeLayout<D>::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  cudaEvent_t* ev = static_cast<cudaEvent_t*>(events);
+  if (ev) cudaEventRecord(ev[0], stream);
+  decode_tree_kernel<D><<<grid, kTreeThreads, TreeLayout<D>::kBytes, stream>>>(tq, tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (ev) cudaEventRecord(ev[1], stream);
+  const int chunks = p.w.row_tiles * (D / 8) * kTile / kJoinThreads;
+  return launch_after(decode_tree_join_kernel<D>, dim3(std::max(grid - 1, 1), chunks), dim3(kJoinThreads), 0, stream, p,
+                      grid);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tree(const jfa_decode_tree_args& a, const TreeBuffers& w, const CUtensorMap& tq,
+                               const CUtensorMap& tk, const CUtensorMap& tv, int box, uint64_t budget_ns, int grid,
+                               cudaStream_t stream) {
+  TreeParams p{};
+  p.page_table = a.page_table;
+  p.seqlens = a.seqlens_k;
+  p.q_offsets = a.q_offsets;
+  p.mask = a.tree_mask;
+  p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.w = w;
+  p.batch = a.batch;
+  p.hq = a.q_heads;
+  p.hkv = a.kv_heads;
+  p.group = a.q_heads / a.kv_heads;
+  p.page_size = a.page_size;
+  p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages;
+  p.total_q = a.total_q;
+  p.max_q = a.max_q;
+  p.nodes_per_tile = tree_nodes_per_tile(p.group);
+  p.box = box;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.budget_ns = budget_ns;
+  return a.head_dim == 128 ? launch_tree_d<128>(tq, tk, tv, p, grid, a.main_kernel_events, stream)
+                           : launch_tree_d<64>(tq, tk, tv, p, grid, a.main_kernel_events, stream);
+}
+
+}  // namespace jfa

@@ -94,6 +94,20 @@ enum WaitSite : int32_t {
   kSiteFp8DecodeTable = 411,  // 8-bit cache decode: a length or page entry out of range
   kSiteFp8Append = 421,       // append: offsets, a length or a page entry out of range
   kSiteFp8Evict = 431,        // evict: a length or page entry out of range, or a new page that is in use
+  kSiteTreeInput = 501,       // tree decode: offsets, a length or a page entry out of range
+  kSiteTreeProdSlot = 511,
+  kSiteTreeProdQ = 512,
+  kSiteTreeMmaQ = 521,
+  kSiteTreeMmaSlot = 522,
+  kSiteTreeMmaP = 523,
+  kSiteTreeMmaOFree = 524,
+  kSiteTreeSoftS = 531,
+  kSiteTreeSoftV = 532,
+  kSiteTreeSoftO = 533,
+  kSiteTreeSoftMl = 534,
+  kSiteTreeDrain = 541,
+  kSiteAppendRope = 551,      // append with rotation: offsets, a length, a position or a page entry out of range
+  kSiteAccept = 561,          // accept: offsets, a length, a count, an index or a page entry out of range
   kSiteSelftestInput = 901,  // the self-test's first stage (its input never arrives)
   kSiteSelftestChain = 902,  // the self-test's second stage (should leave through the abort flag)
 };
@@ -248,6 +262,24 @@ cudaError_t launch_decode_fp8(const jfa_decode_fp8_args& a, const Fp8DecodeBuffe
 cudaError_t launch_cache_append_fp8(const jfa_cache_append_fp8_args& a, int32_t* status, cudaStream_t stream);
 cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint8_t* page_ok, int32_t* status, int sms,
                                    cudaStream_t stream);
+// Speculative decoding over the bf16 paged cache: tree attention, append with rotation, accept.
+struct TreeBuffers {
+  int32_t* status;
+  int64_t* total;       // tiles of the call
+  int32_t* cta_status;  // [grid][2]
+  int4* records;        // [grid][2]: (b, KV head, row group, first tile), (tiles of the line, first row, nodes, two row tiles)
+  float* part_lse2;     // [2 grid][row_tiles][128]
+  float* part_o;        // [2 grid][row_tiles][D / 4][128][4]
+  int32_t row_tiles;    // most row tiles of an item, 1 or 2
+};
+constexpr int kTreeMaxNodes = 64;
+// Nodes whose rows (one per head of the group) fit one tile of 128.
+__host__ __device__ inline int tree_nodes_per_tile(int group) { return kTile / group; }
+cudaError_t launch_decode_tree(const jfa_decode_tree_args& a, const TreeBuffers& w, const CUtensorMap& tq,
+                               const CUtensorMap& tk, const CUtensorMap& tv, int box, uint64_t budget_ns, int grid,
+                               cudaStream_t stream);
+cudaError_t launch_cache_append_rope(const jfa_cache_append_rope_args& a, int32_t* status, cudaStream_t stream);
+cudaError_t launch_cache_accept(const jfa_cache_accept_args& a, int32_t* status, cudaStream_t stream);
 // Clears a call's status block (a kernel, not a memset, so that the call's next
 // kernel can start as its programmatic dependent).
 cudaError_t launch_status_clear(int32_t* status, cudaStream_t stream);
