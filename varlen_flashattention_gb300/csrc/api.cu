@@ -1183,6 +1183,9 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   if (a->max_q > kTreeMaxNodes || a->q_heads / a->kv_heads > kTile) return JFA_ERR_UNSUPPORTED;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return JFA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(a->total_q) * a->q_heads >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
+  // tiles of a sequence's lines (at most 32 row groups a KV head) are numbered with 32 bits
+  const int64_t tiles = static_cast<int64_t>(a->max_pages) * a->page_size / kTile + 1;
+  if (tiles * a->kv_heads * 32 >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
   const bool work = a->batch > 0 && a->total_q > 0;
   if (work && (!aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4))) return JFA_ERR_INVALID_ARG;
   if (a->tree_mask && !aligned(a->tree_mask, 8)) return JFA_ERR_INVALID_ARG;
@@ -1198,7 +1201,7 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   if (ws_bytes < L.bytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
   TreeBuffers buf{};
   buf.status = reinterpret_cast<int32_t*>(w);
-  buf.total = reinterpret_cast<int64_t*>(w + L.total);
+  buf.total = reinterpret_cast<uint32_t*>(w + L.total);
   buf.cta_status = reinterpret_cast<int32_t*>(w + L.cta_status);
   buf.records = reinterpret_cast<int4*>(w + L.records);
   buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);

@@ -30,8 +30,11 @@
 // not finite there becomes 0 for the product, since 0 * NaN would reach every
 // row, and is added to the rows that do see it at the end.
 //
-// Roles (352 threads): warps 0-3 and 4-7 the streams' softmax and epilogue,
-// warp 8 K / V producer, warp 9 MMA issuer, warp 10 Q loads.
+// Roles (384 threads): warps 0-3 and 4-7 the streams' softmax and epilogue, warp
+// 8 K loads, warp 9 Q and V loads, warp 10 MMA issuer, warp 11 the scheduler,
+// which walks the CTA's range and hands its items to the others through a ring in
+// shared memory. (With a walk in each role, the code that only item borders run came
+// from DRAM again and again, past the stream of K and V in L2: an item cost 7.7 us.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -39,6 +42,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "fp8_cache.cuh"  // FastDiv
 #include "jfa_internal.h"
 #include "ptx.cuh"
 
@@ -46,8 +50,10 @@ namespace jfa {
 
 namespace {
 
-constexpr int kTreeThreads = 352;
-constexpr int kWarpKV = 8, kWarpMma = 9, kWarpQ = 10;
+constexpr int kTreeThreads = 384;
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpWalk = 11;
+constexpr int kItemRing = 4;       // items handed out ahead
+constexpr int kItemConsumers = 11;  // every warp but the scheduler
 constexpr float kLn2f = 0.6931471805599453f;
 
 struct TreeParams {
@@ -59,8 +65,10 @@ struct TreeParams {
   __nv_bfloat16* o;
   float* lse;
   TreeBuffers w;
-  int32_t batch, hq, hkv, group, page_size, num_pages, max_pages, total_q, max_q;
+  int32_t batch, hq, hkv, group, num_pages, max_pages, total_q, max_q;
   int32_t nodes_per_tile;  // nodes whose rows fit a tile: 128 / group
+  uint32_t node_tile_mul;  // 2^16 / nodes_per_tile + 1: x / nodes_per_tile = x * this >> 16 for x < 512
+  FastDiv page;            // division by page_size
   int32_t box;             // tokens of a box, or 1: rows are gathered
   float scale_log2;
   uint64_t budget_ns;
@@ -69,26 +77,28 @@ struct TreeParams {
 template <int D>
 struct TreeLayout {
   static constexpr int kTileBytes = kTile * D * 2;  // a Q, K or V tile
-  static constexpr int kSlots = D == 128 ? 5 : 10;
+  // K tiles are free once S is computed, V tiles wait for the softmax: three of the five slots that fit
+  static constexpr int kSlotsK = D == 128 ? 2 : 4, kSlotsV = D == 128 ? 3 : 6;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffSlots = 2 * kTileBytes;
-  static constexpr int kOffMl = kOffSlots + kSlots * kTileBytes;  // float2 (m, l) per stream and row
-  static constexpr int kOffBars = kOffMl + 2 * kTile * 8;
-  // slot_full[S], slot_empty[S], q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free, ml_full[2], drain
-  static constexpr int kNumBars = 2 * kSlots + 2 + 6 + 1 + 2 + 1;
+  static constexpr int kOffK = 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kSlotsK * kTileBytes;
+  static constexpr int kOffMl = kOffV + kSlotsV * kTileBytes;   // float2 (m, l) per stream and row
+  static constexpr int kOffItems = kOffMl + 2 * kTile * 8;      // int4[3] per item
+  static constexpr int kOffBars = kOffItems + kItemRing * 48;
+  // k_full, k_empty, v_full, v_empty, item_full, item_empty, q_full, q_empty, s_full[2], p_full[2], o_full[2],
+  // o_free, ml_full[2], drain
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kSlotsV + 2 * kItemRing + 2 + 6 + 1 + 2 + 1;
   static constexpr int kOffMisc = kOffBars + kNumBars * 8;
-  static constexpr int kBytes = kOffMisc + 256;
+  static constexpr int kBytes = kOffMisc + 192;
   static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // S: 128 columns a stream, O: D
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-// A CTA's share of one line.
+// A CTA's share of one line, as the scheduler hands it out (b = -1: the end).
 struct TreeItem {
-  int b, h, rg;
-  int t0, t1;      // tiles of the line
-  int nt;          // tiles of the whole line
-  int q0, n, L;    // first row of q, nodes, tokens
-  int two;         // two row tiles
+  int b, h, tile0, two;  // sequence, KV head, first row tile, two row tiles
+  int t0, t1, nt, L;     // tiles of the line, of how many, tokens
+  int q0, n;             // first row of q, nodes
 };
 
 // The sequence's new tokens and length; false where they are out of range (reported by the numbering).
@@ -97,77 +107,76 @@ __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, int& q0, in
   const int q1 = p.q_offsets[b + 1];
   L = p.seqlens[b];
   const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_q && q1 - q0 <= p.max_q && L >= q1 - q0 &&
-                  L <= static_cast<int64_t>(p.num_pages ? p.max_pages : 0) * p.page_size && (b > 0 || q0 == 0);
+                  L <= static_cast<int64_t>(p.num_pages ? p.max_pages : 0) * p.page.d && (b > 0 || q0 == 0);
   n = ok ? q1 - q0 : 0;
   return ok;
 }
 __device__ __forceinline__ int row_tiles(const TreeParams& p, int n) {
-  return (n + p.nodes_per_tile - 1) / p.nodes_per_tile;
+  return static_cast<int>((static_cast<uint32_t>(n + p.nodes_per_tile - 1) * p.node_tile_mul) >> 16);
 }
-// Tiles of all the sequence's lines.
-__device__ __forceinline__ int64_t seq_work(const TreeParams& p, int n, int L) {
+// Tiles of all the sequence's lines (below 2^31: the entry point sees to that).
+__device__ __forceinline__ uint32_t seq_work(const TreeParams& p, int n, int L) {
   if (n == 0) return 0;
-  return static_cast<int64_t>(p.hkv) * ((row_tiles(p, n) + 1) >> 1) * ((L + kTile - 1) / kTile);
+  return static_cast<uint32_t>(p.hkv) * ((row_tiles(p, n) + 1) >> 1) * static_cast<uint32_t>((L + kTile - 1) >> 7);
+}
+// Where CTA c's share of `total` tiles begins.
+__device__ __forceinline__ uint32_t share_begin(uint32_t total, uint32_t ctas, uint32_t c) {
+  const uint32_t each = total / ctas;
+  return c * each + min(c, total - each * ctas);
 }
 
 // Walks the items of a range of the long line; a whole warp calls it.
 struct TreeWalk {
   int b, h, rg, t, q0, n, L, nt, groups;
-  int64_t left;
-  __device__ __forceinline__ void open(const TreeParams& p, int b0, int64_t pos, int64_t len) {
+  uint32_t left;
+  __device__ __forceinline__ void open(const TreeParams& p, int b0, uint32_t pos, uint32_t len) {
     left = len;
     b = b0;
-    if (left <= 0) return;
-    seq(p);
-    const int64_t line = pos / nt;
-    t = static_cast<int>(pos % nt);
-    h = static_cast<int>(line / groups);
-    rg = static_cast<int>(line % groups);
-  }
-  __device__ __forceinline__ void seq(const TreeParams& p) {
     tree_seq(p, b, q0, n, L);
-    nt = (L + kTile - 1) / kTile;
+    nt = (L + kTile - 1) >> 7;
     groups = (row_tiles(p, n) + 1) >> 1;
+    const uint32_t line = pos / static_cast<uint32_t>(nt);
+    t = static_cast<int>(pos - line * nt);
+    h = static_cast<int>(line / static_cast<uint32_t>(groups));
+    rg = static_cast<int>(line) - h * groups;
   }
   __device__ __forceinline__ bool next(const TreeParams& p, TreeItem& I) {
-    if (left <= 0) return false;
+    if (left == 0) return false;
     I.b = b;
     I.h = h;
-    I.rg = rg;
+    I.tile0 = 2 * rg;
+    I.two = row_tiles(p, n) - 2 * rg >= 2;
     I.t0 = t;
+    I.t1 = t + static_cast<int>(min(static_cast<uint32_t>(nt - t), left));
     I.nt = nt;
-    I.t1 = static_cast<int>(min(static_cast<int64_t>(nt), t + left));
+    I.L = L;
     I.q0 = q0;
     I.n = n;
-    I.L = L;
-    I.two = row_tiles(p, n) - 2 * rg >= 2;
     left -= I.t1 - I.t0;
-    if (left > 0) {
-      t = 0;
-      if (++rg == groups) {
-        rg = 0;
-        if (++h == p.hkv) {
-          h = 0;
-          // the next sequence with new tokens, 32 looked at together (there is one: tiles are left)
-          for (int from = b + 1;; from += 32) {
-            const int at = from + static_cast<int>(threadIdx.x & 31);
-            int aq = 0, an = 0, al = 0;
-            const bool some = at < p.batch && tree_seq(p, at, aq, an, al) && an > 0;
-            const uint32_t m = __ballot_sync(0xffffffffu, some);
-            if (m) {
-              const int src = __ffs(m) - 1;
-              b = from + src;
-              q0 = __shfl_sync(0xffffffffu, aq, src);
-              n = __shfl_sync(0xffffffffu, an, src);
-              L = __shfl_sync(0xffffffffu, al, src);
-              nt = (L + kTile - 1) / kTile;
-              groups = (row_tiles(p, n) + 1) >> 1;
-              break;
-            }
-            if (from >= p.batch) {  // only if the arrays changed under the call
-              left = 0;
-              break;
-            }
+    t = 0;
+    if (left > 0 && ++rg == groups) {
+      rg = 0;
+      if (++h == p.hkv) {
+        h = 0;
+        // the next sequence with new tokens, 32 looked at together (there is one: tiles are left)
+        for (int from = b + 1;; from += 32) {
+          const int at = from + static_cast<int>(threadIdx.x & 31);
+          int aq = 0, an = 0, al = 0;
+          const bool some = at < p.batch && tree_seq(p, at, aq, an, al) && an > 0;
+          const uint32_t m = __ballot_sync(0xffffffffu, some);
+          if (m) {
+            const int src = __ffs(m) - 1;
+            b = from + src;
+            q0 = __shfl_sync(0xffffffffu, aq, src);
+            n = __shfl_sync(0xffffffffu, an, src);
+            L = __shfl_sync(0xffffffffu, al, src);
+            nt = (L + kTile - 1) >> 7;
+            groups = (row_tiles(p, n) + 1) >> 1;
+            break;
+          }
+          if (from >= p.batch) {  // only if the arrays changed under the call
+            left = 0;
+            break;
           }
         }
       }
@@ -216,10 +225,10 @@ __device__ __noinline__ void add_not_finite(const TreeParams& p, const TreeItem&
     const int j = __ffsll(static_cast<long long>(flags)) - 1;
     flags &= flags - 1;
     const int t = I.L - I.n + j;
-    const int page = p.page_table[static_cast<int64_t>(I.b) * p.max_pages + t / p.page_size];
-    const int64_t row = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)
-                            ? static_cast<int64_t>(page) * p.page_size + t % p.page_size
-                            : t % p.page_size;
+    const int pg = fast_div(t, p.page), slot = t - pg * static_cast<int>(p.page.d);
+    const int page = p.page_table[static_cast<int64_t>(I.b) * p.max_pages + pg];
+    const int64_t row =
+        static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages) ? static_cast<int64_t>(page) * p.page.d + slot : slot;
     const __nv_bfloat16* v = p.v_cache + (row * p.hkv + I.h) * D + col;
     for (int e = 0; e < 32; ++e) {
       const float x = __bfloat162float(v[e]);
@@ -233,16 +242,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
   using Lay = TreeLayout<D>;
-  constexpr int kSlots = Lay::kSlots;
+  constexpr int kSlotsK = Lay::kSlotsK, kSlotsV = Lay::kSlotsV;
   constexpr int kAtoms = D / 64;  // 64-column atoms of a tile
   constexpr int kHalf = D / 2;
   constexpr uint32_t kIdS = ptx::idesc_bf16(kTile, kTile, false, false);  // S = Q K^T
   constexpr uint32_t kIdPV = ptx::idesc_bf16(kTile, D, false, true);      // O += P V, P from TMEM
 
   extern __shared__ uint8_t smem[];
-  uint64_t* slot_full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBars);
-  uint64_t* slot_empty = slot_full + kSlots;
-  uint64_t* q_full = slot_empty + kSlots;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::kOffBars);
+  uint64_t* k_empty = k_full + kSlotsK;
+  uint64_t* v_full = k_empty + kSlotsK;
+  uint64_t* v_empty = v_full + kSlotsV;
+  uint64_t* item_full = v_empty + kSlotsV;
+  uint64_t* item_empty = item_full + kItemRing;
+  uint64_t* q_full = item_empty + kItemRing;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;
   uint64_t* p_full = s_full + 2;
@@ -251,12 +264,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint64_t* ml_full = o_free + 1;
   uint64_t* drain = ml_full + 2;
   float2* ml = reinterpret_cast<float2*>(smem + Lay::kOffMl);
+  int4* items = reinterpret_cast<int4*>(smem + Lay::kOffItems);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc);
   ptx::CtaCtl* ctl = reinterpret_cast<ptx::CtaCtl*>(smem + Lay::kOffMisc + 8);
   int32_t* s_first = reinterpret_cast<int32_t*>(smem + Lay::kOffMisc + 16);     // first sequence of the range
-  int64_t* s_pos = reinterpret_cast<int64_t*>(smem + Lay::kOffMisc + 24);       // where in its lines the range begins
+  uint32_t* s_pos = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc + 20);     // where in its lines the range begins
   unsigned long long* s_flags = reinterpret_cast<unsigned long long*>(smem + Lay::kOffMisc + 32);  // [4]
-  int64_t* s_sum = reinterpret_cast<int64_t*>(smem + Lay::kOffMisc + 64);       // [kTreeThreads / 32] and the total
+  unsigned long long* s_sum = reinterpret_cast<unsigned long long*>(smem + Lay::kOffMisc + 64);    // [kTreeThreads / 32]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
@@ -272,9 +286,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      ptx::mbar_init(slot_full + i, 1);
-      ptx::mbar_init(slot_empty + i, 1);
+    for (int i = 0; i < kSlotsK; ++i) {
+      ptx::mbar_init(k_full + i, 1);
+      ptx::mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < kSlotsV; ++i) {
+      ptx::mbar_init(v_full + i, 1);
+      ptx::mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < kItemRing; ++i) {
+      ptx::mbar_init(item_full + i, 1);
+      ptx::mbar_init(item_empty + i, kItemConsumers);
     }
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(q_empty, 1);
@@ -292,7 +314,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     status[1] = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == kWarpKV && lane == 0) {
+  if (warp == kWarpK && lane == 0) {
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
@@ -305,9 +327,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   // ---------------------------------------------------------------- numbering
   // All tiles of all lines are summed, then the sequence in which this CTA's range begins is found.
-  int64_t total = 0;
+  unsigned long long sum = 0;
+  uint32_t own = 0;  // tiles of the sequence that this thread numbers (its only one in batches up to the block)
   {
-    int64_t mine = 0;
+    unsigned long long mine = 0;
     for (int b = tid; b < p.batch; b += kTreeThreads) {
       int q0, n, L;
       if (!tree_seq(p, b, q0, n, L)) {  // its rows are empty, a share of them a CTA
@@ -319,47 +342,57 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int c = 0; c < D; c += 8) ptx::st_v4(p.o + i * D + c, 0, 0, 0, 0);
         }
       }
-      mine += seq_work(p, n, L);
+      own = seq_work(p, n, L);
+      mine += own;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) s_sum[warp] = mine;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kTreeThreads / 32; ++i) total += s_sum[i];
+    for (int i = 0; i < kTreeThreads / 32; ++i) sum += s_sum[i];
+  }
+  if (sum >= (1ull << 31)) {  // 2^31 tiles are 2^45 bytes of K and V at least: no device holds them
+    if (tid == 0) {
+      atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
+      atomicCAS(status + 1, 0, kSiteTreeInput);
+    }
+    sum = 0;
   }
   // one range a CTA; with fewer tiles than CTAs the last ones have none
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-  const int64_t begin = cta < ctas ? total * cta / ctas : total;
-  const int64_t end = cta < ctas ? total * (cta + 1) / ctas : total;
+  const uint32_t total = static_cast<uint32_t>(sum), ctas = min(gridDim.x, total);
+  const uint32_t begin = static_cast<uint32_t>(cta) < ctas ? share_begin(total, ctas, cta) : 0;
+  const uint32_t end = static_cast<uint32_t>(cta) < ctas ? share_begin(total, ctas, cta + 1) : 0;
   if (cta == 0 && tid == 0) *p.w.total = total;
   if (begin < end) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += kTreeThreads) {
-      int q0, n = 0, L = 0;
-      if (b0 + tid < p.batch) tree_seq(p, b0 + tid, q0, n, L);
-      const int64_t v = seq_work(p, n, L);
-      int64_t incl = v;
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < p.batch && base <= begin; b0 += kTreeThreads) {
+      uint32_t v = own;
+      if (p.batch > kTreeThreads) {
+        int q0, n = 0, L = 0;
+        if (b0 + tid < p.batch) tree_seq(p, b0 + tid, q0, n, L);
+        v = seq_work(p, n, L);
+      }
+      uint32_t incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
       }
       __syncthreads();
       if (lane == 31) s_sum[warp] = incl;
       __syncthreads();
-      int64_t all = 0;
+      uint32_t all = 0;
 #pragma unroll
       for (int i = 0; i < kTreeThreads / 32; ++i) {
         if (i == warp) incl += base + all;
-        all += s_sum[i];
+        all += static_cast<uint32_t>(s_sum[i]);
       }
       if (begin < incl && begin >= incl - v) {
         *s_first = b0 + tid;
         *s_pos = begin - (incl - v);
       }
       base += all;
-      if (base > begin) break;
     }
   }
   ptx::tc_fence_before();
@@ -367,72 +400,124 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint64_t budget = p.budget_ns;
-  TreeWalk walk;
-  walk.open(p, begin < end ? *s_first : 0, begin < end ? *s_pos : 0, end - begin);
-  if (tid == 0 && begin < end) {  // where this CTA's range begins, for the join
-    p.w.records[2 * cta] = make_int4(walk.b, walk.h, walk.rg, walk.t);
-    p.w.records[2 * cta + 1] =
-        make_int4(walk.nt, walk.q0, walk.n, row_tiles(p, walk.n) - 2 * walk.rg >= 2);
-  }
   TreeItem I{};
+  // The next item: entry k of the ring. False at the end, or when a wait gave up.
+  auto take = [&](uint32_t k) -> bool {
+    const uint32_t e = k % kItemRing;
+    if (!ptx::warp_all(ptx::mbar_wait(item_full + e, (k / kItemRing) & 1, ctl, status, kSiteTreeItem, budget)))
+      return false;
+    const int4 a = items[3 * e], c = items[3 * e + 1], d = items[3 * e + 2];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(item_empty + e);
+    I = TreeItem{a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w, d.x, d.y};
+    return I.b >= 0;
+  };
 
-  if (warp == kWarpKV) {
-    // ------------------------------------------------------------ K / V producer
-    uint32_t pos = 0;
+  if (warp == kWarpWalk) {
+    // ------------------------------------------------------------ scheduler
+    TreeWalk walk{};
+    if (begin < end) {
+      walk.open(p, *s_first, *s_pos, end - begin);
+      if (lane == 0) {  // where this CTA's range begins, for the join
+        p.w.records[2 * cta] = make_int4(walk.b, walk.h, walk.rg, walk.t);
+        p.w.records[2 * cta + 1] = make_int4(walk.nt, walk.q0, walk.n, row_tiles(p, walk.n) - 2 * walk.rg >= 2);
+      }
+    }
+    for (uint32_t k = 0;; ++k) {
+      TreeItem J{};
+      const bool more = walk.next(p, J);
+      const uint32_t e = k % kItemRing;
+      if (!ptx::warp_all(
+              ptx::mbar_wait(item_empty + e, ((k / kItemRing) & 1) ^ 1, ctl, status, kSiteTreeItem, budget)))
+        break;
+      if (lane == 0) {
+        items[3 * e] = make_int4(more ? J.b : -1, J.h, J.tile0, J.two);
+        items[3 * e + 1] = make_int4(J.t0, J.t1, J.nt, J.L);
+        items[3 * e + 2] = make_int4(J.q0, J.n, 0, 0);
+        ptx::mbar_arrive(item_full + e);  // release: the record is visible to the entry's waiters
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+  } else if (warp == kWarpK || warp == kWarpV) {
+    // ------------------------------------------------------------ K loads; Q and V loads
+    const bool is_v = warp == kWarpV;
+    const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    const uint32_t slots = is_v ? kSlotsV : kSlotsK;
+    uint8_t* ring = smem + (is_v ? Lay::kOffV : Lay::kOffK);
+    const uint32_t q_bytes = static_cast<uint32_t>(p.nodes_per_tile * p.group) * 128 * kAtoms;
+    uint32_t slot = 0, phase = 1, loads = 0, nq = 0;
     bool ok = true, bad = false;
-    const int box = p.box, boxes = kTile / box;
-    // rows of the [num_pages * page_size, hkv * D] view at which this lane's pieces of a tile begin
-    auto row_of = [&](int t) -> int {
-      const int pg = t / p.page_size;
-      int page = p.page_table[static_cast<int64_t>(I.b) * p.max_pages + pg];
+    const int box = p.box;
+    // The pieces of a tile whose pages this lane looks up: a box of tokens (as many lanes as boxes, once
+    // for each atom), or four single tokens; past the sequence's end its last token again.
+    auto page_of = [&](int t) -> int {
+      return p.page_table[static_cast<int64_t>(I.b) * p.max_pages + fast_div(t, p.page)];
+    };
+    auto row_of = [&](int t, int page) -> int {  // in the [num_pages * page_size, hkv * D] view
       if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) {
         bad = true;
         page = 0;
       }
-      return page * p.page_size + (t - pg * p.page_size);
+      return page * static_cast<int>(p.page.d) + t - fast_div(t, p.page) * static_cast<int>(p.page.d);
     };
-    auto load = [&](const CUtensorMap* map, int tile) -> bool {
-      const int tok = tile * kTile, valid = min(kTile, I.L - tok);
-      const uint32_t slot = pos % kSlots, round = pos / kSlots;
-      uint8_t* dst = smem + Lay::kOffSlots + slot * Lay::kTileBytes;
-      int y[4] = {0, 0, 0, 0};
-      int pieces;
-      if (box > 1) {  // boxes of `box` tokens, a lane a box and atom (what lies past the end in the last is masked)
-        pieces = (valid + box - 1) / box;
-        if ((lane & 15) < pieces) y[0] = row_of(tok + (lane & 15) * box);
-      } else {  // four tokens a lane; past the end the last token again
-        pieces = (valid + 3) / 4;
-        if (lane < pieces) {
+    auto token = [&](int tile, int e) -> int {
+      return min(tile * kTile + (box > 1 ? (lane & 15) * box : 4 * lane + e), I.L - 1);
+    };
+    for (uint32_t it = 0; ok && take(it); ++it) {
+      int pg[4];
+      const int per = box > 1 ? 1 : 4;
+      for (int e = 0; e < 4; ++e) pg[e] = e < per ? page_of(token(I.t0, e)) : 0;
+      if (is_v) {
+        ok = ptx::warp_all(ptx::mbar_wait(q_empty, (it & 1) ^ 1, ctl, status, kSiteTreeProdQ, budget));
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(q_full, q_bytes * (I.two ? 2 : 1));
+          for (int m = 0; m <= I.two; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = row_of(min(tok + 4 * lane + e, I.L - 1));
+            for (int a = 0; a < kAtoms; ++a)
+              tma_load_3d(smem + Lay::kOffQ + m * Lay::kTileBytes + a * 16384, &tm_q, q_full, 64 * a, I.h * p.group,
+                          I.q0 + (I.tile0 + m) * p.nodes_per_tile);
         }
+        __syncwarp();
+        ++nq;
       }
-      if (!(ok = ptx::warp_all(
-                ptx::mbar_wait(slot_empty + slot, (round & 1) ^ 1, ctl, status, kSiteTreeProdSlot, budget))))
-        return false;
-      if (lane == 0)
-        ptx::mbar_arrive_expect_tx(slot_full + slot, static_cast<uint32_t>(pieces * (box > 1 ? box : 4) * 128 * kAtoms));
-      __syncwarp();
-      if (box > 1) {
-        // boxes <= 16, so a half warp an atom
-        const int i = lane & 15, a = lane >> 4;
-        if (a < kAtoms && i < pieces && i < boxes)
-          ptx::tma_load_2d(dst + a * 16384 + i * box * 128, map, slot_full + slot, I.h * D + 64 * a, y[0]);
-      } else if (lane < pieces) {
+      const int x = I.h * D;
+      for (int t = I.t0; t < I.t1; ++t) {
+        const int valid = min(kTile, I.L - t * kTile);
+        int y[4];
 #pragma unroll
-        for (int a = 0; a < kAtoms; ++a)
-          tma_gather4(dst + a * 16384 + lane * 512, map, slot_full + slot, I.h * D + 64 * a, y);
-      }
-      __syncwarp();
-      ++pos;
-      return true;
-    };
-    while (ok && walk.next(p, I)) {
-      const int nt = I.t1 - I.t0, lead = I.two ? 1 : 2;
-      for (int t = 0; ok && t < min(lead, nt); ++t) load(&tm_k, I.t0 + t);
-      for (int t = 0; ok && t < nt; ++t) {
-        load(&tm_v, I.t0 + t);
-        if (ok && t + lead < nt) load(&tm_k, I.t0 + t + lead);
+        for (int e = 0; e < 4; ++e) y[e] = e == 0 || box == 1 ? row_of(token(t, e), pg[e]) : 0;
+        if (t + 1 < I.t1) {  // the next tile's pages, on their way while this one's slot is waited for
+          pg[0] = page_of(token(t + 1, 0));
+          if (box == 1) {
+#pragma unroll
+            for (int e = 1; e < 4; ++e) pg[e] = page_of(token(t + 1, e));
+          }
+        }
+        uint8_t* dst = ring + slot * Lay::kTileBytes;
+        ok = ptx::warp_all(ptx::mbar_wait(empty + slot, phase, ctl, status, kSiteTreeProdSlot, budget));
+        if (!ok) break;
+        const int pieces = box > 1 ? (valid + box - 1) / box : (valid + 3) >> 2;
+        if (lane == 0)
+          ptx::mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(pieces * (box > 1 ? box : 4) * 128 * kAtoms));
+        __syncwarp();
+        if (box > 1) {  // at most 16 boxes: a half warp an atom
+          const int i = lane & 15, a = lane >> 4;
+          if (a < kAtoms && i < pieces)
+            ptx::tma_load_2d(dst + a * 16384 + i * box * 128, map, full + slot, x + 64 * a, y[0]);
+        } else if (lane < pieces) {
+#pragma unroll
+          for (int a = 0; a < kAtoms; ++a) tma_gather4(dst + a * 16384 + lane * 512, map, full + slot, x + 64 * a, y);
+        }
+        __syncwarp();
+        ++loads;
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) {
@@ -442,48 +527,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // after an abort some loads may have no consumer: none may be in flight when the CTA exits
     if (lane == 0) {
       ptx::CtaCtl no_abort{0, 0};
-      for (uint32_t i = pos > kSlots ? pos - kSlots : 0; i < pos; ++i)
-        ptx::mbar_wait(slot_full + i % kSlots, (i / kSlots) & 1, &no_abort, nullptr, kSiteTreeDrain, budget);
-    }
-    __syncwarp();
-  } else if (warp == kWarpQ) {
-    // ------------------------------------------------------------ Q loads
-    uint32_t it = 0;
-    const uint32_t bytes = static_cast<uint32_t>(p.nodes_per_tile * p.group) * 128 * kAtoms;
-    while (walk.next(p, I)) {
-      if (!ptx::warp_all(ptx::mbar_wait(q_empty, (it & 1) ^ 1, ctl, status, kSiteTreeProdQ, budget))) break;
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full, bytes * (I.two ? 2 : 1));
-        for (int m = 0; m < (I.two ? 2 : 1); ++m)
-#pragma unroll
-          for (int a = 0; a < kAtoms; ++a)
-            tma_load_3d(smem + Lay::kOffQ + m * Lay::kTileBytes + a * 16384, &tm_q, q_full, 64 * a, I.h * p.group,
-                        I.q0 + (2 * I.rg + m) * p.nodes_per_tile);
-      }
-      __syncwarp();
-      ++it;
-    }
-    if (lane == 0 && it > 0) {
-      ptx::CtaCtl no_abort{0, 0};
-      ptx::mbar_wait(q_full, (it - 1) & 1, &no_abort, nullptr, kSiteTreeDrain, budget);
+      for (uint32_t i = loads > slots ? loads - slots : 0; i < loads; ++i)
+        ptx::mbar_wait(full + i % slots, (i / slots) & 1, &no_abort, nullptr, kSiteTreeDrain, budget);
+      if (nq > 0) ptx::mbar_wait(q_full, (nq - 1) & 1, &no_abort, nullptr, kSiteTreeDrain, budget);
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop; one elected lane issues.
-    uint32_t pos = 0, it = 0, np[2] = {0, 0};
+    uint32_t it = 0, np[2] = {0, 0}, kslot = 0, kphase = 0, vslot = 0, vphase = 0;
     bool ok = true;
-    auto slot_wait = [&]() -> uint32_t {
-      const uint32_t slot = pos % kSlots, round = pos / kSlots;
-      ok = ptx::warp_all(ptx::mbar_wait(slot_full + slot, round & 1, ctl, status, kSiteTreeMmaSlot, budget));
+    auto k_wait = [&]() -> uint32_t {
+      const uint32_t slot = kslot;
+      ok = ptx::warp_all(ptx::mbar_wait(k_full + slot, kphase, ctl, status, kSiteTreeMmaSlot, budget));
       ptx::tc_fence_after();
-      ++pos;
+      if (++kslot == kSlotsK) {
+        kslot = 0;
+        kphase ^= 1;
+      }
+      return slot;
+    };
+    auto v_wait = [&]() -> uint32_t {
+      const uint32_t slot = vslot;
+      ok = ptx::warp_all(ptx::mbar_wait(v_full + slot, vphase, ctl, status, kSiteTreeMmaSlot, budget));
+      ptx::tc_fence_after();
+      if (++vslot == kSlotsV) {
+        vslot = 0;
+        vphase ^= 1;
+      }
       return slot;
     };
     // S of stream g over the K tile in `slot`; free_slot and free_q: its last readers
     auto issue_s = [&](int g, int qtile, uint32_t slot, bool free_slot, bool free_q) {
       const uint64_t q_desc = ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffQ + qtile * Lay::kTileBytes), 16, 1024);
-      const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffSlots + slot * Lay::kTileBytes), 16, 1024);
+      const uint64_t k_desc = ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffK + slot * Lay::kTileBytes), 16, 1024);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -491,7 +568,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           ptx::mma_ss(tmem + Lay::kColS + g * kTile, q_desc + (off >> 4), k_desc + (off >> 4), kIdS, kk > 0 ? 1u : 0u);
         }
         ptx::mma_commit(s_full + g);
-        if (free_slot) ptx::mma_commit(slot_empty + slot);
+        if (free_slot) ptx::mma_commit(k_empty + slot);
         if (free_q) ptx::mma_commit(q_empty);
       }
       __syncwarp();
@@ -505,36 +582,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       ++np[g];
       ptx::tc_fence_after();
       const uint64_t v_desc =
-          ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffSlots + slot * Lay::kTileBytes), 16384, 1024);
+          ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffV + slot * Lay::kTileBytes), 16384, 1024);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           ptx::mma_ts(tmem + Lay::kColO + g * D, tmem + Lay::kColS + g * kTile + kk * 8, v_desc + ((kk * 2048) >> 4),
                       kIdPV, (!first || kk > 0) ? 1u : 0u);
-        if (free_slot) ptx::mma_commit(slot_empty + slot);
+        if (free_slot) ptx::mma_commit(v_empty + slot);
         if (last) ptx::mma_commit(o_full + g);
       }
       __syncwarp();
     };
-    while (ok && walk.next(p, I)) {
+    while (ok && take(it)) {
       const int nt = I.t1 - I.t0;
       ok = ptx::warp_all(ptx::mbar_wait(q_full, it & 1, ctl, status, kSiteTreeMmaQ, budget));
       if (!ok) break;
       ptx::tc_fence_after();
-      uint32_t slot = slot_wait();
+      uint32_t slot = k_wait();
       if (!ok) break;
       if (I.two) {
         issue_s(0, 0, slot, false, false);
         issue_s(1, 1, slot, true, nt == 1);
         for (int t = 0; ok && t < nt; ++t) {
           const bool more = t + 1 < nt;
-          const uint32_t vs = slot_wait();
+          const uint32_t vs = v_wait();
           if (!ok) break;
           issue_pv(0, vs, t == 0, !more, false);
           if (!ok) break;
           uint32_t ks = 0;
           if (more) {
-            ks = slot_wait();
+            ks = k_wait();
             if (!ok) break;
             issue_s(0, 0, ks, false, false);
           }
@@ -545,16 +622,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       } else {
         issue_s(0, 0, slot, true, nt == 1);
         if (nt > 1) {
-          slot = slot_wait();
+          slot = k_wait();
           if (!ok) break;
           issue_s(1, 0, slot, true, nt == 2);
         }
         for (int t = 0; ok && t < nt; ++t) {
-          const uint32_t vs = slot_wait();
+          const uint32_t vs = v_wait();
           if (!ok) break;
           issue_pv(t & 1, vs, t < 2, t + 2 >= nt, true);
           if (ok && t + 2 < nt) {
-            slot = slot_wait();
+            slot = k_wait();
             if (!ok) break;
             issue_s(t & 1, 0, slot, true, t + 3 == nt);
           }
@@ -577,15 +654,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int row_node = r / p.group, row_head = r % p.group;  // of this row in its tile
     const float sl = p.scale_log2;
     const uint64_t sl2 = ptx::f2_packf(sl, sl);
-    uint32_t ring = 0, ns = 0, it = 0;
+    uint32_t nv = 0, ns = 0, it = 0;
     uint32_t no0 = 0, no1 = 0, nml0 = 0, nml1 = 0;  // phases of o_full and ml_full so far
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase, int site) -> bool {  // the warp agrees, so that votes below are whole
       return ok = ptx::warp_all(ptx::mbar_wait(bar, phase & 1, ctl, status, site, budget));
     };
-    while (ok && walk.next(p, I)) {
+    while (ok && take(it)) {
       const int nt = I.t1 - I.t0, C = I.L - I.n;
-      const int node = (2 * I.rg + (I.two ? g : 0)) * p.nodes_per_tile + row_node;
+      const int node = (I.tile0 + (I.two ? g : 0)) * p.nodes_per_tile + row_node;
       const bool row_ok = row_node < p.nodes_per_tile && node < I.n;
       const bool active = __any_sync(0xffffffffu, row_ok);
       uint64_t bits = 0;  // the drafts that this row sees
@@ -603,25 +680,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ++ns;
         ptx::tc_fence_after();
         if (active) {
-          uint32_t s[4][32];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) ptx::tmem_ld32(s_tmem + 32 * u, s[u]);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 4; ++u) ptx::reg_fence32(s[u]);
-          if (masked) {
-#pragma unroll
+          if (masked) {  // -inf for what a row does not see (rolled: this code is cold)
+#pragma unroll 1
             for (int u = 0; u < 4; ++u) {
               const int at = tok + 32 * u - C;  // draft number of the first of these columns
               const uint32_t sees = at >= 64    ? 0u
                                     : at >= 0   ? static_cast<uint32_t>(bits >> at)
                                     : at <= -32 ? 0xffffffffu
                                                 : (static_cast<uint32_t>(bits << -at) | ((1u << -at) - 1u));
+              uint32_t sv[32];
+              ptx::tmem_ld32(s_tmem + 32 * u, sv);
+              ptx::tmem_ld_wait();
+              ptx::reg_fence32(sv);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(sees >> e & 1)) s[u][e] = 0xff800000u;  // -inf
+                if (!(sees >> e & 1)) sv[e] = 0xff800000u;
+              ptx::tmem_st32(s_tmem + 32 * u, sv);
             }
+            ptx::tmem_st_wait();
           }
+          uint32_t s[4][32];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ptx::tmem_ld32(s_tmem + 32 * u, s[u]);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ptx::reg_fence32(s[u]);
           float mx8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
@@ -677,29 +760,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         // V of a tile with drafts, by one stream's 128 threads: a token a thread
         if (masked && !(I.two && g)) {
-          const uint32_t at = ring + min(t + (I.two ? 1 : 2), nt) + t;  // the ring position of this V
-          const uint32_t slot = at % kSlots;
-          if (!wait(slot_full + slot, at / kSlots, kSiteTreeSoftV)) break;
+          const uint32_t slot = (nv + t) % kSlotsV;
+          if (!wait(v_full + slot, (nv + t) / kSlotsV, kSiteTreeSoftV)) break;
           const int draft = tok + r - C;
           if (draft >= 0) {
-            uint8_t* row = smem + Lay::kOffSlots + slot * Lay::kTileBytes + r * 128;
+            uint8_t* row = smem + Lay::kOffV + slot * Lay::kTileBytes + r * 128;
             bool found = false;
+#pragma unroll 1
+            for (int c = 0; c < 8 * kAtoms; c += 4) {  // the swizzle only orders a row's chunks: all are looked at
+              uint4 v[4];
 #pragma unroll
-            for (int a = 0; a < kAtoms; ++a)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {  // the swizzle only orders the eight chunks of a row: all are looked at
-                uint4* at16 = reinterpret_cast<uint4*>(row + a * 16384 + ((c ^ (r & 7)) << 4));
-                uint4 v = *at16;
-                if (!all_finite(v)) {
-                  if (!found && draft < I.n) atomicOr(s_flags + (it & 3), 1ull << draft);
-                  found = true;
-                  v.x = keep_finite(v.x);
-                  v.y = keep_finite(v.y);
-                  v.z = keep_finite(v.z);
-                  v.w = keep_finite(v.w);
-                  *at16 = v;
-                }
+              for (int e = 0; e < 4; ++e)
+                v[e] = *reinterpret_cast<uint4*>(row + ((c + e) >> 3) * 16384 + ((((c + e) & 7) ^ (r & 7)) << 4));
+              if (all_finite(v[0]) && all_finite(v[1]) && all_finite(v[2]) && all_finite(v[3])) continue;
+              if (!found && draft < I.n) atomicOr(s_flags + (it & 3), 1ull << draft);
+              found = true;
+#pragma unroll 1
+              for (int e = 0; e < 4; ++e) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(row + ((c + e) >> 3) * 16384 + ((((c + e) & 7) ^ (r & 7)) << 4));
+                for (int i = 0; i < 4; ++i) w[i] = keep_finite(w[i]);
               }
+            }
             if (found) ptx::fence_proxy_async_smem();
           }
         }
@@ -709,10 +790,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) ptx::mbar_arrive(p_full + g);
       }
       if (!ok) break;
-      ring += 2 * nt;
+      nv += nt;
       // -------------------------------------------------------- the item's end
       const bool whole = I.t0 == 0 && I.t1 == I.nt;
-      const int slot = 2 * cta + (I.t0 > 0 ? 0 : 1);  // a CTA's first item may continue a line, its last one be cut
+      const int64_t slot = 2 * cta + (I.t0 > 0 ? 0 : 1);  // a CTA's first item may continue a line, its last one be cut
       const int mt = I.two ? g : 0;
       const int64_t out_row = row_ok ? static_cast<int64_t>(I.q0 + node) * p.hq + I.h * p.group + row_head : 0;
       float f0 = 0.f, f1 = 0.f, lse2 = -INFINITY;
@@ -790,7 +871,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                            ptx::pack_bf16(of[e + 4], of[e + 5]), ptx::pack_bf16(of[e + 6], of[e + 7]));
             } else {  // [slot][row tile][D / 4][128 rows] of four columns: neighbouring lanes side by side
               float4* out = reinterpret_cast<float4*>(p.w.part_o) +
-                            ((static_cast<int64_t>(slot) * p.w.row_tiles + mt) * (D / 4) + c / 4) * kTile + r;
+                            ((slot * p.w.row_tiles + mt) * (D / 4) + c / 4) * kTile + r;
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 out[(e / 4) * kTile] = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
@@ -801,7 +882,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (whole)
             p.lse[out_row] = lse2 * kLn2f;
           else
-            p.w.part_lse2[(static_cast<int64_t>(slot) * p.w.row_tiles + mt) * kTile + r] = lse2;
+            p.w.part_lse2[(slot * p.w.row_tiles + mt) * kTile + r] = lse2;
         }
       }
       ptx::tc_fence_before();
@@ -841,15 +922,14 @@ __global__ void __launch_bounds__(kJoinThreads) decode_tree_join_kernel(const Tr
     for (int i = threadIdx.x; i < static_cast<int>(kStatusBytes / 4); i += 32)
       p.w.status[i] = i == 0 ? code : (i == 1 ? site : 0);
   }
-  const int64_t total = *p.w.total;
-  const int64_t ctas = min(static_cast<int64_t>(ctas_launched), total);
-  const int c = blockIdx.x + 1;
+  const uint32_t total = *p.w.total, ctas = min(static_cast<uint32_t>(ctas_launched), total);
+  const uint32_t c = blockIdx.x + 1;
   if (c >= ctas) return;
   const int4 first = p.w.records[2 * c], rest = p.w.records[2 * c + 1];
   const int t0 = first.w;
   if (t0 == 0) return;  // a line begins at the border
-  const int64_t start = total * c / ctas, line = start - t0, line_end = line + rest.x;
-  if (total * (c - 1) / ctas > line) return;  // an earlier border lies inside this line
+  const uint32_t line = share_begin(total, ctas, c) - t0, line_end = line + rest.x;
+  if (share_begin(total, ctas, c - 1) > line) return;  // an earlier border lies inside this line
   const int two = rest.w, rg = first.z, q0 = rest.y, n = rest.z;
   const int item = blockIdx.y * kJoinThreads + threadIdx.x;  // [row tile][D / 8][128 rows]
   const int r = item & (kTile - 1), chunk = (item >> 7) % (D / 8), mt = (item >> 7) / (D / 8);
@@ -858,10 +938,10 @@ __global__ void __launch_bounds__(kJoinThreads) decode_tree_join_kernel(const Tr
   const int node = (2 * rg + mt) * p.nodes_per_tile + row_node;
   if (row_node >= p.nodes_per_tile || node >= n) return;
   // the parts: the last item of CTA c - 1, then the first ones of c, c + 1, .. up to the line's end
-  int last = c;
-  while (last + 1 < ctas && total * (last + 1) / ctas < line_end) ++last;
-  const int parts = last - c + 2;
-  auto slot_of = [&](int i) { return (i == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + i)) * static_cast<int64_t>(p.w.row_tiles) + mt; };
+  uint32_t last = c;
+  while (last + 1 < ctas && share_begin(total, ctas, last + 1) < line_end) ++last;
+  const int parts = static_cast<int>(last - c) + 2;
+  auto slot_of = [&](int i) -> int64_t { return (i == 0 ? 2 * c - 1 : 2 * (c - 1 + i)) * static_cast<int64_t>(p.w.row_tiles) + mt; };
   float M = -INFINITY;
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) M = fmaxf(M, p.w.part_lse2[slot_of(i) * kTile + r]);
@@ -930,12 +1010,13 @@ cudaError_t launch_decode_tree(const jfa_decode_tree_args& a, const TreeBuffers&
   p.hq = a.q_heads;
   p.hkv = a.kv_heads;
   p.group = a.q_heads / a.kv_heads;
-  p.page_size = a.page_size;
+  p.page = make_fast_div(a.page_size);
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;
   p.total_q = a.total_q;
   p.max_q = a.max_q;
   p.nodes_per_tile = tree_nodes_per_tile(p.group);
+  p.node_tile_mul = 65536u / static_cast<uint32_t>(p.nodes_per_tile) + 1;
   p.box = box;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.budget_ns = budget_ns;

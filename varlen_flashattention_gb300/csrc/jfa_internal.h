@@ -106,6 +106,7 @@ enum WaitSite : int32_t {
   kSiteTreeSoftO = 533,
   kSiteTreeSoftMl = 534,
   kSiteTreeDrain = 541,
+  kSiteTreeItem = 542,
   kSiteAppendRope = 551,      // append with rotation: offsets, a length, a position or a page entry out of range
   kSiteAccept = 561,          // accept: offsets, a length, a count, an index or a page entry out of range
   kSiteSelftestInput = 901,  // the self-test's first stage (its input never arrives)
@@ -265,7 +266,7 @@ cudaError_t launch_cache_evict_fp8(const jfa_cache_evict_fp8_args& a, uint8_t* p
 // Speculative decoding over the bf16 paged cache: tree attention, append with rotation, accept.
 struct TreeBuffers {
   int32_t* status;
-  int64_t* total;       // tiles of the call
+  uint32_t* total;      // tiles of the call
   int32_t* cta_status;  // [grid][2]
   int4* records;        // [grid][2]: (b, KV head, row group, first tile), (tiles of the line, first row, nodes, two row tiles)
   float* part_lse2;     // [2 grid][row_tiles][128]
