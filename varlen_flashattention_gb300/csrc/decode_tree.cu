@@ -217,22 +217,27 @@ __device__ __forceinline__ uint32_t keep_finite(uint32_t w) {
   return w;
 }
 
-// Adds the non-finite values of the flagged drafts that a row sees to 32 of its columns
-// (rare: kept out of line).
-__device__ __noinline__ void add_not_finite(const TreeParams& p, const TreeItem& I, uint64_t flags, int D, int col,
-                                            float* o) {
+// Adds the non-finite values of the flagged drafts that a row sees to columns c .. end of what it has
+// written: its row of O, or its partial result (rare: kept out of line, and off the registers of the
+// item's end).
+__device__ __noinline__ void add_not_finite(const TreeParams& p, int b, int kv_row, int first, uint64_t flags, int D,
+                                            int c, int end, __nv_bfloat16* whole, float* part) {
   while (flags) {
-    const int j = __ffsll(static_cast<long long>(flags)) - 1;
+    const int t = first + __ffsll(static_cast<long long>(flags)) - 1;
     flags &= flags - 1;
-    const int t = I.L - I.n + j;
     const int pg = fast_div(t, p.page), slot = t - pg * static_cast<int>(p.page.d);
-    const int page = p.page_table[static_cast<int64_t>(I.b) * p.max_pages + pg];
+    const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + pg];
     const int64_t row =
         static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages) ? static_cast<int64_t>(page) * p.page.d + slot : slot;
-    const __nv_bfloat16* v = p.v_cache + (row * p.hkv + I.h) * D + col;
-    for (int e = 0; e < 32; ++e) {
+    const __nv_bfloat16* v = p.v_cache + (row * p.hkv + kv_row) * D;
+#pragma unroll 1
+    for (int e = c; e < end; ++e) {
       const float x = __bfloat162float(v[e]);
-      if (!(fabsf(x) < INFINITY)) o[e] += x;
+      if (fabsf(x) < INFINITY) continue;
+      if (whole)
+        whole[e] = __float2bfloat16(__bfloat162float(whole[e]) + x);
+      else
+        part[(e / 4) * 4 * kTile + e % 4] += x;
     }
   }
 }
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (ptx::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          ptx::mma_ts(tmem + Lay::kColO + g * D, tmem + Lay::kColS + g * kTile + kk * 8, v_desc + ((kk * 2048) >> 4),
+          ptx::mma_ts(tmem + Lay::kColO + g * D, tmem + Lay::kColS + g * kTile + 64 + kk * 8, v_desc + ((kk * 2048) >> 4),
                       kIdPV, (!first || kk > 0) ? 1u : 0u);
         if (free_slot) ptx::mma_commit(v_empty + slot);
         if (last) ptx::mma_commit(o_full + g);
@@ -699,20 +704,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             ptx::tmem_st_wait();
           }
-          uint32_t s[4][32];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) ptx::tmem_ld32(s_tmem + 32 * u, s[u]);
+          // The row's maximum, half by half; the upper half stays in registers, the lower one is read again
+          // (128 scores at once spill, and the spills, past a full L1, cost more than the second read).
+          uint32_t sa[2][32], sb[2][32];
+          ptx::tmem_ld32(s_tmem, sa[0]);
+          ptx::tmem_ld32(s_tmem + 32, sa[1]);
           ptx::tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 4; ++u) ptx::reg_fence32(s[u]);
+          ptx::reg_fence32(sa[0]);
+          ptx::reg_fence32(sa[1]);
+          ptx::tmem_ld32(s_tmem + 64, sb[0]);
+          ptx::tmem_ld32(s_tmem + 96, sb[1]);
           float mx8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
+          auto fold = [&](const uint32_t(&v)[32]) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
-              mx8[(e >> 1) & 7] = ptx::fmax3(mx8[(e >> 1) & 7], __uint_as_float(s[u][e]), __uint_as_float(s[u][e + 1]));
+              mx8[(e >> 1) & 7] = ptx::fmax3(mx8[(e >> 1) & 7], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          };
+          fold(sa[0]);
+          fold(sa[1]);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(sb[0]);
+          ptx::reg_fence32(sb[1]);
+          ptx::tmem_ld32(s_tmem, sa[0]);
+          fold(sb[0]);
+          fold(sb[1]);
           const float mnew = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
                                    ptx::fmax3(ptx::fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])) * sl;
           if (t < step) {
@@ -741,19 +758,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const float mu = m == -INFINITY ? 0.f : m;  // a row with no visible key yet keeps P = 0
           const uint64_t nmu2 = ptx::f2_packf(-mu, -mu);
           uint64_t ls2[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          // P of 32 keys, over columns of S whose scores have been read: the upper half of S, in the keys' order
+          auto exps = [&](const uint32_t(&v)[32], int u) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float x0, x1;
-              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[u][2 * e], s[u][2 * e + 1]), sl2, nmu2), x0, x1);
+              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(v[2 * e], v[2 * e + 1]), sl2, nmu2), x0, x1);
               const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
               ls2[e & 3] = ptx::f2_add(ls2[e & 3], ptx::f2_packf(p0, p1));
               pk[e] = ptx::pack_bf16(p0, p1);  // off by up to 2^-8 of a weight; the sum takes it unrounded
             }
-            ptx::tmem_st16(s_tmem + 16 * u, pk);
-          }
+            ptx::tmem_st16(s_tmem + 64 + 16 * u, pk);
+          };
+          exps(sb[0], 2);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(sa[0]);
+          ptx::tmem_ld32(s_tmem + 32, sa[1]);
+          exps(sb[1], 3);
+          exps(sa[0], 0);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(sa[1]);
+          exps(sa[1], 1);
           float a0, a1;
           ptx::f2_unpack(ptx::f2_add(ptx::f2_add(ls2[0], ls2[1]), ptx::f2_add(ls2[2], ls2[3])), a0, a1);
           l += a0 + a1;
@@ -838,6 +864,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // two row tiles: a stream reads its own accumulator; else both halves of the columns are shared out
       const int c_begin = I.two ? 0 : g * kHalf, c_end = I.two ? D : c_begin + kHalf;
       if (active) {
+        __nv_bfloat16* out_o = p.o + out_row * D;
+        // [slot][row tile][D / 4][128 rows] of four columns: neighbouring lanes side by side
+        float* out_part = p.w.part_o + ((slot * p.w.row_tiles + mt) * (D / 4) * kTile + r) * 4;
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
           uint32_t ov[32];
@@ -854,30 +883,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) of[e] += f1 == 0.f ? 0.f : __uint_as_float(ov[e]) * f1;
           }
-          if (flagged) {
-            float tmp[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) tmp[e] = of[e];
-            add_not_finite(p, I, flagged, D, c, tmp);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) of[e] = tmp[e];
-          }
           if (row_ok) {
             if (whole) {
-              __nv_bfloat16* out = p.o + out_row * D + c;
 #pragma unroll
               for (int e = 0; e < 32; e += 8)
-                ptx::st_v4(out + e, ptx::pack_bf16(of[e], of[e + 1]), ptx::pack_bf16(of[e + 2], of[e + 3]),
+                ptx::st_v4(out_o + c + e, ptx::pack_bf16(of[e], of[e + 1]), ptx::pack_bf16(of[e + 2], of[e + 3]),
                            ptx::pack_bf16(of[e + 4], of[e + 5]), ptx::pack_bf16(of[e + 6], of[e + 7]));
-            } else {  // [slot][row tile][D / 4][128 rows] of four columns: neighbouring lanes side by side
-              float4* out = reinterpret_cast<float4*>(p.w.part_o) +
-                            ((slot * p.w.row_tiles + mt) * (D / 4) + c / 4) * kTile + r;
+            } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                out[(e / 4) * kTile] = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
+                *reinterpret_cast<float4*>(out_part + (c + e) * kTile) = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
             }
           }
         }
+        if (flagged) add_not_finite(p, I.b, I.h, C, flagged, D, c_begin, c_end, whole ? out_o : nullptr, out_part);
         if (row_ok && (I.two || g == 0)) {
           if (whole)
             p.lse[out_row] = lse2 * kLn2f;
