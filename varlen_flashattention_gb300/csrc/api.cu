@@ -1184,7 +1184,7 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return JFA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(a->total_q) * a->q_heads >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
   // tiles of a sequence's lines (at most 32 row groups a KV head) are numbered with 32 bits
-  const int64_t tiles = static_cast<int64_t>(a->max_pages) * a->page_size / kTile + 1;
+  const int64_t tiles = static_cast<int64_t>(a->max_pages) * a->page_size / kTile + 8;
   if (tiles * a->kv_heads * 32 >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
   const bool work = a->batch > 0 && a->total_q > 0;
   if (work && (!aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4))) return JFA_ERR_INVALID_ARG;

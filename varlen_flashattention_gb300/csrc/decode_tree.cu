@@ -85,11 +85,11 @@ struct TreeLayout {
   static constexpr int kOffMl = kOffV + kSlotsV * kTileBytes;   // float2 (m, l) per stream and row
   static constexpr int kOffItems = kOffMl + 2 * kTile * 8;      // int4[3] per item
   static constexpr int kOffBars = kOffItems + kItemRing * 48;
-  // k_full, k_empty, v_full, v_empty, item_full, item_empty, q_full, q_empty, s_full[2], p_full[2], o_full[2],
-  // o_free, ml_full[2], drain
-  static constexpr int kNumBars = 2 * kSlotsK + 2 * kSlotsV + 2 * kItemRing + 2 + 6 + 1 + 2 + 1;
-  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
-  static constexpr int kBytes = kOffMisc + 192;
+  // k_full, k_empty, v_full, v_empty, item_full, item_empty, q_full, q_empty, s_full[2], p_half[2], p_full[2],
+  // o_full[2], o_free, ml_full[2], drain, scan_ask, scan_done
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kSlotsV + 2 * kItemRing + 2 + 8 + 1 + 2 + 1 + 2;
+  static constexpr int kOffMisc = (kOffBars + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kBytes = kOffMisc + 176;
   static constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // S: 128 columns a stream, O: D
   static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -114,12 +114,16 @@ __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, int& q0, in
 __device__ __forceinline__ int row_tiles(const TreeParams& p, int n) {
   return static_cast<int>((static_cast<uint32_t>(n + p.nodes_per_tile - 1) * p.node_tile_mul) >> 16);
 }
-// Tiles of all the sequence's lines (below 2^31: the entry point sees to that).
+// A line's end (its mask, the last products, the results, the next line's Q) takes about as long as this many
+// tiles, so it counts like them when the work is split.
+constexpr int kLineCost = 3;
+// What all the sequence's lines cost, in tiles (below 2^31: the entry point sees to that).
 __device__ __forceinline__ uint32_t seq_work(const TreeParams& p, int n, int L) {
   if (n == 0) return 0;
-  return static_cast<uint32_t>(p.hkv) * ((row_tiles(p, n) + 1) >> 1) * static_cast<uint32_t>((L + kTile - 1) >> 7);
+  return static_cast<uint32_t>(p.hkv) * ((row_tiles(p, n) + 1) >> 1) *
+         static_cast<uint32_t>(((L + kTile - 1) >> 7) + kLineCost);
 }
-// Where CTA c's share of `total` tiles begins.
+// Where CTA c's share of the work begins.
 __device__ __forceinline__ uint32_t share_begin(uint32_t total, uint32_t ctas, uint32_t c) {
   const uint32_t each = total / ctas;
   return c * each + min(c, total - each * ctas);
@@ -127,59 +131,69 @@ __device__ __forceinline__ uint32_t share_begin(uint32_t total, uint32_t ctas, u
 
 // Walks the items of a range of the long line; a whole warp calls it.
 struct TreeWalk {
-  int b, h, rg, t, q0, n, L, nt, groups;
+  int b, h, rg, x, q0, n, L, nt, groups;  // x: where in its line, in units of cost (from nt on: behind its tiles)
   uint32_t left;
-  __device__ __forceinline__ void open(const TreeParams& p, int b0, uint32_t pos, uint32_t len) {
-    left = len;
-    b = b0;
-    tree_seq(p, b, q0, n, L);
+  __device__ __forceinline__ void seq(const TreeParams& p) {
     nt = (L + kTile - 1) >> 7;
     groups = (row_tiles(p, n) + 1) >> 1;
-    const uint32_t line = pos / static_cast<uint32_t>(nt);
-    t = static_cast<int>(pos - line * nt);
+  }
+  __device__ __forceinline__ void open(const TreeParams& p, int4 first, uint32_t pos, uint32_t len) {
+    left = len;
+    b = first.x;
+    q0 = first.y;
+    n = first.z;
+    L = first.w;
+    seq(p);
+    const uint32_t each = static_cast<uint32_t>(nt + kLineCost), line = pos / each;
+    x = static_cast<int>(pos - line * each);
     h = static_cast<int>(line / static_cast<uint32_t>(groups));
     rg = static_cast<int>(line) - h * groups;
   }
+  __device__ __forceinline__ void next_line(const TreeParams& p) {
+    x = 0;
+    if (left == 0 || ++rg < groups) return;
+    rg = 0;
+    if (++h < p.hkv) return;
+    h = 0;
+    // the next sequence with new tokens, 32 looked at together (there is one: work is left)
+    for (int from = b + 1; from < p.batch; from += 32) {
+      const int at = from + static_cast<int>(threadIdx.x & 31);
+      int aq = 0, an = 0, al = 0;
+      const bool some = at < p.batch && tree_seq(p, at, aq, an, al) && an > 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, some);
+      if (m) {
+        const int src = __ffs(m) - 1;
+        b = from + src;
+        q0 = __shfl_sync(0xffffffffu, aq, src);
+        n = __shfl_sync(0xffffffffu, an, src);
+        L = __shfl_sync(0xffffffffu, al, src);
+        seq(p);
+        return;
+      }
+    }
+    left = 0;  // only if the arrays changed under the call
+  }
   __device__ __forceinline__ bool next(const TreeParams& p, TreeItem& I) {
+    if (left > 0 && x >= nt) {
+      left -= min(left, static_cast<uint32_t>(nt + kLineCost - x));
+      next_line(p);
+    }
     if (left == 0) return false;
     I.b = b;
     I.h = h;
     I.tile0 = 2 * rg;
     I.two = row_tiles(p, n) - 2 * rg >= 2;
-    I.t0 = t;
-    I.t1 = t + static_cast<int>(min(static_cast<uint32_t>(nt - t), left));
+    I.t0 = x;
+    I.t1 = x + static_cast<int>(min(static_cast<uint32_t>(nt - x), left));
     I.nt = nt;
     I.L = L;
     I.q0 = q0;
     I.n = n;
     left -= I.t1 - I.t0;
-    t = 0;
-    if (left > 0 && ++rg == groups) {
-      rg = 0;
-      if (++h == p.hkv) {
-        h = 0;
-        // the next sequence with new tokens, 32 looked at together (there is one: tiles are left)
-        for (int from = b + 1;; from += 32) {
-          const int at = from + static_cast<int>(threadIdx.x & 31);
-          int aq = 0, an = 0, al = 0;
-          const bool some = at < p.batch && tree_seq(p, at, aq, an, al) && an > 0;
-          const uint32_t m = __ballot_sync(0xffffffffu, some);
-          if (m) {
-            const int src = __ffs(m) - 1;
-            b = from + src;
-            q0 = __shfl_sync(0xffffffffu, aq, src);
-            n = __shfl_sync(0xffffffffu, an, src);
-            L = __shfl_sync(0xffffffffu, al, src);
-            nt = (L + kTile - 1) >> 7;
-            groups = (row_tiles(p, n) + 1) >> 1;
-            break;
-          }
-          if (from >= p.batch) {  // only if the arrays changed under the call
-            left = 0;
-            break;
-          }
-        }
-      }
+    x = I.t1;
+    if (x == nt) {
+      left -= min(left, static_cast<uint32_t>(kLineCost));
+      next_line(p);
     }
     return true;
   }
@@ -263,18 +277,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint64_t* q_full = item_empty + kItemRing;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;
-  uint64_t* p_full = s_full + 2;
+  uint64_t* p_half = s_full + 2;  // P of keys 64-127, which the products start with
+  uint64_t* p_full = p_half + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* o_free = o_full + 2;
   uint64_t* ml_full = o_free + 1;
   uint64_t* drain = ml_full + 2;
+  uint64_t* scan_ask = drain + 1;  // V of a tile with drafts has arrived / has been looked over
+  uint64_t* scan_done = drain + 2;
   float2* ml = reinterpret_cast<float2*>(smem + Lay::kOffMl);
   int4* items = reinterpret_cast<int4*>(smem + Lay::kOffItems);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc);
   ptx::CtaCtl* ctl = reinterpret_cast<ptx::CtaCtl*>(smem + Lay::kOffMisc + 8);
-  int32_t* s_first = reinterpret_cast<int32_t*>(smem + Lay::kOffMisc + 16);     // first sequence of the range
-  uint32_t* s_pos = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc + 20);     // where in its lines the range begins
+  // the sequence in which the range begins (its number, first row, nodes, tokens), and where in its lines
+  int4* s_first = reinterpret_cast<int4*>(smem + Lay::kOffMisc + 160);
+  uint32_t* s_pos = reinterpret_cast<uint32_t*>(smem + Lay::kOffMisc + 20);
   unsigned long long* s_flags = reinterpret_cast<unsigned long long*>(smem + Lay::kOffMisc + 32);  // [4]
+  int2* scan_slot = reinterpret_cast<int2*>(smem + Lay::kOffMisc + 24);  // what scan_ask asks for
   unsigned long long* s_sum = reinterpret_cast<unsigned long long*>(smem + Lay::kOffMisc + 64);    // [kTreeThreads / 32]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -307,12 +326,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     ptx::mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(s_full + i, 1);
-      ptx::mbar_init(p_full + i, 4);  // the stream's softmax warps
+      ptx::mbar_init(p_half + i, 4);  // the stream's softmax warps
+      ptx::mbar_init(p_full + i, 4);
       ptx::mbar_init(o_full + i, 1);
       ptx::mbar_init(ml_full + i, 4);
     }
     ptx::mbar_init(o_free, 8);
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(scan_ask, 1);
+    ptx::mbar_init(scan_done, 1);
     for (int i = 0; i < 4; ++i) s_flags[i] = 0;
     ctl->abort = 0;
     status[0] = 0;
@@ -331,13 +353,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();  // the status words are cleared
 
   // ---------------------------------------------------------------- numbering
-  // All tiles of all lines are summed, then the sequence in which this CTA's range begins is found.
+  // The work of all lines is summed, then the sequence in which this CTA's range begins is found.
   unsigned long long sum = 0;
-  uint32_t own = 0;  // tiles of the sequence that this thread numbers (its only one in batches up to the block)
+  int q0 = 0, n = 0, L = 0;  // the sequence that this thread numbers (its only one in batches up to the block)
   {
     unsigned long long mine = 0;
     for (int b = tid; b < p.batch; b += kTreeThreads) {
-      int q0, n, L;
       if (!tree_seq(p, b, q0, n, L)) {  // its rows are empty, a share of them a CTA
         atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
         atomicCAS(status + 1, 0, kSiteTreeInput);
@@ -347,8 +368,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int c = 0; c < D; c += 8) ptx::st_v4(p.o + i * D + c, 0, 0, 0, 0);
         }
       }
-      own = seq_work(p, n, L);
-      mine += own;
+      mine += seq_work(p, n, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -372,12 +392,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (begin < end) {
     uint32_t base = 0;
     for (int b0 = 0; b0 < p.batch && base <= begin; b0 += kTreeThreads) {
-      uint32_t v = own;
       if (p.batch > kTreeThreads) {
-        int q0, n = 0, L = 0;
+        n = 0;
         if (b0 + tid < p.batch) tree_seq(p, b0 + tid, q0, n, L);
-        v = seq_work(p, n, L);
       }
+      const uint32_t v = seq_work(p, n, L);
       uint32_t incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -394,7 +413,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         all += static_cast<uint32_t>(s_sum[i]);
       }
       if (begin < incl && begin >= incl - v) {
-        *s_first = b0 + tid;
+        *s_first = make_int4(b0 + tid, q0, n, L);
         *s_pos = begin - (incl - v);
       }
       base += all;
@@ -423,26 +442,80 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     TreeWalk walk{};
     if (begin < end) {
       walk.open(p, *s_first, *s_pos, end - begin);
-      if (lane == 0) {  // where this CTA's range begins, for the join
-        p.w.records[2 * cta] = make_int4(walk.b, walk.h, walk.rg, walk.t);
+      if (lane == 0) {  // where this CTA's range begins, for the join (behind a line's tiles: at the next line)
+        p.w.records[2 * cta] = make_int4(walk.b, walk.h, walk.rg, walk.x < walk.nt ? walk.x : 0);
         p.w.records[2 * cta + 1] = make_int4(walk.nt, walk.q0, walk.n, row_tiles(p, walk.n) - 2 * walk.rg >= 2);
       }
     }
-    for (uint32_t k = 0;; ++k) {
-      TreeItem J{};
-      const bool more = walk.next(p, J);
-      const uint32_t e = k % kItemRing;
-      if (!ptx::warp_all(
-              ptx::mbar_wait(item_empty + e, ((k / kItemRing) & 1) ^ 1, ctl, status, kSiteTreeItem, budget)))
-        break;
-      if (lane == 0) {
-        items[3 * e] = make_int4(more ? J.b : -1, J.h, J.tile0, J.two);
-        items[3 * e + 1] = make_int4(J.t0, J.t1, J.nt, J.L);
-        items[3 * e + 2] = make_int4(J.q0, J.n, 0, 0);
-        ptx::mbar_arrive(item_full + e);  // release: the record is visible to the entry's waiters
+    // Two things to do in the order they come up: the next item, once the ring has an entry for it; and V of a
+    // tile with drafts, which the MMA warp asks for. What is not finite there, of a draft that some row may not see or
+    // behind the last token, becomes 0 for the product; drafts with such values are flagged for the item's end.
+    TreeItem J{};
+    bool more = walk.next(p, J), given = false;
+    uint32_t items_out = 0, scans = 0;
+    while (true) {
+      bool idle = true;
+      if (!given) {
+        const uint32_t e = items_out % kItemRing;
+        if (ptx::warp_all(ptx::mbar_test(item_empty + e, ((items_out / kItemRing) & 1) ^ 1))) {
+          idle = false;
+          if (lane == 0) {
+            items[3 * e] = make_int4(more ? J.b : -1, J.h, J.tile0, J.two);
+            items[3 * e + 1] = make_int4(J.t0, J.t1, J.nt, J.L);
+            items[3 * e + 2] = make_int4(J.q0, J.n, 0, 0);
+            ptx::mbar_arrive(item_full + e);  // release: the record is visible to the entry's waiters
+          }
+          __syncwarp();
+          ++items_out;
+          given = !more;
+          if (more) more = walk.next(p, J);
+        }
       }
-      __syncwarp();
-      if (!more) break;
+      if (ptx::warp_all(ptx::mbar_test(scan_ask, scans & 1))) {
+        idle = false;
+        const int2 ask = *scan_slot;  // (V slot, draft number of its first token)
+        const uint32_t item = ask.x >> 8;
+        uint8_t* v = smem + Lay::kOffV + (ask.x & 255) * Lay::kTileBytes;
+        // half a warp a row (a quarter at D = 64); the swizzle only orders a row's chunks, so all are looked at
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 8;
+        const int c = lane % kLanes;
+        uint8_t* col = v + (c >> 3) * 16384 + (c & 7) * 16;
+        bool dirty = false;
+        for (int r0 = max(0, -ask.y) / kRows * kRows + lane / kLanes; r0 < kTile; r0 += kRows * kAhead) {
+          uint4 x[kAhead];
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e)
+            x[e] = r0 + e * kRows < kTile ? *reinterpret_cast<uint4*>(col + (r0 + e * kRows) * 128) : make_uint4(0, 0, 0, 0);
+          bool fine = true;
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e) fine = fine && all_finite(x[e]);
+          if (fine) continue;
+#pragma unroll 1
+          for (int e = 0; e < kAhead; ++e) {
+            const int r = r0 + e * kRows, draft = ask.y + r;
+            if (r >= kTile || draft < 0) continue;
+            uint32_t* w = reinterpret_cast<uint32_t*>(col + r * 128);
+            bool found = false;
+            for (int i = 0; i < 4; ++i) found = found || keep_finite(w[i]) != w[i];
+            if (!found) continue;
+            dirty = true;
+            if (draft < kTreeMaxNodes) {
+              atomicOr(s_flags + (item & 3), 1ull << draft);  // bits past the drafts meet no row's mask
+              __threadfence_block();
+            }
+            for (int i = 0; i < 4; ++i) w[i] = keep_finite(w[i]);
+          }
+        }
+        if (dirty) ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(scan_done);
+        ++scans;
+      }
+      if (given && ptx::warp_all(ptx::mbar_test(drain, 0))) break;
+      if (idle) {
+        if (__any_sync(0xffffffffu, ctl->abort != 0)) break;  // whoever waits for this warp gives up in time
+        __nanosleep(40);
+      }
     }
   } else if (warp == kWarpK || warp == kWarpV) {
     // ------------------------------------------------------------ K loads; Q and V loads
@@ -539,23 +612,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop; one elected lane issues.
-    uint32_t it = 0, np[2] = {0, 0}, kslot = 0, kphase = 0, vslot = 0, vphase = 0;
+    // The whole warp runs the loop; one elected lane issues. A look at a barrier takes some 300 cycles while
+    // MMAs read shared memory, so barriers are looked at ahead, and the answer is taken after the next MMAs.
+    // One warp for both streams: with a warp each they fall into step, both softmaxes beside idle tensor
+    // cores (one sequence of 131k tokens and 240 rows: 140 us against 118).
+    uint32_t it = 0, scans = 0, np[2] = {0, 0}, kslot = 0, kphase = 0, vslot = 0, vphase = 0;
     bool ok = true;
-    auto k_wait = [&]() -> uint32_t {
+    auto wait = [&](uint64_t* bar, uint32_t phase, int site, bool ahead = false) -> bool {
+      if (!ahead) ok = ptx::warp_all(ptx::mbar_wait(bar, phase, ctl, status, site, budget));
+      return ok;
+    };
+    auto k_look = [&]() { return ptx::mbar_test(k_full + kslot, kphase); };
+    auto v_look = [&]() { return ptx::mbar_test(v_full + vslot, vphase); };
+    auto p_look = [&](int g) { return ptx::mbar_test(p_half + g, np[g] & 1); };
+    auto k_wait = [&](bool ahead = false) -> uint32_t {
       const uint32_t slot = kslot;
-      ok = ptx::warp_all(ptx::mbar_wait(k_full + slot, kphase, ctl, status, kSiteTreeMmaSlot, budget));
-      ptx::tc_fence_after();
+      wait(k_full + slot, kphase, kSiteTreeMmaSlot, ahead);
       if (++kslot == kSlotsK) {
         kslot = 0;
         kphase ^= 1;
       }
       return slot;
     };
-    auto v_wait = [&]() -> uint32_t {
+    auto v_wait = [&](bool ahead = false) -> uint32_t {
       const uint32_t slot = vslot;
-      ok = ptx::warp_all(ptx::mbar_wait(v_full + slot, vphase, ctl, status, kSiteTreeMmaSlot, budget));
-      ptx::tc_fence_after();
+      wait(v_full + slot, vphase, kSiteTreeMmaSlot, ahead);
       if (++vslot == kSlotsV) {
         vslot = 0;
         vphase ^= 1;
@@ -578,21 +659,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int g, uint32_t slot, bool first, bool last, bool free_slot) {
-      if (first && it > 0)  // the item before has been read out of the accumulators
-        ok = ptx::warp_all(ptx::mbar_wait(o_free, (it - 1) & 1, ctl, status, kSiteTreeMmaOFree, budget));
-      if (!ok) return;
-      ok = ptx::warp_all(ptx::mbar_wait(p_full + g, np[g] & 1, ctl, status, kSiteTreeMmaP, budget));
-      if (!ok) return;
-      ++np[g];
-      ptx::tc_fence_after();
+    // V of tile t has arrived: is it one with drafts?
+    auto has_drafts = [&](int t) -> bool { return (I.t0 + t + 1) * kTile > I.L - I.n; };
+    auto ask_scan = [&](int t, uint32_t slot) {
+      if (!has_drafts(t)) return;
+      if (ptx::elect_one()) {
+        *scan_slot = make_int2(static_cast<int>(slot | it << 8), (I.t0 + t) * kTile - (I.L - I.n));
+        ptx::mbar_arrive(scan_ask);  // release: the slot is visible to the scheduler
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int g, int t, uint32_t slot, bool first, bool last, bool free_slot, bool ahead) {
+      if (first && it > 0 && !wait(o_free, (it - 1) & 1, kSiteTreeMmaOFree)) return;  // read out of the accumulators
+      if ((g == 0 || !I.two) && has_drafts(t) && !wait(scan_done, scans++ & 1, kSiteTreeMmaScan)) return;
+      if (!ahead && !wait(p_half + g, np[g] & 1, kSiteTreeMmaP)) return;
+      ptx::tc_fence_after();  // P and the accumulators were last touched by the softmax warps
       const uint64_t v_desc =
           ptx::sdesc_sw128(ptx::smem_u32(smem + Lay::kOffV + slot * Lay::kTileBytes), 16384, 1024);
+      const uint32_t o = tmem + Lay::kColO + g * D, pt = tmem + Lay::kColS + g * kTile + 64;
       if (ptx::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          ptx::mma_ts(tmem + Lay::kColO + g * D, tmem + Lay::kColS + g * kTile + 64 + kk * 8, v_desc + ((kk * 2048) >> 4),
-                      kIdPV, (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 4; kk < 8; ++kk)
+          ptx::mma_ts(o, pt + kk * 8, v_desc + ((kk * 2048) >> 4), kIdPV, (!first || kk > 4) ? 1u : 0u);
+      }
+      __syncwarp();
+      if (!wait(p_full + g, np[g] & 1, kSiteTreeMmaP)) return;
+      ++np[g];
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) ptx::mma_ts(o, pt + kk * 8, v_desc + ((kk * 2048) >> 4), kIdPV, 1u);
         if (free_slot) ptx::mma_commit(v_empty + slot);
         if (last) ptx::mma_commit(o_full + g);
       }
@@ -600,45 +696,57 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
     while (ok && take(it)) {
       const int nt = I.t1 - I.t0;
-      ok = ptx::warp_all(ptx::mbar_wait(q_full, it & 1, ctl, status, kSiteTreeMmaQ, budget));
-      if (!ok) break;
-      ptx::tc_fence_after();
-      uint32_t slot = k_wait();
+      if (!wait(q_full, it & 1, kSiteTreeMmaQ)) break;
+      uint32_t ks = k_wait();
       if (!ok) break;
       if (I.two) {
-        issue_s(0, 0, slot, false, false);
-        issue_s(1, 1, slot, true, nt == 1);
+        issue_s(0, 0, ks, false, false);
+        issue_s(1, 1, ks, true, nt == 1);
+        uint32_t vs = v_wait();
+        if (!ok) break;
+        ask_scan(0, vs);
+        if (nt > 1) ks = k_wait();
         for (int t = 0; ok && t < nt; ++t) {
           const bool more = t + 1 < nt;
-          const uint32_t vs = v_wait();
+          issue_pv(0, t, vs, t == 0, !more, false, false);
           if (!ok) break;
-          issue_pv(0, vs, t == 0, !more, false);
+          const bool p1 = p_look(1);
+          if (more) issue_s(0, 0, ks, false, false);
+          issue_pv(1, t, vs, t == 0, !more, true, ptx::warp_all(p1));
           if (!ok) break;
-          uint32_t ks = 0;
           if (more) {
-            ks = k_wait();
+            const bool v = v_look();
+            const uint32_t at = ks;
+            const bool next = t + 2 < nt, k = next && k_look();
+            issue_s(1, 1, at, true, !next);
+            const bool here = ptx::warp_all(v && (k || !next));
+            vs = v_wait(here);
             if (!ok) break;
-            issue_s(0, 0, ks, false, false);
+            ask_scan(t + 1, vs);
+            if (next) ks = k_wait(here);
           }
-          issue_pv(1, vs, t == 0, !more, true);
-          if (!ok) break;
-          if (more) issue_s(1, 1, ks, true, t + 2 == nt);
         }
       } else {
-        issue_s(0, 0, slot, true, nt == 1);
+        issue_s(0, 0, ks, true, nt == 1);
         if (nt > 1) {
-          slot = k_wait();
+          ks = k_wait();
           if (!ok) break;
-          issue_s(1, 0, slot, true, nt == 2);
+          issue_s(1, 0, ks, true, nt == 2);
         }
+        bool v = false;
         for (int t = 0; ok && t < nt; ++t) {
-          const uint32_t vs = v_wait();
+          const bool more = t + 2 < nt;
+          const uint32_t vs = v_wait(ptx::warp_all(v));
           if (!ok) break;
-          issue_pv(t & 1, vs, t < 2, t + 2 >= nt, true);
-          if (ok && t + 2 < nt) {
-            slot = k_wait();
+          ask_scan(t, vs);
+          const bool k = more && k_look();
+          issue_pv(t & 1, t, vs, t < 2, t + 2 >= nt, true, false);
+          if (!ok) break;
+          v = t + 1 < nt && v_look();
+          if (more) {
+            ks = k_wait(ptx::warp_all(k));
             if (!ok) break;
-            issue_s(t & 1, 0, slot, true, t + 3 == nt);
+            issue_s(t & 1, 0, ks, true, t + 3 == nt);
           }
         }
       }
@@ -659,7 +767,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int row_node = r / p.group, row_head = r % p.group;  // of this row in its tile
     const float sl = p.scale_log2;
     const uint64_t sl2 = ptx::f2_packf(sl, sl);
-    uint32_t nv = 0, ns = 0, it = 0;
+    uint32_t ns = 0, it = 0;
     uint32_t no0 = 0, no1 = 0, nml0 = 0, nml1 = 0;  // phases of o_full and ml_full so far
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase, int site) -> bool {  // the warp agrees, so that votes below are whole
@@ -776,6 +884,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           ptx::reg_fence32(sa[0]);
           ptx::tmem_ld32(s_tmem + 32, sa[1]);
           exps(sb[1], 3);
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(p_half + g);
           exps(sa[0], 0);
           ptx::tmem_ld_wait();
           ptx::reg_fence32(sa[1]);
@@ -783,32 +895,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           float a0, a1;
           ptx::f2_unpack(ptx::f2_add(ptx::f2_add(ls2[0], ls2[1]), ptx::f2_add(ls2[2], ls2[3])), a0, a1);
           l += a0 + a1;
-        }
-        // V of a tile with drafts, by one stream's 128 threads: a token a thread
-        if (masked && !(I.two && g)) {
-          const uint32_t slot = (nv + t) % kSlotsV;
-          if (!wait(v_full + slot, (nv + t) / kSlotsV, kSiteTreeSoftV)) break;
-          const int draft = tok + r - C;
-          if (draft >= 0) {
-            uint8_t* row = smem + Lay::kOffV + slot * Lay::kTileBytes + r * 128;
-            bool found = false;
-#pragma unroll 1
-            for (int c = 0; c < 8 * kAtoms; c += 4) {  // the swizzle only orders a row's chunks: all are looked at
-              uint4 v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = *reinterpret_cast<uint4*>(row + ((c + e) >> 3) * 16384 + ((((c + e) & 7) ^ (r & 7)) << 4));
-              if (all_finite(v[0]) && all_finite(v[1]) && all_finite(v[2]) && all_finite(v[3])) continue;
-              if (!found && draft < I.n) atomicOr(s_flags + (it & 3), 1ull << draft);
-              found = true;
-#pragma unroll 1
-              for (int e = 0; e < 4; ++e) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(row + ((c + e) >> 3) * 16384 + ((((c + e) & 7) ^ (r & 7)) << 4));
-                for (int i = 0; i < 4; ++i) w[i] = keep_finite(w[i]);
-              }
-            }
-            if (found) ptx::fence_proxy_async_smem();
-          }
+        } else if (lane == 0) {
+          ptx::mbar_arrive(p_half + g);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
@@ -816,7 +904,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) ptx::mbar_arrive(p_full + g);
       }
       if (!ok) break;
-      nv += nt;
       // -------------------------------------------------------- the item's end
       const bool whole = I.t0 == 0 && I.t1 == I.nt;
       const int64_t slot = 2 * cta + (I.t0 > 0 ? 0 : 1);  // a CTA's first item may continue a line, its last one be cut
@@ -867,6 +954,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __nv_bfloat16* out_o = p.o + out_row * D;
         // [slot][row tile][D / 4][128 rows] of four columns: neighbouring lanes side by side
         float* out_part = p.w.part_o + ((slot * p.w.row_tiles + mt) * (D / 4) * kTile + r) * 4;
+        int rows4[4];  // the rows of this lane's four lanes
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          rows4[k] = __shfl_sync(0xffffffffu, row_ok ? static_cast<int>(out_row) : -1, (lane & ~3) + k);
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
           uint32_t ov[32];
@@ -883,19 +974,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) of[e] += f1 == 0.f ? 0.f : __uint_as_float(ov[e]) * f1;
           }
-          if (row_ok) {
-            if (whole) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                ptx::st_v4(out_o + c + e, ptx::pack_bf16(of[e], of[e + 1]), ptx::pack_bf16(of[e + 2], of[e + 3]),
-                           ptx::pack_bf16(of[e + 4], of[e + 5]), ptx::pack_bf16(of[e + 6], of[e + 7]));
-            } else {
+          if (!whole) {
+            if (row_ok) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(out_part + (c + e) * kTile) = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
             }
+          } else {
+            // Four lanes exchange the 16-byte pieces of their four rows, so that a store writes 64 bytes of eight
+            // rows and not 16 of 32 (a line a lane: 4600 cycles for two tiles of 128 rows, more than an own tile costs).
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = ptx::pack_bf16(of[2 * e], of[2 * e + 1]);
+            const bool hi2 = lane & 2, hi1 = lane & 1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // pieces 2, 3 of the lower pair against 0, 1 of the upper
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, hi2 ? w[e] : w[8 + e], 2);
+              w[e] = hi2 ? got : w[e];
+              w[8 + e] = hi2 ? w[8 + e] : got;
+            }
+#pragma unroll
+            for (int q = 0; q < 16; q += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {  // pieces 1 (3) of the even lane against 0 (2) of the odd
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, hi1 ? w[q + e] : w[q + 4 + e], 1);
+                w[q + e] = hi1 ? got : w[q + e];
+                w[q + 4 + e] = hi1 ? w[q + 4 + e] : got;
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (rows4[k] >= 0)
+                ptx::st_v4(p.o + static_cast<int64_t>(rows4[k]) * D + c + 8 * (lane & 3), w[4 * k], w[4 * k + 1],
+                           w[4 * k + 2], w[4 * k + 3]);
           }
         }
+        __syncwarp();
         if (flagged) add_not_finite(p, I.b, I.h, C, flagged, D, c_begin, c_end, whole ? out_o : nullptr, out_part);
         if (row_ok && (I.two || g == 0)) {
           if (whole)

@@ -102,7 +102,7 @@ enum WaitSite : int32_t {
   kSiteTreeMmaP = 523,
   kSiteTreeMmaOFree = 524,
   kSiteTreeSoftS = 531,
-  kSiteTreeSoftV = 532,
+  kSiteTreeMmaScan = 525,
   kSiteTreeSoftO = 533,
   kSiteTreeSoftMl = 534,
   kSiteTreeDrain = 541,
