@@ -227,3 +227,14 @@ def test_binding_refusals(which, change, error):
 def test_binding_asks_for_the_device(which):
     with pytest.raises(ValueError, match="CUDA"):
         _call(which)
+
+
+@pytest.mark.parametrize("struct,pack", [(_abi.CacheAppendRopeArgs, _abi.pack_cache_append_rope),
+                                         (_abi.DecodeTreeArgs, _abi.pack_decode_tree),
+                                         (_abi.CacheAcceptArgs, _abi.pack_cache_accept)])
+def test_packed_arguments_are_the_struct(struct, pack):
+    values = [i + 1.5 if t is _abi.c_f32 else 7 * i + 1 for i, (_, t) in enumerate(struct._fields_)]
+    packed = pack(*values)
+    assert len(packed) == ctypes.sizeof(struct)
+    back = struct.from_buffer_copy(packed)
+    assert [getattr(back, f) for f, _ in struct._fields_] == values

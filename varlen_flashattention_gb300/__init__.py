@@ -181,6 +181,32 @@ def _run_here(entry, size_entry, a, device, workspace, stream, check):
         _finish(ws, check, stream, entry)
 
 
+def _run_packed(entry, packed, need, device, workspace, stream, check):
+    """_run for the arguments of a call as the bytes of its struct, and a known workspace size."""
+    index = device.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _run_packed(entry, packed, need, device, workspace, stream, check)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream belongs to {stream.device}, the call runs on {device}")
+    else:
+        raw = stream.cuda_stream
+    if workspace is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            ws.record_stream(stream)  # allocated on the current stream, used on this one
+    else:
+        ws = _workspace(need, device, workspace)
+        need = _nbytes(ws)
+    status = _abi.packed_entry(entry)(packed, ws.data_ptr(), need, raw)
+    if status != _abi.JFA_OK:
+        raise JfaError(status, entry)
+    if check:
+        _finish(ws, check, stream, entry)
+
+
 def _check(status, where):
     if status != _abi.JFA_OK:
         raise JfaError(status, where)
@@ -704,20 +730,25 @@ def jfa_cache_evict_fp8(k_cache, v_cache, k_scale, v_scale, page_table, seqlens_
 
 # ---------------------------------------------------------------- speculative decoding
 
+def _adr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _paged_ok(k_cache, v_cache, page_table, seqlens_k, offsets, B):
+    """The usual case of a bf16 paged cache and a batch over it, in one test: types, layouts and one
+    CUDA device. What is not usual is named by _paged_inputs."""
+    bf16, i32, i = torch.bfloat16, torch.int32, k_cache.get_device()
+    return (i >= 0 and k_cache.dtype is bf16 and v_cache.dtype is bf16 and page_table.dtype is i32 and
+            seqlens_k.dtype is i32 and offsets.dtype is i32 and v_cache.shape == k_cache.shape and
+            seqlens_k.shape == (B,) and offsets.shape == (B + 1,) and v_cache.get_device() == i and
+            page_table.get_device() == i and seqlens_k.get_device() == i and offsets.get_device() == i and
+            k_cache.is_contiguous() and v_cache.is_contiguous() and page_table.is_contiguous() and
+            seqlens_k.is_contiguous() and offsets.is_contiguous())
+
+
 def _paged_inputs(k_cache, v_cache, page_table, seqlens_k, offsets, offsets_name):
     """Shapes of a bf16 paged cache and of the batch over it: (num_pages, page size, KV heads,
     head dim, batch, max_pages)."""
-    try:  # the usual case in one test; what follows it names what is wrong
-        num_pages, P, Hkv, d = shape = k_cache.shape
-        B, mp = page_table.shape
-        bf16, i32 = torch.bfloat16, torch.int32
-        if (k_cache.dtype is bf16 and v_cache.dtype is bf16 and page_table.dtype is i32 and seqlens_k.dtype is i32 and
-                offsets.dtype is i32 and v_cache.shape == shape and seqlens_k.shape == (B,) and
-                offsets.shape == (B + 1,) and k_cache.is_contiguous() and v_cache.is_contiguous() and
-                page_table.is_contiguous() and seqlens_k.is_contiguous() and offsets.is_contiguous()):
-            return num_pages, P, Hkv, d, B, mp
-    except (AttributeError, TypeError, ValueError):
-        pass
     _need(k_cache, "k_cache", torch.bfloat16, 4)
     num_pages, P, Hkv, d = k_cache.shape
     _need(v_cache, "v_cache", torch.bfloat16, k_cache.shape)
@@ -738,12 +769,19 @@ def _need_rows(t, name, heads, d, rows):
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3 or t.shape[1:] != (heads, d) or (rows is not None and t.shape[0] != rows):
         raise ValueError(f"{name} must have shape {('rows' if rows is None else rows, heads, d)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return heads * d
     stride, inner, last = t.stride()
-    if last != 1 or (heads > 1 and inner != d) or (t.shape[0] > 1 and (stride < heads * d or stride % 8 != 0)):
+    if t.shape[0] <= 1 or t.is_contiguous():
+        stride = heads * d
+    if t.numel() and (last != 1 or (heads > 1 and inner != d) or stride < heads * d or stride % 8 != 0):
         raise ValueError(f"{name}: a row's heads must be contiguous and its stride a multiple of 8, got {t.stride()}")
-    return stride if t.shape[0] > 1 else heads * d
+    return stride
+
+
+def _same_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            return False
+    return True
 
 
 def jfa_cache_append_rope(q, k, v, k_cache, v_cache, page_table, seqlens_k, new_offsets, cos, sin, positions=None,
@@ -758,7 +796,14 @@ def jfa_cache_append_rope(q, k, v, k_cache, v_cache, page_table, seqlens_k, new_
     tokens' places in their sequences. Pairs are columns (j, j + rot_dim / 2), or neighbours if
     interleaved. Returns the rotated Q (q_out, which may be q itself; None without q); its rows behind
     new_offsets[B] are not written."""
-    num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, new_offsets, "new_offsets")
+    try:
+        num_pages, P, Hkv, d = k_cache.shape
+        B, mp = page_table.shape
+        usual = _paged_ok(k_cache, v_cache, page_table, seqlens_k, new_offsets, B)
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, new_offsets, "new_offsets")
     ks = _need_rows(k, "k", Hkv, d, None)
     total = k.shape[0]
     vs = _need_rows(v, "v", Hkv, d, total)
@@ -771,7 +816,8 @@ def jfa_cache_append_rope(q, k, v, k_cache, v_cache, page_table, seqlens_k, new_
     rows = rot = 0
     if cos is not None or sin is not None:
         _need(cos, "cos", torch.float32, 2)
-        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        rows, rot = cos.shape
+        rot *= 2
         _need(sin, "sin", torch.float32, cos.shape)
         if rot > d or rot % 16 != 0:
             raise ValueError(f"cos must hold a multiple of 8 up to {d // 2} columns, got {cos.shape[1]}")
@@ -779,17 +825,23 @@ def jfa_cache_append_rope(q, k, v, k_cache, v_cache, page_table, seqlens_k, new_
         _need(positions, "positions", torch.int32, (total,))
     if q_out is not None:
         _need(q_out, "q_out", torch.bfloat16, q.shape)
-    dev = _device(k=k, v=v, q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k,
-                  new_offsets=new_offsets, cos=cos, sin=sin, positions=positions, q_out=q_out)
+    if not usual or not _same_device(k_cache.get_device(), k, v, q, cos, sin, positions, q_out):
+        _device(k=k, v=v, q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k,
+                new_offsets=new_offsets, cos=cos, sin=sin, positions=positions, q_out=q_out)
+    dev = k_cache.device
     if q is not None and q_out is None:
         q_out = torch.empty((total, Hq, d), dtype=torch.bfloat16, device=dev)
         if stream is not None:  # new memory belongs to the current stream
             q_out.record_stream(stream)
-    a = _abi.CacheAppendRopeArgs(_ptr(q), _ptr(k), _ptr(v), _ptr(new_offsets), _ptr(positions), _ptr(cos), _ptr(sin),
-                                 _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens_k), qs, ks,
-                                 vs, B, Hq, Hkv, d, rot, int(bool(interleaved)), rows, P, num_pages, mp, total)
-    _run("jfa_cache_append_rope", "jfa_cache_append_rope_workspace_size", a, dev, workspace, stream, check)
+    packed = _abi.pack_cache_append_rope(
+        _adr(q), k.data_ptr(), v.data_ptr(), new_offsets.data_ptr(), _adr(positions), _adr(cos), _adr(sin), _adr(q_out),
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), seqlens_k.data_ptr(), qs, ks, vs, B, Hq, Hkv, d,
+        rot, 1 if interleaved else 0, rows, P, num_pages, mp, total)
+    _run_packed("jfa_cache_append_rope", packed, 256, dev, workspace, stream, check)
     return q_out
+
+
+_tree_workspaces = {}  # bytes of the workspace by device, group, head dim and max_q
 
 
 def jfa_decode_tree(q, k_cache, v_cache, page_table, seqlens_k, q_offsets, tree_mask=None, max_q=64, scale=None, o=None,
@@ -800,31 +852,50 @@ def jfa_decode_tree(q, k_cache, v_cache, page_table, seqlens_k, q_offsets, tree_
     tokens. A row sees all tokens before the new ones and new token j iff bit j of its tree_mask (int64 or
     uint64 [total_q]) is set: its ancestors in the tree and itself; without tree_mask j <= i. Returns O bf16
     [total_q, Hq, d] and LSE fp32 [total_q, Hq]; rows behind q_offsets[B] are not written."""
-    num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, q_offsets, "q_offsets")
-    _need(q, "q", torch.bfloat16, 3)
-    total, Hq, _ = q.shape
-    _need(q, "q", torch.bfloat16, (total, Hq, d))
+    try:
+        num_pages, P, Hkv, d = k_cache.shape
+        B, mp = page_table.shape
+        total, Hq, qd = q.shape
+        usual = (_paged_ok(k_cache, v_cache, page_table, seqlens_k, q_offsets, B) and q.dtype is torch.bfloat16 and
+                 qd == d and q.is_contiguous() and q.get_device() == k_cache.get_device())
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, q_offsets, "q_offsets")
+        _need(q, "q", torch.bfloat16, 3)
+        total, Hq, _ = q.shape
+        _need(q, "q", torch.bfloat16, (total, Hq, d))
     if tree_mask is not None:
-        mask_type = torch.uint64 if isinstance(tree_mask, torch.Tensor) and tree_mask.dtype == torch.uint64 else torch.int64
+        mask_type = torch.uint64 if isinstance(tree_mask, torch.Tensor) and tree_mask.dtype is torch.uint64 else torch.int64
         _need(tree_mask, "tree_mask", mask_type, (total,))
     if o is not None:
         _need(o, "o", torch.bfloat16, q.shape)
     if lse is not None:
         _need(lse, "lse", torch.float32, (total, Hq))
-    dev = _device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k,
-                  q_offsets=q_offsets, tree_mask=tree_mask, o=o, lse=lse)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if not usual or not _same_device(k_cache.get_device(), tree_mask, o, lse):
+        _device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k,
+                q_offsets=q_offsets, tree_mask=tree_mask, o=o, lse=lse)
+    dev = k_cache.device
+    max_q = int(max_q)
+    scale = d ** -0.5 if scale is None else float(scale)
     o = torch.empty_like(q) if o is None else o
     lse = torch.empty((total, Hq), dtype=torch.float32, device=dev) if lse is None else lse
     if stream is not None:  # new memory belongs to the current stream
         o.record_stream(stream)
         lse.record_stream(stream)
-    a = _abi.DecodeTreeArgs(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens_k), _ptr(q_offsets),
-                            _ptr(tree_mask), B, Hq, Hkv, d, P, num_pages, mp, total, int(max_q), scale, _ptr(o),
-                            _ptr(lse), None)
+    ev = 0
     if events is not None:
-        a.main_kernel_events, _keep = _events(events)
-    _run("jfa_decode_tree", "jfa_decode_tree_workspace_size", a, dev, workspace, stream, check)
+        _, _keep = _events(events)
+        ev = ctypes.addressof(_keep)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), seqlens_k.data_ptr(),
+            q_offsets.data_ptr(), _adr(tree_mask), B, Hq, Hkv, d, P, num_pages, mp, total, max_q, scale, o.data_ptr(),
+            lse.data_ptr(), ev)
+    need = _tree_workspaces.get((dev, Hq, Hkv, d, max_q))
+    if need is None:
+        with torch.cuda.device(dev):  # the size depends on the device's number of SMs
+            need = _entry("jfa_decode_tree_workspace_size")(ctypes.byref(_abi.DecodeTreeArgs(*args)))
+        _tree_workspaces[dev, Hq, Hkv, d, max_q] = need
+    _run_packed("jfa_decode_tree", _abi.pack_decode_tree(*args), need, dev, workspace, stream, check)
     return o, lse
 
 
@@ -834,21 +905,31 @@ def jfa_cache_accept(k_cache, v_cache, page_table, seqlens_k, q_offsets, accepte
     tokens accepted[b][k], k < counts[b] (int32 [B, width <= 64] and [B]; 0 .. n_b - 1, n_b = q_offsets[b+1] -
     q_offsets[b]), move to the places behind the tokens before the new ones, in that order. Returns
     new_seqlens int32 [B] = seqlens_k - n_b + counts."""
-    num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, q_offsets, "q_offsets")
+    try:
+        num_pages, P, Hkv, d = k_cache.shape
+        B, mp = page_table.shape
+        usual = _paged_ok(k_cache, v_cache, page_table, seqlens_k, q_offsets, B)
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        num_pages, P, Hkv, d, B, mp = _paged_inputs(k_cache, v_cache, page_table, seqlens_k, q_offsets, "q_offsets")
     width = accepted.shape[1] if isinstance(accepted, torch.Tensor) and accepted.dim() == 2 else 0
     _need(accepted, "accepted", torch.int32, (B, width))
     _need(counts, "counts", torch.int32, (B,))
     if new_seqlens is not None:
         _need(new_seqlens, "new_seqlens", torch.int32, (B,))
-    dev = _device(k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k, q_offsets=q_offsets,
-                  accepted=accepted, counts=counts, new_seqlens=new_seqlens)
+    if not usual or not _same_device(k_cache.get_device(), accepted, counts, new_seqlens):
+        _device(k_cache=k_cache, v_cache=v_cache, page_table=page_table, seqlens_k=seqlens_k, q_offsets=q_offsets,
+                accepted=accepted, counts=counts, new_seqlens=new_seqlens)
+    dev = k_cache.device
     if new_seqlens is None:
         new_seqlens = torch.empty_like(seqlens_k)
         if stream is not None:  # new memory belongs to the current stream
             new_seqlens.record_stream(stream)
-    a = _abi.CacheAcceptArgs(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seqlens_k), _ptr(q_offsets),
-                             _ptr(accepted), _ptr(counts), B, Hkv, d, P, num_pages, mp, width, _ptr(new_seqlens))
-    _run("jfa_cache_accept", "jfa_cache_accept_workspace_size", a, dev, workspace, stream, check)
+    packed = _abi.pack_cache_accept(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), seqlens_k.data_ptr(),
+                                    q_offsets.data_ptr(), accepted.data_ptr(), counts.data_ptr(), B, Hkv, d, P,
+                                    num_pages, mp, width, new_seqlens.data_ptr())
+    _run_packed("jfa_cache_accept", packed, 256, dev, workspace, stream, check)
     return new_seqlens
 
 

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libjfa.so")
@@ -164,6 +165,19 @@ class CacheAcceptArgs(ctypes.Structure):
                 ("new_seqlens", c_void_p)]
 
 
+_CODES = {c_void_p: "P", c_i32: "i", c_i64: "q", c_f32: "f"}
+
+
+def packer(args):
+    """A function that packs the fields of an argument struct, in order, into the bytes of the C
+    struct (0 for a null pointer): a third of the time that filling the ctypes structure takes."""
+    return struct.Struct("@" + "".join(_CODES[t] for _, t in args._fields_) + "0P").pack
+
+
+pack_cache_append_rope = packer(CacheAppendRopeArgs)
+pack_decode_tree = packer(DecodeTreeArgs)
+pack_cache_accept = packer(CacheAcceptArgs)
+
 # (name, argtypes, restype) of every exported symbol declared in include/jfa.h
 SIGNATURES = [
     ("jfa_fwd_workspace_size", [ctypes.POINTER(FwdArgs)], ctypes.c_size_t),
@@ -210,6 +224,16 @@ SIGNATURES = [
 ]
 
 _lib = None
+_packed = {}
+
+
+def packed_entry(name):
+    """The entry point `name` with its argument struct given as packed bytes."""
+    f = _packed.get(name)
+    if f is None:
+        proto = ctypes.CFUNCTYPE(c_i32, ctypes.c_char_p, c_void_p, ctypes.c_size_t, c_void_p)
+        f = _packed[name] = proto((name, load()))
+    return f
 
 
 def load() -> ctypes.CDLL:
