@@ -41,6 +41,7 @@ struct AppendRopeParams {
   const int32_t* seqlens;
   int64_t qs, ks, vs;
   int32_t batch, hq, hkv, rot, interleaved, table_rows, num_pages, max_pages, total_new;
+  int32_t share;  // warps that share a token: kAppendWarps, or 1
   FastDiv page;
   int32_t* status;
 };
@@ -104,7 +105,7 @@ __device__ void append_rope_report(const AppendRopeParams& p, int64_t cap) {
     __syncthreads();
     for (int j = tid >> 5; j < s_left; j += kAppendWarps) {
       const int last = s_hi[j];
-#pragma unroll 4
+#pragma unroll 16
       for (int i = s_lo[j] + lane; i <= last; i += 32) check(s_b[j], i);
     }
     __syncthreads();
@@ -114,7 +115,7 @@ __device__ void append_rope_report(const AppendRopeParams& p, int64_t cap) {
     p.status[tid] = !bad ? 0 : (tid == 0 ? JFA_ERR_BAD_INPUT : (tid == 1 ? kSiteAppendRope : 0));
 }
 
-// A block a token.
+// A warp a token, or a block.
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kAppendWarps) append_rope_kernel(const AppendRopeParams p) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a head, heads of a warp
@@ -123,8 +124,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_rope_kernel(const Ap
     append_rope_report(p, cap);
     return;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x;
+  const int lane = threadIdx.x & 31, share = p.share;
+  const int warp = (threadIdx.x >> 5) & (share - 1);  // among those of its token
+  const int row = (blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) / share;
+  if (row >= p.total_new) return;
   const int b = sequence_of(p.offsets, p.batch, row);
   const int o0 = p.offsets[b], o1 = p.offsets[b + 1], L = p.seqlens[b];
   if (row < o0 || row >= o1 || !new_range_ok(b, o0, o1, L, p.total_new, cap)) return;
@@ -156,11 +159,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_rope_kernel(const Ap
   const __nv_bfloat16* src_q = p.q + row * p.qs + col;
   const __nv_bfloat16* src_k = p.k + row * p.ks + col;
   const __nv_bfloat16* src_v = p.v + row * p.vs + col;
-  for (int h0 = warp * kPer; h0 < heads; h0 += kAppendWarps * kPer * kAppendBatch) {
+  for (int h0 = warp * kPer; h0 < heads; h0 += share * kPer * kAppendBatch) {
     uint4 x[kAppendBatch];
 #pragma unroll
     for (int i = 0; i < kAppendBatch; ++i) {
-      const int h = h0 + i * kAppendWarps * kPer + lane / kLanes;
+      const int h = h0 + i * share * kPer + lane / kLanes;
       if (h < hq)
         x[i] = __ldcs(reinterpret_cast<const uint4*>(src_q + h * D));
       else if (h < hq + p.hkv)
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_rope_kernel(const Ap
     }
 #pragma unroll
     for (int i = 0; i < kAppendBatch; ++i) {
-      const int h = h0 + i * kAppendWarps * kPer + lane / kLanes;
+      const int h = h0 + i * share * kPer + lane / kLanes;
       uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       if (INTERLEAVED) {
         if (turns && h < hq + p.hkv) {
@@ -355,7 +358,13 @@ cudaError_t launch_cache_append_rope(const jfa_cache_append_rope_args& a, int32_
   p.total_new = a.total_new;
   p.page = make_fast_div(a.page_size);
   p.status = status;
-  const int grid = a.total_new + 1;
+  // Few tokens leave the device empty, and a block each shortens their chain; many keep it full with a warp
+  // each, which looks its sequence, page and angles up once for all heads. 32 heads on 8 of 128: one token 3.4 us
+  // (a warp 6.4), 512 sequences of one 5.0 (7.4), 2048 of one 19.0 (13.8), 16 prompts of 61-8192 291 (257),
+  // the same of head_dim 64 217 (140).
+  p.share = a.total_new <= 1024 ? kAppendWarps : 1;
+  const int per_block = kAppendWarps / p.share;
+  const int grid = (a.total_new + per_block - 1) / per_block + 1;
   if (a.head_dim == 128) {
     if (a.interleaved)
       append_rope_kernel<128, true><<<grid, 32 * kAppendWarps, 0, stream>>>(p);
