@@ -1033,16 +1033,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // Joins the parts of the lines that were cut: lse = log2 sum 2^lse_p, O = sum 2^(lse_p - lse) O_p.
-// Block column x looks at the border between the ranges of CTA x and x + 1: if it is the first one
-// inside its line, the blocks (x, y) join that line, a thread eight columns of a row. The first
-// block also gathers the CTAs' findings.
-constexpr int kJoinThreads = 256;
+// Every block looks at all borders between the CTAs' ranges and lists those that are the first in their
+// line; the listed lines, in pieces of 256 threads with four columns of a row each, are dealt out to the
+// blocks. (A block for each border and piece, most of which had nothing to do, and two passes over the
+// parts: 20 us against 8 for 8 lines of 19 parts and 240 rows.) The first block also gathers the CTAs' findings.
+constexpr int kJoinThreads = 256, kJoinCtas = 512, kJoinAhead = 4, kJoinBlocks = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) decode_tree_join_kernel(const TreeParams p, int ctas_launched) {
+  __shared__ int4 s_line[kJoinCtas], s_rest[kJoinCtas];  // (border, KV head, row group, parts), (-, first row, nodes, two)
+  __shared__ int s_found[kJoinThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_prior_grid();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+  const uint32_t total = *p.w.total, ctas = min(static_cast<uint32_t>(ctas_launched), total);
+  int lines = 0;
+  for (uint32_t c0 = 1; c0 < ctas; c0 += kJoinThreads) {
+    const uint32_t c = c0 + tid;
+    int4 first = make_int4(0, 0, 0, 0), rest = first;
+    if (c < ctas) {
+      first = p.w.records[2 * c];
+      rest = p.w.records[2 * c + 1];
+    }
+    const uint32_t line = c < ctas ? share_begin(total, ctas, c) - first.w : 0, end = line + rest.x;
+    // a line goes on over the border, and no earlier border lies inside it
+    const bool found = first.w > 0 && share_begin(total, ctas, c - 1) <= line;
+    const uint32_t m = __ballot_sync(0xffffffffu, found);
+    if (lane == 0) s_found[warp] = __popc(m);
+    __syncthreads();
+    int at = lines + __popc(m & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      at += w < warp ? s_found[w] : 0;
+      lines += s_found[w];
+    }
+    if (found) {
+      // how many shares begin before the line's end
+      const uint32_t each = total / ctas, longer = total - each * ctas;
+      const uint32_t before = end <= longer * (each + 1) ? (end + each) / (each + 1)
+                                                         : longer + (end - longer * (each + 1) + each - 1) / each;
+      s_line[at] = make_int4(c, first.y, first.z, static_cast<int>(min(before, ctas) - c) + 1);
+      s_rest[at] = rest;
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid < 32) {
     int code = 0, site = 0;
-    for (int c = threadIdx.x; c < ctas_launched; c += 32)
+    for (int c = tid; c < ctas_launched; c += 32)
       if (code == 0 && p.w.cta_status[2 * c] != 0) {
         code = p.w.cta_status[2 * c];
         site = p.w.cta_status[2 * c + 1];
@@ -1051,63 +1086,59 @@ __global__ void __launch_bounds__(kJoinThreads) decode_tree_join_kernel(const Tr
     const int src = any ? __ffs(any) - 1 : 0;
     code = __shfl_sync(0xffffffffu, code, src);
     site = __shfl_sync(0xffffffffu, site, src);
-    for (int i = threadIdx.x; i < static_cast<int>(kStatusBytes / 4); i += 32)
+    for (int i = tid; i < static_cast<int>(kStatusBytes / 4); i += 32)
       p.w.status[i] = i == 0 ? code : (i == 1 ? site : 0);
   }
-  const uint32_t total = *p.w.total, ctas = min(static_cast<uint32_t>(ctas_launched), total);
-  const uint32_t c = blockIdx.x + 1;
-  if (c >= ctas) return;
-  const int4 first = p.w.records[2 * c], rest = p.w.records[2 * c + 1];
-  const int t0 = first.w;
-  if (t0 == 0) return;  // a line begins at the border
-  const uint32_t line = share_begin(total, ctas, c) - t0, line_end = line + rest.x;
-  if (share_begin(total, ctas, c - 1) > line) return;  // an earlier border lies inside this line
-  const int two = rest.w, rg = first.z, q0 = rest.y, n = rest.z;
-  const int item = blockIdx.y * kJoinThreads + threadIdx.x;  // [row tile][D / 8][128 rows]
-  const int r = item & (kTile - 1), chunk = (item >> 7) % (D / 8), mt = (item >> 7) / (D / 8);
-  if (mt > two) return;
-  const int row_node = r / p.group;
-  const int node = (2 * rg + mt) * p.nodes_per_tile + row_node;
-  if (row_node >= p.nodes_per_tile || node >= n) return;
-  // the parts: the last item of CTA c - 1, then the first ones of c, c + 1, .. up to the line's end
-  uint32_t last = c;
-  while (last + 1 < ctas && share_begin(total, ctas, last + 1) < line_end) ++last;
-  const int parts = static_cast<int>(last - c) + 2;
-  auto slot_of = [&](int i) -> int64_t { return (i == 0 ? 2 * c - 1 : 2 * (c - 1 + i)) * static_cast<int64_t>(p.w.row_tiles) + mt; };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) M = fmaxf(M, p.w.part_lse2[slot_of(i) * kTile + r]);
-  const float Mu = M == -INFINITY ? 0.f : M;
-  float sum = 0.f, acc[8] = {};
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const int64_t slot = slot_of(i);
-    const float w = ptx::ex2(p.w.part_lse2[slot * kTile + r] - Mu);
-    const float4* o = reinterpret_cast<const float4*>(p.w.part_o) + (slot * (D / 4) + 2 * chunk) * kTile + r;
-    const float4 a = o[0], b = o[kTile];
-    sum += w;
-    if (w != 0.f) {
-      acc[0] += w * a.x;
-      acc[1] += w * a.y;
-      acc[2] += w * a.z;
-      acc[3] += w * a.w;
-      acc[4] += w * b.x;
-      acc[5] += w * b.y;
-      acc[6] += w * b.z;
-      acc[7] += w * b.w;
+  const int pieces = p.w.row_tiles * (D / 4) * kTile / kJoinThreads;  // of a line: [row tile][D / 4][128 rows]
+  for (int w = blockIdx.x; w < lines * pieces; w += gridDim.x) {
+    const int4 line = s_line[w / pieces], rest = s_rest[w / pieces];
+    const int item = w % pieces * kJoinThreads + tid;
+    const int r = item & (kTile - 1), chunk = (item >> 7) % (D / 4), mt = (item >> 7) / (D / 4);
+    const int row_node = r / p.group, node = (2 * line.z + mt) * p.nodes_per_tile + row_node;
+    if (mt > rest.w || row_node >= p.nodes_per_tile || node >= rest.z) continue;
+    // the parts: the last item of CTA c - 1, then the first ones of c, c + 1, .. up to the line's end
+    const int c = line.x, parts = line.w;
+    float M = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += kJoinAhead) {
+      float lse[kJoinAhead];
+      float4 o[kJoinAhead];
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const int i = i0 + e;
+        lse[e] = -INFINITY;
+        if (i < parts) {
+          const int64_t slot = (i == 0 ? 2 * c - 1 : 2 * (c - 1 + i)) * static_cast<int64_t>(p.w.row_tiles) + mt;
+          lse[e] = p.w.part_lse2[slot * kTile + r];
+          o[e] = reinterpret_cast<const float4*>(p.w.part_o)[(slot * (D / 4) + chunk) * kTile + r];
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) top = fmaxf(top, lse[e]);
+      const float ref = top == -INFINITY ? 0.f : top, f = ptx::ex2(M - ref);  // M = -inf: 0
+      sum *= f;
+      acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float wt = ptx::ex2(lse[e] - ref);  // no such part: 0
+        sum += wt;
+        if (wt != 0.f) acc.x += wt * o[e].x, acc.y += wt * o[e].y, acc.z += wt * o[e].z, acc.w += wt * o[e].w;
+      }
+      M = top;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = static_cast<int64_t>(rest.y + node) * p.hq + line.y * p.group + r % p.group;
+    *reinterpret_cast<uint2*>(p.o + row * D + 4 * chunk) =
+        make_uint2(ptx::pack_bf16(acc.x * inv, acc.y * inv), ptx::pack_bf16(acc.z * inv, acc.w * inv));
+    if (chunk == 0) p.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2f;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t row = static_cast<int64_t>(q0 + node) * p.hq + first.y * p.group + r % p.group;
-  ptx::st_v4(p.o + row * D + 8 * chunk, ptx::pack_bf16(acc[0] * inv, acc[1] * inv),
-             ptx::pack_bf16(acc[2] * inv, acc[3] * inv), ptx::pack_bf16(acc[4] * inv, acc[5] * inv),
-             ptx::pack_bf16(acc[6] * inv, acc[7] * inv));
-  if (chunk == 0) p.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2f;
 }
 
 template <int D>
 cudaError_t launch_tree_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                           int grid, void* events, cudaStream_t stream) {
+  if (grid > kJoinCtas) grid = kJoinCtas;
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
     return cudaFuncSetAttribute(decode_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1119,9 +1150,7 @@ cudaError_t launch_tree_d(const CUtensorMap& tq, const CUtensorMap& tk, const CU
   decode_tree_kernel<D><<<grid, kTreeThreads, TreeLayout<D>::kBytes, stream>>>(tq, tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (ev) cudaEventRecord(ev[1], stream);
-  const int chunks = p.w.row_tiles * (D / 8) * kTile / kJoinThreads;
-  return launch_after(decode_tree_join_kernel<D>, dim3(std::max(grid - 1, 1), chunks), dim3(kJoinThreads), 0, stream, p,
-                      grid);
+  return launch_after(decode_tree_join_kernel<D>, dim3(kJoinBlocks * grid), dim3(kJoinThreads), 0, stream, p, grid);
 }
 
 }  // namespace
