@@ -812,16 +812,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             ptx::tmem_st_wait();
           }
-          // The row's maximum, half by half; the upper half stays in registers, the lower one is read again
-          // (128 scores at once spill, and the spills, past a full L1, cost more than the second read).
-          uint32_t sa[2][32], sb[2][32];
-          ptx::tmem_ld32(s_tmem, sa[0]);
-          ptx::tmem_ld32(s_tmem + 32, sa[1]);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(sa[0]);
-          ptx::reg_fence32(sa[1]);
-          ptx::tmem_ld32(s_tmem + 64, sb[0]);
-          ptx::tmem_ld32(s_tmem + 96, sb[1]);
+          // The row's maximum, then P, a half of the scores at a time: rolled, since 128 scores at once spill, and
+          // the code of four unrolled quarters pushes that of the MMA warp, the slowest link with two row tiles,
+          // out of the instruction cache.
+          uint32_t sa[32], sb[32];
           float mx8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
@@ -830,14 +824,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int e = 0; e < 32; e += 2)
               mx8[(e >> 1) & 7] = ptx::fmax3(mx8[(e >> 1) & 7], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           };
-          fold(sa[0]);
-          fold(sa[1]);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(sb[0]);
-          ptx::reg_fence32(sb[1]);
-          ptx::tmem_ld32(s_tmem, sa[0]);
-          fold(sb[0]);
-          fold(sb[1]);
+#pragma unroll 1
+          for (int u = 0; u < 128; u += 64) {
+            ptx::tmem_ld32(s_tmem + u, sa);
+            ptx::tmem_ld32(s_tmem + u + 32, sb);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(sa);
+            ptx::reg_fence32(sb);
+            fold(sa);
+            fold(sb);
+          }
           const float mnew = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
                                    ptx::fmax3(ptx::fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7])) * sl;
           if (t < step) {
@@ -879,19 +875,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             ptx::tmem_st16(s_tmem + 64 + 16 * u, pk);
           };
-          exps(sb[0], 2);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(sa[0]);
-          ptx::tmem_ld32(s_tmem + 32, sa[1]);
-          exps(sb[1], 3);
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(p_half + g);
-          exps(sa[0], 0);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(sa[1]);
-          exps(sa[1], 1);
+#pragma unroll 1
+          for (int half = 1; half >= 0; --half) {
+            ptx::tmem_ld32(s_tmem + 64 * half, sa);
+            ptx::tmem_ld32(s_tmem + 64 * half + 32, sb);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(sa);
+            ptx::reg_fence32(sb);
+            exps(sa, 2 * half);
+            exps(sb, 2 * half + 1);
+            if (half) {
+              ptx::tmem_st_wait();
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(p_half + g);
+            }
+          }
           float a0, a1;
           ptx::f2_unpack(ptx::f2_add(ptx::f2_add(ls2[0], ls2[1]), ptx::f2_add(ls2[2], ls2[3])), a0, a1);
           l += a0 + a1;
