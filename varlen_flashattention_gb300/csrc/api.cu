@@ -1207,8 +1207,8 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   buf.part_lse2 = reinterpret_cast<float*>(w + L.part_lse2);
   buf.part_o = reinterpret_cast<float*>(w + L.part_o);
   buf.row_tiles = L.row_tiles;
-  // Boxes of tokens that lie side by side in a page, whole swizzle atoms of 8 rows; in pages that 8 does not
-  // divide, rows are gathered four at a time through boxes one row high.
+  // Boxes of tokens that lie side by side in a page, whole swizzle atoms of 8 rows; pages that 8 does not
+  // divide are read row by row, in part through boxes one row high.
   int box = a->page_size & -a->page_size;
   box = box < 8 ? 1 : std::min(box, kTile);
   const int group = a->q_heads / a->kv_heads;
