@@ -501,7 +501,7 @@ typedef struct {
   const int32_t* positions;   /* optional: int32 [total_new], 0 <= p < table_rows */
   const float* cos_table;     /* fp32 [table_rows, rot_dim / 2] */
   const float* sin_table;     /* as cos_table */
-  void* q_out;                /* out (with q): bf16 [total_new, q_heads, head_dim]; may be q itself if its rows touch */
+  void* q_out;                /* out (with q): bf16 [total_new, q_heads, head_dim]; q itself if its rows touch, or apart from it */
   void* k_cache;              /* in/out: bf16 [num_pages, page_size, kv_heads, head_dim] */
   void* v_cache;              /* in/out: as k_cache */
   const int32_t* page_table;  /* int32 [batch, max_pages]; entries past ceil(L_b/page_size) are not read */
@@ -523,7 +523,8 @@ typedef struct {
  * that see their token and no others. n_b <= max_q <= 64; q_heads / kv_heads may be any
  * number up to 128. The work is split evenly over the device whatever the lengths; there
  * is no split count to choose. A sequence whose length or offsets are out of range gets
- * O = 0, LSE = -inf (its rows of total_q), and the call reports it. */
+ * O = 0, LSE = -inf (its rows of total_q), and the call reports it. With total_q = 0 there
+ * is nothing to do, and the arrays are not looked at. */
 typedef struct {
   const void* q;              /* bf16 [total_q, q_heads, head_dim] */
   const void* k_cache;        /* bf16 [num_pages, page_size, kv_heads, head_dim] */
@@ -537,7 +538,7 @@ typedef struct {
   int32_t total_q;            /* host: rows of q */
   int32_t max_q;              /* host: >= every n_b, 1 .. 64 */
   float scale;
-  void* o;                    /* out: bf16 [total_q, q_heads, head_dim] */
+  void* o;                    /* out: bf16 [total_q, q_heads, head_dim] (apart from q) */
   float* lse;                 /* out: fp32 [total_q, q_heads] */
   void* main_kernel_events;   /* optional cudaEvent_t[2] around the main kernel */
 } jfa_decode_tree_args;
@@ -547,8 +548,8 @@ typedef struct {
  * what that of C_b + accepted[b][k] was, for k < counts[b] (all rows are read before
  * any is written; the order is the caller's), and
  *   new_seqlens[b] = C_b + counts[b].
- * Rows turned by jfa_cache_append_rope with positions by depth need no other turn. A
- * sequence with a count, index, length or page out of range is left as it is and gets
+ * Rows turned by jfa_cache_append_rope with positions by depth need no other turn. A slot of
+ * a new token belongs to one sequence, once. A sequence with a count, index, length or page out of range is left as it is and gets
  * C_b, or L_b where the length or the offsets are what is wrong; the call reports it. */
 typedef struct {
   void* k_cache;              /* in/out: bf16 [num_pages, page_size, kv_heads, head_dim] */
@@ -561,7 +562,7 @@ typedef struct {
   int32_t batch, kv_heads, head_dim;
   int32_t page_size, num_pages, max_pages;
   int32_t width;              /* 0 .. 64 */
-  int32_t* new_seqlens;       /* out: int32 [batch] (not seqlens_k itself) */
+  int32_t* new_seqlens;       /* out: int32 [batch] (apart from the arrays above) */
 } jfa_cache_accept_args;
 
 /* Workspace sizes in bytes (0 only when args is NULL). */

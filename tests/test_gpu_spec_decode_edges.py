@@ -286,3 +286,83 @@ def test_tree_events_and_status_of_a_reused_workspace():
     assert jfa.jfa_read_device_status(ws) == (0, 0)
     with pytest.raises(ValueError, match="workspace"):
         jfa.jfa_decode_tree(s["q"], *cache(g), g["offs"], s["mask"], workspace=ws[:1024])
+
+
+def test_captured_turns_keep_their_workspaces():
+    """Two captured turns whose calls got workspaces of their own, replayed at the same time between calls
+    and tensors that take and give back memory of every size."""
+    runs = []
+    for seed, explicit in ((67, False), (68, True)):
+        g, s = _turn_state(seed)
+        was = {x: g[x].clone() for x in ("kc", "vc")}
+        _turn(g, s)
+        want = _results(g, s)
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            for x in ("kc", "vc"):
+                g[x].copy_(was[x])
+            _turn(g, s, stream=side if explicit else None)
+        runs.append((g, s, want, side, graph, was))  # the graph reads was
+    other, t = _turn_state(69)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for _ in range(8):
+        held = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (256, 512, 4 << 10, 1 << 20, 20 << 20, 80 << 20)]
+        for g, s, want, side, graph, _ in runs:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                graph.replay()
+        _turn(other, t)
+        torch.cuda.synchronize()
+        assert all((x == 255).all() for x in held)
+        for g, s, want, side, graph, _ in runs:
+            assert _same(_results(g, s), want)
+
+
+def test_turns_of_several_threads():
+    """Calls from four host threads, each on its own stream."""
+    import threading
+
+    states = [_turn_state(70 + i) for i in range(4)]
+    wants, was = [], []
+    for g, s in states:
+        was.append({x: g[x].clone() for x in ("kc", "vc")})
+        _turn(g, s)
+        wants.append(_results(g, s))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        g, s = states[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                for x in ("kc", "vc"):
+                    g[x].copy_(was[i][x])
+                _turn(g, s)
+                if not _same(_results(g, s), wants[i]):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert not wrong
+
+
+def test_outputs_that_lie_over_inputs():
+    """The tree decode may not write over Q, nor accept over what it reads; rotated Q may, row on row."""
+    g, s = _turn_state(74)
+    for o in (s["q"], torch.empty(0, device="cuda")):
+        with pytest.raises((jfa.JfaError, TypeError)):
+            jfa.jfa_decode_tree(s["q"], *cache(g), g["offs"], s["mask"], o=o)
+    for name in ("count", "lens"):
+        new = s["count"] if name == "count" else g["lens"]
+        with pytest.raises(jfa.JfaError):
+            jfa.jfa_cache_accept(*cache(g), g["offs"], s["path"], s["count"], new_seqlens=new)
+    both = torch.zeros(s["q"].shape[0] + 1, 8, 128, dtype=bf16, device="cuda")
+    with pytest.raises(jfa.JfaError):
+        jfa.jfa_cache_append_rope(both[:-1], s["k"], s["v"], *cache(g), g["offs"], s["cos"], s["sin"], q_out=both[1:])
+    jfa.jfa_cache_append_rope(both[:-1], s["k"], s["v"], *cache(g), g["offs"], s["cos"], s["sin"], q_out=both[:-1], check=True)

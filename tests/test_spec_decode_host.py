@@ -116,11 +116,11 @@ def lib():
 
 
 X = 4096  # an aligned address that nothing reads
-APPEND = dict(q=X, k=X, v=X, new_offsets=X, positions=None, cos_table=X, sin_table=X, q_out=2 * X, k_cache=X, v_cache=X,
+APPEND = dict(q=X, k=X, v=X, new_offsets=X, positions=None, cos_table=X, sin_table=X, q_out=8 * X, k_cache=X, v_cache=X,
               page_table=X, seqlens_k=X, q_stride=512, k_stride=256, v_stride=256, batch=2, q_heads=4, kv_heads=2,
               head_dim=128, rot_dim=128, interleaved=0, table_rows=100, page_size=16, num_pages=8, max_pages=4, total_new=5)
 TREE = dict(q=X, k_cache=X, v_cache=X, page_table=X, seqlens_k=X, q_offsets=X, tree_mask=X, batch=2, q_heads=4,
-            kv_heads=2, head_dim=128, page_size=16, num_pages=8, max_pages=4, total_q=5, max_q=64, scale=0.1, o=X, lse=X,
+            kv_heads=2, head_dim=128, page_size=16, num_pages=8, max_pages=4, total_q=5, max_q=64, scale=0.1, o=8 * X, lse=X,
             main_kernel_events=None)
 ACCEPT = dict(k_cache=X, v_cache=X, page_table=X, seqlens_k=X, q_offsets=X, accepted=X, counts=X, batch=2, kv_heads=2,
               head_dim=128, page_size=16, num_pages=8, max_pages=4, width=4, new_seqlens=2 * X)
@@ -134,14 +134,18 @@ BAD = [(n, c, INV) for n in ("append", "tree", "accept") for c in CACHE] + \
         dict(new_offsets=None), dict(total_new=-1), dict(total_new=2 ** 31 - 1), dict(rot_dim=8), dict(rot_dim=144),
         dict(rot_dim=-16), dict(interleaved=2), dict(table_rows=-1), dict(q_heads=0), dict(k=None), dict(v=X + 8),
         dict(k_stride=248), dict(v_stride=260), dict(q_stride=504), dict(q_out=None), dict(q_out=X, q_stride=1024),
-        dict(cos_table=None), dict(sin_table=X + 8), dict(positions=X + 1), dict(batch=0))] + \
+        dict(cos_table=None), dict(sin_table=X + 8), dict(positions=X + 1), dict(batch=0), dict(total_new=2 ** 31 - 100),
+        dict(q_out=X + 1024), dict(q_out=X - 2048), dict(q_out=X + 5104))] + \
     [("tree", c, INV) for c in (
         dict(q_offsets=None), dict(q_heads=5), dict(q_heads=0), dict(total_q=-1), dict(max_q=0), dict(scale=0.0),
         dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(o=X + 8), dict(lse=X + 2),
-        dict(tree_mask=X + 4), dict(total_q=2 ** 30))] + \
+        dict(tree_mask=X + 4), dict(total_q=2 ** 30),
+        dict(o=X), dict(o=X + 5104), dict(o=X - 2048))] + \
     [("tree", dict(max_q=65), UNS), ("tree", dict(q_heads=258), UNS)] + \
     [("accept", c, INV) for c in (dict(q_offsets=None), dict(width=-1), dict(counts=None), dict(accepted=None),
-                                  dict(new_seqlens=None), dict(new_seqlens=X), dict(batch=2 ** 29, kv_heads=2))] + \
+                                  dict(new_seqlens=None), dict(new_seqlens=X), dict(batch=2 ** 29, kv_heads=2),
+                                  dict(seqlens_k=2 * X), dict(counts=2 * X), dict(counts=2 * X - 4),
+                                  dict(q_offsets=2 * X - 8), dict(accepted=2 * X - 28), dict(page_table=2 * X - 28))] + \
     [("accept", dict(width=65), UNS)]
 CALLS = {"append": ("jfa_cache_append_rope", _abi.CacheAppendRopeArgs, APPEND),
          "tree": ("jfa_decode_tree", _abi.DecodeTreeArgs, TREE), "accept": ("jfa_cache_accept", _abi.CacheAcceptArgs, ACCEPT)}
@@ -238,3 +242,11 @@ def test_packed_arguments_are_the_struct(struct, pack):
     assert len(packed) == ctypes.sizeof(struct)
     back = struct.from_buffer_copy(packed)
     assert [getattr(back, f) for f, _ in struct._fields_] == values
+
+
+@pytest.mark.parametrize("which,change", [("tree", dict(max_q=2 ** 40)), ("append", dict(k_stride=2 ** 63)),
+                                          ("accept", dict(width=-2 ** 31 - 1))])
+def test_packed_arguments_that_do_not_fit(which, change):
+    struct, good = CALLS[which][1:]
+    with pytest.raises(ValueError, match=struct.__name__):
+        _abi.packer(struct)(*[{**good, **change}[f] or 0 for f, _ in struct._fields_])

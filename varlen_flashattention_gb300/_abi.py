@@ -171,7 +171,14 @@ _CODES = {c_void_p: "P", c_i32: "i", c_i64: "q", c_f32: "f"}
 def packer(args):
     """A function that packs the fields of an argument struct, in order, into the bytes of the C
     struct (0 for a null pointer): a third of the time that filling the ctypes structure takes."""
-    return struct.Struct("@" + "".join(_CODES[t] for _, t in args._fields_) + "0P").pack
+    pack = struct.Struct("@" + "".join(_CODES[t] for _, t in args._fields_) + "0P").pack
+
+    def fields(*values):
+        try:
+            return pack(*values)
+        except struct.error as e:  # a size does not fit its field
+            raise ValueError(f"{args.__name__}: {e}") from None
+    return fields
 
 
 pack_cache_append_rope = packer(CacheAppendRopeArgs)

@@ -326,6 +326,12 @@ TreeLayoutBytes tree_layout(const jfa_decode_tree_args& a, int sms) {
 
 // ------------------------------------------------------------------ validation
 
+// Whether `bytes` from one place on and `other_bytes` from another share any.
+bool overlap(const void* p, int64_t bytes, const void* other, int64_t other_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(other);
+  return bytes > 0 && other_bytes > 0 && a < b + static_cast<uint64_t>(other_bytes) && b < a + static_cast<uint64_t>(bytes);
+}
+
 // What the calls on the bf16 paged cache of speculative decoding have in common.
 jfa_status check_paged_cache(const void* kc, const void* vc, const int32_t* table, const int32_t* seqlens,
                              const int32_t* offsets, int32_t batch, int32_t kv_heads, int32_t head_dim,
@@ -1144,7 +1150,8 @@ jfa_status jfa_cache_append_rope(const jfa_cache_append_rope_args* a, void* ws, 
   const jfa_status st = check_paged_cache(a->k_cache, a->v_cache, a->page_table, a->seqlens_k, a->new_offsets, a->batch,
                                           a->kv_heads, a->head_dim, a->page_size, a->num_pages, a->max_pages);
   if (st != JFA_OK) return st;
-  if (a->total_new < 0 || a->total_new == INT32_MAX || (a->batch == 0 && a->total_new > 0)) return JFA_ERR_INVALID_ARG;
+  if (a->total_new < 0 || a->total_new > INT32_MAX - 256 || (a->batch == 0 && a->total_new > 0))
+    return JFA_ERR_INVALID_ARG;
   if (a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 16 != 0 || a->table_rows < 0)
     return JFA_ERR_INVALID_ARG;
   if (a->interleaved != 0 && a->interleaved != 1) return JFA_ERR_INVALID_ARG;
@@ -1157,7 +1164,10 @@ jfa_status jfa_cache_append_rope(const jfa_cache_append_rope_args* a, void* ws, 
     if (a->q) {
       if (!aligned(a->q, 16) || !aligned(a->q_out, 16) || !stride_ok(a->q_stride, a->q_heads)) return JFA_ERR_INVALID_ARG;
       // in place only if a row of q_out is the same row of q
-      if (a->q_out == a->q && a->q_stride != static_cast<int64_t>(a->q_heads) * a->head_dim) return JFA_ERR_INVALID_ARG;
+      const int64_t row = static_cast<int64_t>(a->q_heads) * a->head_dim;
+      if (!(a->q_out == a->q && a->q_stride == row) &&
+          overlap(a->q_out, 2 * a->total_new * row, a->q, 2 * ((a->total_new - 1) * a->q_stride + row)))
+        return JFA_ERR_INVALID_ARG;
     }
     if (a->rot_dim > 0 && a->table_rows > 0 && (!aligned(a->cos_table, 16) || !aligned(a->sin_table, 16)))
       return JFA_ERR_INVALID_ARG;
@@ -1188,6 +1198,8 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   if (tiles * a->kv_heads * 32 >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
   const bool work = a->batch > 0 && a->total_q > 0;
   if (work && (!aligned(a->q, 16) || !aligned(a->o, 16) || !aligned(a->lse, 4))) return JFA_ERR_INVALID_ARG;
+  const int64_t row_bytes = 2ll * a->q_heads * a->head_dim;  // several CTAs read a row of q, one writes o's
+  if (work && overlap(a->o, a->total_q * row_bytes, a->q, a->total_q * row_bytes)) return JFA_ERR_INVALID_ARG;
   if (a->tree_mask && !aligned(a->tree_mask, 8)) return JFA_ERR_INVALID_ARG;
   if (!aligned(ws, 256) || !events_ok(a->main_kernel_events)) return JFA_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -1208,7 +1220,7 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   buf.part_o = reinterpret_cast<float*>(w + L.part_o);
   buf.row_tiles = L.row_tiles;
   // Boxes of tokens that lie side by side in a page, whole swizzle atoms of 8 rows; pages that 8 does not
-  // divide are read row by row, in part through boxes one row high.
+  // divide are copied row by row, and the maps of K and V not used.
   int box = a->page_size & -a->page_size;
   box = box < 8 ? 1 : std::min(box, kTile);
   const int group = a->q_heads / a->kv_heads;
@@ -1233,7 +1245,11 @@ jfa_status jfa_cache_accept(const jfa_cache_accept_args* a, void* ws, size_t ws_
   if (a->width > kTreeMaxNodes) return JFA_ERR_UNSUPPORTED;
   if (a->batch > 0 && (!aligned(a->counts, 4) || !aligned(a->new_seqlens, 4) || (a->width > 0 && !aligned(a->accepted, 4))))
     return JFA_ERR_INVALID_ARG;
-  if (a->batch > 0 && a->new_seqlens == a->seqlens_k) return JFA_ERR_INVALID_ARG;  // other blocks still read them
+  const int64_t out = 4ll * a->batch;  // written while other blocks read what the call is given
+  if (overlap(a->new_seqlens, out, a->seqlens_k, out) || overlap(a->new_seqlens, out, a->counts, out) ||
+      overlap(a->new_seqlens, out, a->q_offsets, out + 4) || overlap(a->new_seqlens, out, a->accepted, out * a->width) ||
+      overlap(a->new_seqlens, out, a->page_table, out * a->max_pages))
+    return JFA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(a->batch) * a->kv_heads >= int64_t(1) << 29) return JFA_ERR_INVALID_ARG;  // blocks of the grid
   if (!aligned(ws, 256)) return JFA_ERR_INVALID_ARG;
   if (ws_bytes < kStatusBytes) return JFA_ERR_WORKSPACE_TOO_SMALL;
