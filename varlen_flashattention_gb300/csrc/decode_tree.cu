@@ -24,8 +24,9 @@
 //
 // Tiles are gathered through the page table: by TMA in boxes of as many tokens as
 // lie side by side (the largest power of two that divides the page size); for
-// pages that 8 does not divide row by row with cp.async (73% of the copy rate;
-// TMA's gather of four rows, measured in its place, 56%).
+// pages that 8 does not divide row by row with cp.async, whose copies arrive at the
+// tile's barrier themselves (76% of the copy rate; waited for by their warp before
+// it announced the tile, 72%; TMA's gather of four rows, 56%).
 // Drafts are the last tokens, so only a line's last one or two tiles have a
 // mask. In those V rows that some row may not see are checked first: what is
 // not finite there becomes 0 for the product, since 0 * NaN would reach every
@@ -213,11 +214,11 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives at the barrier once the thread's copies so far have been written.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Eight bf16 values without infinities and NaN; the values of a word that are finite, 0 for the others.
 __device__ __forceinline__ bool all_finite(const uint4& v) {
@@ -313,11 +314,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kSlotsK; ++i) {
-      ptx::mbar_init(k_full + i, 1);
+      ptx::mbar_init(k_full + i, p.box > 1 ? 1 : 32);  // row by row every lane arrives
       ptx::mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < kSlotsV; ++i) {
-      ptx::mbar_init(v_full + i, 1);
+      ptx::mbar_init(v_full + i, p.box > 1 ? 1 : 32);
       ptx::mbar_init(v_empty + i, 1);
     }
     for (int i = 0; i < kItemRing; ++i) {
@@ -531,16 +532,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint32_t slot = 0, phase = 1, loads = 0, nq = 0;
     bool ok = true, bad = false;
     const int box = p.box;
-    // Row by row, a tile's copies are waited for when the next tile's are on their way, or at the latest before
-    // this warp waits for anything else: `due` is the slot of a tile that has not been announced.
     const char* cache = reinterpret_cast<const char*>(is_v ? p.v_cache : p.k_cache);
-    int due = -1;
-    auto announce = [&]() {
-      ptx::fence_proxy_async_smem();  // the products read what ordinary copies have written
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(full + due);
-      due = -1;
-    };
     auto copy_rows = [&](uint32_t dst, const int (&y)[4], int valid) {
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a step
       const int c = lane % kLanes, sub = lane / kLanes;
@@ -552,11 +544,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int i = 0; i < 8 / kRows; ++i) swizzled[i] = dst + (((c & 7) ^ (i * kRows + sub)) << 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (e == 2 && due >= 0) {  // the last tile is announced on the way
-          cp_async_commit();
-          cp_async_wait<1>();
-          announce();
-        }
 #pragma unroll 2
         for (int r8 = 0; r8 < 32; r8 += 8)
 #pragma unroll
@@ -566,7 +553,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (r + sub < valid) cp_async16(swizzled[i] + r * 128, src + from * row_bytes);
           }
       }
-      cp_async_commit();
     };
     // The tokens of a tile whose pages this lane looks up: the first of a box (as many lanes as boxes, once
     // for each atom), or every 32nd; past the sequence's end its last token again.
@@ -615,12 +601,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         uint8_t* dst = ring + slot * Lay::kTileBytes;
-        if (box == 1) {
-          if (due >= 0 && !ptx::warp_all(ptx::mbar_test(empty + slot, phase))) {
-            cp_async_wait<0>();
-            announce();
-          }
-        }
         ok = ptx::warp_all(ptx::mbar_wait(empty + slot, phase, ctl, status, kSiteTreeProdSlot, budget));
         if (!ok) break;
         if (box > 1) {
@@ -635,7 +615,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           __syncwarp();
         } else {
           copy_rows(ptx::smem_u32(dst), y, valid);
-          due = static_cast<int>(slot);
+          cp_async_arrive(full + slot);
         }
         ++loads;
         if (++slot == slots) {
@@ -643,12 +623,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           phase ^= 1;
         }
       }
-      if (due >= 0) {
-        cp_async_wait<0>();
-        announce();
-      }
     }
-    if (box == 1) cp_async_wait<0>();
+    cp_async_wait_all();
     if (__any_sync(0xffffffffu, bad) && lane == 0) {
       atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
       atomicCAS(status + 1, 0, kSiteTreeInput);
@@ -679,6 +655,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     auto k_wait = [&](bool ahead = false) -> uint32_t {
       const uint32_t slot = kslot;
       wait(k_full + slot, kphase, kSiteTreeMmaSlot, ahead);
+      if (p.box == 1) ptx::fence_proxy_async_smem();  // the products read what ordinary copies have written
       if (++kslot == kSlotsK) {
         kslot = 0;
         kphase ^= 1;
@@ -688,6 +665,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     auto v_wait = [&](bool ahead = false) -> uint32_t {
       const uint32_t slot = vslot;
       wait(v_full + slot, vphase, kSiteTreeMmaSlot, ahead);
+      if (p.box == 1) ptx::fence_proxy_async_smem();
       if (++vslot == kSlotsV) {
         vslot = 0;
         vphase ^= 1;
