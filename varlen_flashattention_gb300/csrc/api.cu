@@ -86,7 +86,8 @@ bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols
 
 // 2-D bf16 view [rows, cols] (cols contiguous) read in 128-row x 64-column
 // boxes with the 128-byte swizzle the tcgen05 descriptors expect.
-bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = kTile) {
+bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = kTile,
+                    CUtensorMapL2promotion fetch = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   if (rows == 0) rows = 1;  // nothing is read from an empty tensor; the map must still be valid
@@ -95,8 +96,8 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
   const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 // fp32 [rows, cols] accumulator read and reduced in 32-column x 128-row boxes
@@ -1226,10 +1227,14 @@ jfa_status jfa_decode_tree(const jfa_decode_tree_args* a, void* ws, size_t ws_by
   const int group = a->q_heads / a->kv_heads;
   const uint64_t rows = static_cast<uint64_t>(a->num_pages) * a->page_size;
   const uint64_t cols = static_cast<uint64_t>(a->kv_heads) * a->head_dim;
+  // What a load fetches into L2: no more than one head's row, since the next head's is another CTA's, later
+  // (32 x 1k-32k tokens of 8 heads of 64: 198 us, with 256 bytes 250).
+  const CUtensorMapL2promotion fetch =
+      a->head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   CUtensorMap tq, tk, tv;  // without pages no tile is loaded; the maps must still be valid
   if (!make_tmap_bf16_heads(&tq, a->q, a->total_q, a->q_heads, a->head_dim, group, tree_nodes_per_tile(group)) ||
-      !make_tmap_bf16(&tk, rows ? a->k_cache : a->q, rows, cols, box) ||
-      !make_tmap_bf16(&tv, rows ? a->v_cache : a->q, rows, cols, box))
+      !make_tmap_bf16(&tk, rows ? a->k_cache : a->q, rows, cols, box, fetch) ||
+      !make_tmap_bf16(&tv, rows ? a->v_cache : a->q, rows, cols, box, fetch))
     return JFA_ERR_CUDA;
   return cuda_status(launch_decode_tree(*a, buf, tq, tk, tv, box, wait_budget_ns(), sms, stream));
 }
