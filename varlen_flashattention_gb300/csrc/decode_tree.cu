@@ -25,8 +25,8 @@
 // Tiles are gathered through the page table: by TMA in boxes of as many tokens as
 // lie side by side (the largest power of two that divides the page size); for
 // pages that 8 does not divide row by row with cp.async, whose copies arrive at the
-// tile's barrier themselves (76% of the copy rate; waited for by their warp before
-// it announced the tile, 72%; TMA's gather of four rows, 56%).
+// tile's barrier themselves (95% of the copy rate; waited for by their warp before it
+// announced the tile, and looked up one by one, 72%; TMA's gather of four rows, 56%).
 // Drafts are the last tokens, so only a line's last one or two tiles have a
 // mask. In those V rows that some row may not see are checked first: what is
 // not finite there becomes 0 for the product, since 0 * NaN would reach every
@@ -544,14 +544,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int i = 0; i < 8 / kRows; ++i) swizzled[i] = dst + (((c & 7) ^ (i * kRows + sub)) << 4);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-#pragma unroll 2
-        for (int r8 = 0; r8 < 32; r8 += 8)
+        int from[32 / kRows];  // all looked up before the first copy: a shuffle's latency once
 #pragma unroll
-          for (int i = 0; i < 8 / kRows; ++i) {
-            const int r = 32 * e + r8 + i * kRows;  // and sub more
-            const int from = __shfl_sync(0xffffffffu, y[e], r8 + i * kRows + sub);
-            if (r + sub < valid) cp_async16(swizzled[i] + r * 128, src + from * row_bytes);
-          }
+        for (int i = 0; i < 32 / kRows; ++i) from[i] = __shfl_sync(0xffffffffu, y[e], i * kRows + sub);
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const int r = 32 * e + i * kRows;  // and sub more
+          if (r + sub < valid) cp_async16(swizzled[i % (8 / kRows)] + r * 128, src + from[i] * row_bytes);
+        }
       }
     };
     // The tokens of a tile whose pages this lane looks up: the first of a box (as many lanes as boxes, once
