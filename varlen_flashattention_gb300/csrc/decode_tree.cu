@@ -220,14 +220,15 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Eight bf16 values without infinities and NaN; the values of a word that are finite, 0 for the others.
-__device__ __forceinline__ bool all_finite(const uint4& v) {
+// acc + 0 * v in the halves: NaN from then on once a value is infinite or NaN.
+__device__ __forceinline__ __nv_bfloat162 not_finite(__nv_bfloat162 acc, const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool ok = true;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
-  return ok;
+  for (int i = 0; i < 4; ++i)
+    acc = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(w + i), __nv_bfloat162(0.f, 0.f), acc);
+  return acc;
 }
+// The values of a word that are finite, 0 for the others.
 __device__ __forceinline__ uint32_t keep_finite(uint32_t w) {
   if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
@@ -489,10 +490,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
           for (int e = 0; e < kAhead; ++e)
             x[e] = r0 + e * kRows < kTile ? *reinterpret_cast<uint4*>(col + (r0 + e * kRows) * 128) : make_uint4(0, 0, 0, 0);
-          bool fine = true;
+          __nv_bfloat162 acc(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < kAhead; ++e) fine = fine && all_finite(x[e]);
-          if (fine) continue;
+          for (int e = 0; e < kAhead; ++e) acc = not_finite(acc, x[e]);
+          if (!__hisnan(acc.x) && !__hisnan(acc.y)) continue;
 #pragma unroll 1
           for (int e = 0; e < kAhead; ++e) {
             const int r = r0 + e * kRows, draft = ask.y + r;
