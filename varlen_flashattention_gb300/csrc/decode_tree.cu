@@ -194,10 +194,6 @@ struct TreeWalk {
     I.n = n;
     left -= I.t1 - I.t0;
     x = I.t1;
-    if (x == nt) {
-      left -= min(left, static_cast<uint32_t>(kLineCost));
-      next_line(p);
-    }
     return true;
   }
 };
@@ -455,11 +451,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // tile with drafts, which the MMA warp asks for. What is not finite there, of a draft that some row may not see or
     // behind the last token, becomes 0 for the product; drafts with such values are flagged for the item's end.
     TreeItem J{};
-    bool more = walk.next(p, J), given = false;
+    bool more = true, due = true, given = false;
     uint32_t items_out = 0, scans = 0;
     while (true) {
       bool idle = true;
-      if (!given) {
+      if (due) {  // the walk's only copy: what runs once an item has to be small to stay in the instruction caches
+        more = walk.next(p, J);
+        due = idle = false;
+      } else if (!given) {
         const uint32_t e = items_out % kItemRing;
         if (ptx::warp_all(ptx::mbar_test(item_empty + e, ((items_out / kItemRing) & 1) ^ 1))) {
           idle = false;
@@ -471,8 +470,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           __syncwarp();
           ++items_out;
+          due = more;
           given = !more;
-          if (more) more = walk.next(p, J);
         }
       }
       if (ptx::warp_all(ptx::mbar_test(scan_ask, scans & 1))) {
