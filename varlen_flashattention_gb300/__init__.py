@@ -773,6 +773,11 @@ def _paged_inputs(k_cache, v_cache, page_table, seqlens_k, offsets, offsets_name
 def _need_rows(t, name, heads, d, rows):
     """bf16 [rows, heads, d] whose rows may lie apart (a view of a fused projection's
     output); returns the row stride in elements."""
+    if type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.dim() == 3 and \
+            t.shape == (t.shape[0] if rows is None else rows, heads, d):
+        stride, inner, last = t.stride()
+        if last == 1 and inner == d and stride >= heads * d and stride % 8 == 0:
+            return stride  # the usual case; what follows names what is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
