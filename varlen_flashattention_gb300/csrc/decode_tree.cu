@@ -37,6 +37,13 @@
 // which walks the CTA's range and hands its items to the others through a ring in
 // shared memory. (With a walk in each role, the code that only item borders run came
 // from DRAM again and again, past the stream of K and V in L2: an item cost 7.7 us.)
+//
+// Measured, 8 KV heads of 128, pages of 16, device time with the join: 32 x 1k-32k tokens,
+// 4 rows a head 337 us (98% of the copy rate), 64 rows 347 (96%), 256 rows 416 (79%). Where
+// rows are many the chain of one stream is the bound (softmax 1660 cycles, then its products
+// behind the other stream's, 1024 a pair of tiles, and barriers between): 16 x 0.5k-8k with 512
+// rows on 4 heads 75 us, tensor cores busy 46% of the cycles. Where lines are short it is the
+// chain at a line's end: 512 x 1-300 tokens 155 us, 31% of the copy rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,7 +61,7 @@ namespace {
 
 constexpr int kTreeThreads = 384;
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpWalk = 11;
-constexpr int kItemRing = 4;       // items handed out ahead
+constexpr int kItemRing = 4;        // items handed out ahead
 constexpr int kItemConsumers = 11;  // every warp but the scheduler
 constexpr float kLn2f = 0.6931471805599453f;
 
@@ -118,7 +125,8 @@ __device__ __forceinline__ int row_tiles(const TreeParams& p, int n) {
   return static_cast<int>((static_cast<uint32_t>(n + p.nodes_per_tile - 1) * p.node_tile_mul) >> 16);
 }
 // A line's end (its mask, the last products, the results, the next line's Q) takes about as long as this many
-// tiles, so it counts like them when the work is split.
+// tiles, so it counts like them when the work is split. (16 x 0.5k-8k tokens with 512 rows a head: 84 us if it
+// counts 1, 78 for 2, 75 for 3, 79 for 4; 512 x 1-300 tokens of one row tile 150, 153, 155, 161.)
 constexpr int kLineCost = 3;
 // What all the sequence's lines cost, in tiles (below 2^31: the entry point sees to that).
 __device__ __forceinline__ uint32_t seq_work(const TreeParams& p, int n, int L) {
