@@ -914,11 +914,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           };
 #pragma unroll 1
           for (int half = 1; half >= 0; --half) {
-            ptx::tmem_ld32(s_tmem + 64 * half, sa);
-            ptx::tmem_ld32(s_tmem + 64 * half + 32, sb);
-            ptx::tmem_ld_wait();
-            ptx::reg_fence32(sa);
-            ptx::reg_fence32(sb);
+            if (!half) {  // the upper ones are still here
+              ptx::tmem_ld32(s_tmem, sa);
+              ptx::tmem_ld32(s_tmem + 32, sb);
+              ptx::tmem_ld_wait();
+              ptx::reg_fence32(sa);
+              ptx::reg_fence32(sb);
+            }
             exps(sa, 2 * half);
             exps(sb, 2 * half + 1);
             if (half) {
