@@ -39,8 +39,8 @@
 // from DRAM again and again, past the stream of K and V in L2: an item cost 7.7 us.)
 //
 // Measured, 8 KV heads of 128, pages of 16, device time with the join: 32 x 1k-32k tokens,
-// 4 rows a head 329-338 us by the card (98-100% of the copy rate), 64 rows 338-347 (96-98%), 256
-// rows 409-420 (79%). Where rows are many the chain of one stream is the bound (softmax 1860
+// 4 rows a head 328-338 us by the card (98-100% of the copy rate), 64 rows 339-348 (96-98%), 256
+// rows 406-411 (80%). Where rows are many the chain of one stream is the bound (softmax 1860
 // cycles, then its products behind the other stream's, 1024 each, and barriers between): 16 x
 // 0.5k-8k with 512 rows on 4 heads 74 us, tensor cores busy 46% of the cycles. Where lines are
 // short it is the chain at a line's end: 512 x 1-300 tokens 159 us, 31% of the copy rate.
