@@ -1004,6 +1004,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           rows4[k] = __shfl_sync(0xffffffffu, row_ok ? static_cast<int>(out_row) : -1, (lane & ~3) + k);
+        // A weight of 0 multiplies too: a NaN or an infinity of V stays not finite however small its weight. (A row
+        // that saw nothing has P = 0 and V without such values behind it, so its accumulator is 0.)
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
           uint32_t ov[32];
@@ -1012,13 +1014,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           ptx::reg_fence32(ov);
           float of[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) of[e] = f0 == 0.f ? 0.f : __uint_as_float(ov[e]) * f0;
+          for (int e = 0; e < 32; ++e) of[e] = __uint_as_float(ov[e]) * f0;
           if (both) {
             ptx::tmem_ld32(o_tmem + D + c, ov);
             ptx::tmem_ld_wait();
             ptx::reg_fence32(ov);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) of[e] += f1 == 0.f ? 0.f : __uint_as_float(ov[e]) * f1;
+            for (int e = 0; e < 32; ++e) of[e] += __uint_as_float(ov[e]) * f1;
           }
           if (!whole) {
             if (row_ok) {
@@ -1169,7 +1171,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_tree_join_kernel(const Tr
       for (int e = 0; e < kJoinAhead; ++e) {
         const float wt = ptx::ex2(lse[e] - ref);  // no such part: 0
         sum += wt;
-        if (wt != 0.f) acc.x += wt * o[e].x, acc.y += wt * o[e].y, acc.z += wt * o[e].z, acc.w += wt * o[e].w;
+        // a part whose weight is 0 counts: 0 * NaN, and 0 * infinity, are NaN
+        if (i0 + e < parts) acc.x += wt * o[e].x, acc.y += wt * o[e].y, acc.z += wt * o[e].z, acc.w += wt * o[e].w;
       }
       M = top;
     }
