@@ -1164,9 +1164,9 @@ jfa_status jfa_cache_append_rope(const jfa_cache_append_rope_args* a, void* ws, 
       return JFA_ERR_INVALID_ARG;
     if (a->q) {
       if (!aligned(a->q, 16) || !aligned(a->q_out, 16) || !stride_ok(a->q_stride, a->q_heads)) return JFA_ERR_INVALID_ARG;
-      // in place only if a row of q_out is the same row of q
+      // in place only if a row of q_out is the same row of q (a single one is, whatever its stride)
       const int64_t row = static_cast<int64_t>(a->q_heads) * a->head_dim;
-      if (!(a->q_out == a->q && a->q_stride == row) &&
+      if (!(a->q_out == a->q && (a->q_stride == row || a->total_new == 1)) &&
           overlap(a->q_out, 2 * a->total_new * row, a->q, 2 * ((a->total_new - 1) * a->q_stride + row)))
         return JFA_ERR_INVALID_ARG;
     }
