@@ -525,7 +525,9 @@ typedef struct {
  * that see their token and no others. n_b <= max_q <= 64; q_heads / kv_heads may be any
  * number up to 128. The work is split evenly over the device whatever the lengths; there
  * is no split count to choose. A sequence whose length or offsets are out of range gets
- * O = 0, LSE = -inf (its rows of total_q), and the call reports it. With total_q = 0 there
+ * O = 0, LSE = -inf (its rows of total_q), and the call reports it; so does every sequence of a
+ * call whose work, ceil(L_b / 128) + 3 for each KV head and each 2 floor(128 / group) of its new
+ * tokens begun, adds up to 2^31 or more. With total_q = 0 there
  * is nothing to do, and the arrays are not looked at. */
 typedef struct {
   const void* q;              /* bf16 [total_q, q_heads, head_dim] */

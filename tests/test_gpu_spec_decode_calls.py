@@ -1,5 +1,6 @@
 """Calls of speculative decoding over the bf16 paged cache that other tests leave out: one token of a fused
-projection rotated in place."""
+projection rotated in place, and more work than is numbered."""
+import numpy as np
 import pytest
 import torch
 
@@ -30,3 +31,22 @@ def test_one_token_of_a_fused_projection_in_place(d, Hq, Hkv, interleaved):
                                         check=True)
         assert out is gq and torch.equal(gr[:, Hq:].cpu(), row[:, Hq:])
         check_append(c, g, q, k, v, gq, cos, sin, None, interleaved, cut)
+
+
+def test_more_work_than_is_numbered():
+    """Lines of more than 2^31 tiles together (here over shared pages): reported, and the rows are empty, as those of
+    any sequence that is refused. Rows behind the last sequence stay."""
+    P, H, d, B, mp = 1024, 1024, 64, 33, 8190
+    kc = torch.zeros(1, P, H, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(B, mp, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), mp * P, dtype=torch.int32, device="cuda")
+    new = [2] + [1] * (B - 1)
+    assert (mp * P // 128 + 3) * H * (B - 1) < 2 ** 31 <= (mp * P // 128 + 3) * H * B
+    offs = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).cuda()
+    used = sum(new)
+    q = torch.ones(used + 2, H, d, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.full_like(q, 7), torch.full((used + 2, H), 7.0, device="cuda")
+    with pytest.raises(jfa.JfaError, match="501"):
+        jfa.jfa_decode_tree(q, kc, kc, table, lens, offs, max_q=2, o=o, lse=lse, check=True)
+    assert (o[:used] == 0).all() and torch.isneginf(lse[:used]).all()
+    assert (o[used:] == 7).all() and (lse[used:] == 7).all()

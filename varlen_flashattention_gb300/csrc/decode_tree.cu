@@ -364,18 +364,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // The work of all lines is summed, then the sequence in which this CTA's range begins is found.
   unsigned long long sum = 0;
   int q0 = 0, n = 0, L = 0;  // the sequence that this thread numbers (its only one in batches up to the block)
+  // Reports the input; the rows of q from first_row to end_row are empty, a share of them a CTA.
+  auto refuse = [&](int first_row, int end_row) {
+    atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
+    atomicCAS(status + 1, 0, kSiteTreeInput);
+    const int64_t to = static_cast<int64_t>(min(end_row, p.total_q)) * p.hq;
+    for (int64_t i = static_cast<int64_t>(max(first_row, 0)) * p.hq + cta; i < to; i += gridDim.x) {
+      p.lse[i] = -INFINITY;
+      for (int c = 0; c < D; c += 8) ptx::st_v4(p.o + i * D + c, 0, 0, 0, 0);
+    }
+  };
   {
     unsigned long long mine = 0;
     for (int b = tid; b < p.batch; b += kTreeThreads) {
-      if (!tree_seq(p, b, q0, n, L)) {  // its rows are empty, a share of them a CTA
-        atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
-        atomicCAS(status + 1, 0, kSiteTreeInput);
-        const int64_t q1 = min(p.q_offsets[b + 1], p.total_q);
-        for (int64_t i = static_cast<int64_t>(max(q0, 0)) * p.hq + cta; i < q1 * p.hq; i += gridDim.x) {
-          p.lse[i] = -INFINITY;
-          for (int c = 0; c < D; c += 8) ptx::st_v4(p.o + i * D + c, 0, 0, 0, 0);
-        }
-      }
+      if (!tree_seq(p, b, q0, n, L)) refuse(q0, p.q_offsets[b + 1]);
       mine += seq_work(p, n, L);
     }
 #pragma unroll
@@ -385,11 +387,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
     for (int i = 0; i < kTreeThreads / 32; ++i) sum += s_sum[i];
   }
-  if (sum >= (1ull << 31)) {  // 2^31 tiles are 2^45 bytes of K and V at least: no device holds them
-    if (tid == 0) {
-      atomicCAS(status, JFA_OK, JFA_ERR_BAD_INPUT);
-      atomicCAS(status + 1, 0, kSiteTreeInput);
-    }
+  // The work is numbered with 31 bits; 2^31 tiles would take this kernel some twenty seconds (1.5 us a tile of 128 x
+  // 128 at the copy rate, 152 at a time). Lines that share pages can come to more: no sequence is done then.
+  if (sum >= (1ull << 31)) {
+    for (int b = tid; b < p.batch; b += kTreeThreads) refuse(p.q_offsets[b], p.q_offsets[b + 1]);
     sum = 0;
   }
   // one range a CTA; with fewer tiles than CTAs the last ones have none
