@@ -503,7 +503,7 @@ typedef struct {
   const int32_t* positions;   /* optional: int32 [total_new], 0 <= p < table_rows */
   const float* cos_table;     /* fp32 [table_rows, rot_dim / 2] */
   const float* sin_table;     /* as cos_table */
-  void* q_out;                /* out (with q): bf16 [total_new, q_heads, head_dim]; q itself if its rows touch or there is one, or apart from it */
+  void* q_out;                /* out (with q): bf16 [total_new, q_heads, head_dim]; q itself if its rows touch or there is one, or apart from it; apart from k, v */
   void* k_cache;              /* in/out: bf16 [num_pages, page_size, kv_heads, head_dim] */
   void* v_cache;              /* in/out: as k_cache */
   const int32_t* page_table;  /* int32 [batch, max_pages]; entries past ceil(L_b/page_size) are not read */

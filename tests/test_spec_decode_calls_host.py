@@ -12,10 +12,22 @@ def _checked(lib, which, **change):
     return getattr(lib, name)(ctypes.byref(struct(**{**good, **change})), X, 128, None)
 
 
+APART = dict(k=64 * X, v=128 * X)
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(), WS), (dict(q_out=X), WS), (dict(q_out=X, q_stride=1024), INV),
     (dict(q_out=X, q_stride=1024, total_new=1), WS),  # a single row lies on itself
     (dict(q_out=X + 16, q_stride=1024, total_new=1), INV), (dict(q_out=X + 1024, q_stride=2048, total_new=1), WS),
     (dict(q_out=X + 16, total_new=1), INV), (dict(q_out=X, total_new=1), WS)], ids=lambda x: str(x))
 def test_rotated_in_place(lib, change, status):  # noqa: F811
-    assert _checked(lib, "append", **change) == status
+    assert _checked(lib, "append", **{**APART, **change}) == status
+
+
+# five rows of 512 bytes of k and v, 1024 apart: 4608 bytes from 64 X and 128 X on; q_out takes 5120
+@pytest.mark.parametrize("change,status", [
+    (dict(q_out=64 * X), INV), (dict(q_out=128 * X), INV), (dict(q_out=64 * X - 5120), WS), (dict(q_out=64 * X - 5104), INV),
+    (dict(q_out=128 * X + 4608), WS), (dict(q_out=128 * X + 4592), INV), (dict(q_out=64 * X + 512, total_new=1), WS),
+    (dict(q_out=64 * X + 496, total_new=1), INV), (dict(q=None, q_out=64 * X), WS)], ids=lambda x: str(x))
+def test_rotated_over_new_keys_and_values(lib, change, status):  # noqa: F811
+    assert _checked(lib, "append", **{**APART, "k_stride": 512, "v_stride": 512, **change}) == status

@@ -809,8 +809,8 @@ def jfa_cache_append_rope(q, k, v, k_cache, v_cache, page_table, seqlens_k, new_
     max_pages]. cos, sin: fp32 [positions, rot_dim / 2] with rot_dim a multiple of 16 up to d, or both
     None (nothing turns). positions (optional, int32 [total_new]): the tables' rows, by default the
     tokens' places in their sequences. Pairs are columns (j, j + rot_dim / 2), or neighbours if
-    interleaved. Returns the rotated Q (q_out, which may be q itself; None without q); its rows behind
-    new_offsets[B] are not written."""
+    interleaved. Returns the rotated Q (q_out, which may be q itself, and no part of k or v; None
+    without q); its rows behind new_offsets[B] are not written."""
     try:
         num_pages, P, Hkv, d = k_cache.shape
         B, mp = page_table.shape

@@ -1169,6 +1169,11 @@ jfa_status jfa_cache_append_rope(const jfa_cache_append_rope_args* a, void* ws, 
       if (!(a->q_out == a->q && (a->q_stride == row || a->total_new == 1)) &&
           overlap(a->q_out, 2 * a->total_new * row, a->q, 2 * ((a->total_new - 1) * a->q_stride + row)))
         return JFA_ERR_INVALID_ARG;
+      // nor over the rows of k and v, which other blocks read
+      const int64_t kv_row = static_cast<int64_t>(a->kv_heads) * a->head_dim;
+      if (overlap(a->q_out, 2 * a->total_new * row, a->k, 2 * ((a->total_new - 1) * a->k_stride + kv_row)) ||
+          overlap(a->q_out, 2 * a->total_new * row, a->v, 2 * ((a->total_new - 1) * a->v_stride + kv_row)))
+        return JFA_ERR_INVALID_ARG;
     }
     if (a->rot_dim > 0 && a->table_rows > 0 && (!aligned(a->cos_table, 16) || !aligned(a->sin_table, 16)))
       return JFA_ERR_INVALID_ARG;
