@@ -3,7 +3,6 @@ import ctypes
 
 import pytest
 
-from varlen_flashattention_gb300 import _abi
 from tests.test_spec_decode_host import CALLS, INV, WS, X, lib  # noqa: F401 (lib: the fixture)
 
 
@@ -32,11 +31,3 @@ def test_rotated_in_place(lib, change, status):  # noqa: F811
     (dict(q_out=64 * X + 496, total_new=1), INV), (dict(q=None, q_out=64 * X), WS)], ids=lambda x: str(x))
 def test_rotated_over_new_keys_and_values(lib, change, status):  # noqa: F811
     assert _checked(lib, "append", **{**APART, "k_stride": 512, "v_stride": 512, **change}) == status
-
-
-@pytest.mark.parametrize("scale", [1e39, -1e300])
-def test_scale_past_fp32(scale):
-    """Refused as a size that does not fit its field is."""
-    struct, good = CALLS["tree"][1:]
-    with pytest.raises(ValueError, match="DecodeTreeArgs"):
-        _abi.packer(struct)(*[{**good, "scale": scale}[f] or 0 for f, _ in struct._fields_])

@@ -176,7 +176,7 @@ def packer(args):
     def fields(*values):
         try:
             return pack(*values)
-        except (struct.error, OverflowError) as e:  # a size or a scale does not fit its field
+        except struct.error as e:  # a size does not fit its field
             raise ValueError(f"{args.__name__}: {e}") from None
     return fields
 
