@@ -1,9 +1,12 @@
-"""Calls of speculative decoding over the bf16 paged cache without a GPU: arguments that the checks let pass."""
+"""Calls of speculative decoding over the bf16 paged cache without a GPU: arguments that the checks let pass,
+and a wait whose running out no GPU can show unless it has stopped answering."""
 import ctypes
+import os
+import re
 
 import pytest
 
-from tests.test_spec_decode_host import CALLS, INV, WS, X, lib  # noqa: F401 (lib: the fixture)
+from tests.test_spec_decode_host import CALLS, INV, ROOT, WS, X, lib  # noqa: F401 (lib: the fixture)
 
 
 def _checked(lib, which, **change):
@@ -31,3 +34,13 @@ def test_rotated_in_place(lib, change, status):  # noqa: F811
     (dict(q_out=64 * X + 496, total_new=1), INV), (dict(q=None, q_out=64 * X), WS)], ids=lambda x: str(x))
 def test_rotated_over_new_keys_and_values(lib, change, status):  # noqa: F811
     assert _checked(lib, "append", **{**APART, "k_stride": 512, "v_stride": 512, **change}) == status
+
+
+def test_a_drain_that_runs_out_ends_the_scheduler():
+    """The tree decode's scheduler leaves when the products have drained or the abort flag is raised, and has no limit of
+    its own: whoever gives up waiting for the drain has to raise the flag (read in the source)."""
+    with open(os.path.join(ROOT, "varlen_flashattention_gb300", "csrc", "decode_tree.cu")) as f:
+        code = f.read()
+    assert "if (given && ptx::warp_all(ptx::mbar_test(drain, 0))) break;" in code
+    waits = re.findall(r"^.*mbar_wait\(drain,.*$", code, re.M)
+    assert waits and all(re.search(r"if \(!ptx::mbar_wait\(drain,.*\) ctl->abort = 1;", w) for w in waits)

@@ -793,7 +793,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (ptx::elect_one()) ptx::mma_commit(drain);
     __syncwarp();
     ptx::CtaCtl no_abort{0, 0};
-    ptx::mbar_wait(drain, 0, &no_abort, nullptr, kSiteTreeDrain, budget);
+    // the scheduler waits for it too, with no limit of its own but the abort flag
+    if (!ptx::mbar_wait(drain, 0, &no_abort, status, kSiteTreeDrain, budget)) ctl->abort = 1;
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and epilogue (warps 0-7)
