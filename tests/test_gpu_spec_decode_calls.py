@@ -1,11 +1,12 @@
 """Calls of speculative decoding over the bf16 paged cache that other tests leave out: one token of a fused
-projection rotated in place, and more work than is numbered."""
+projection rotated in place, more work than is numbered, and a captured turn whose batch changes between replays."""
 import numpy as np
 import pytest
 import torch
 
 import varlen_flashattention_gb300 as jfa
-from tests.test_gpu_spec_decode import _bf16, cache, check_append, dev, make, tables
+from tests.test_gpu_spec_decode import _bf16, as_i64, cache, check_append, dev, make, tables, words
+from tests.test_gpu_spec_decode_edges import _results, _same, _turn
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,40 @@ def test_more_work_than_is_numbered():
         jfa.jfa_decode_tree(q, kc, kc, table, lens, offs, max_q=2, o=o, lse=lse, check=True)
     assert (o[:used] == 0).all() and torch.isneginf(lse[:used]).all()
     assert (o[used:] == 7).all() and (lse[used:] == 7).all()
+
+
+def _state(seed, before, new):
+    """A turn's tensors for a batch of these lengths; batches of as many new tokens fill tensors of the same sizes."""
+    need = [-(-(a + n) // 16) for a, n in zip(before, new)]
+    c = make(seed, before, new, 2, 128, 16, spare=90 - sum(need), wide=60 - max(need))
+    g, rng, n = dev(c), c["rng"], sum(new)
+    s = {x: _bf16(rng, n, h, 128).cuda() for x, h in (("q", 8), ("k", 2), ("v", 2))}
+    s["cos"], s["sin"] = (torch.from_numpy(x).cuda() for x in tables(1000, 128))
+    s["mask"] = as_i64(words(rng, new, "tree"))
+    s["count"] = torch.tensor([int(rng.integers(0, min(5, m) + 1)) for m in new], dtype=torch.int32).cuda()
+    s["path"] = torch.from_numpy(np.stack([rng.integers(0, max(m, 1), 5) for m in new]).astype(np.int32)).cuda()
+    s["qr"], s["o"] = torch.zeros_like(s["q"]), torch.zeros_like(s["q"])
+    s["lse"], s["left"] = torch.zeros(n, 8, device="cuda"), torch.zeros_like(g["lens"])
+    return g, s
+
+
+def test_captured_turn_replays_with_another_batch():
+    """A graph reads lengths and offsets when it runs: the same turn for sequences of other lengths and other numbers of
+    new tokens (lines, cuts and parts all move), for the first ones again, and for a batch that is partly empty."""
+    batches = [([100, 700, 5, 33, 256], [12, 1, 0, 30, 7]), ([33, 5, 256, 700, 100], [0, 30, 12, 1, 7]),
+               ([0, 640, 1, 300, 120], [1, 9, 33, 0, 7]), ([0, 0, 0, 0, 890], [0, 0, 0, 0, 50])]
+    g, s = _state(210, *batches[0])
+    _turn(g, s)  # sets the kernels up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _turn(g, s)
+    for seed, which in enumerate((0, 1, 2, 3, 0)):
+        g2, s2 = _state(220 + seed, *batches[which])
+        for mine, other in ((g, g2), (s, s2)):
+            for x in other:
+                assert mine[x].shape == other[x].shape, x
+                mine[x].copy_(other[x])
+        _turn(g2, s2)
+        graph.replay()
+        assert _same(_results(g, s), _results(g2, s2)), which
