@@ -42,7 +42,7 @@ struct AppendRopeParams {
   const int32_t* page_table;
   const int32_t* seqlens;
   int64_t qs, ks, vs;
-  int32_t batch, hq, hkv, rot, interleaved, table_rows, num_pages, max_pages, total_new;
+  int32_t batch, hq, hkv, rot, table_rows, num_pages, max_pages, total_new;
   int32_t share;  // warps that share a token: kAppendWarps, or 1
   FastDiv page;
   int32_t* status;
@@ -222,7 +222,7 @@ struct AcceptParams {
   const int32_t* offsets;
   const int32_t* accepted;
   const int32_t* counts;
-  int32_t batch, hkv, num_pages, max_pages, width;
+  int32_t batch, num_pages, max_pages, width;
   FastDiv page;
   int32_t* new_seqlens;
   int32_t* status;
@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kReportThreads) accept_kernel(const AcceptPara
       for (int e = 0; e < kAcceptAhead; ++e)
         if (k0 + e < count && s_from[k0 + e] != s_to[k0 + e]) c[s_to[k0 + e] * pieces] = x[e];
     }
-  } else {  // any order, an index more than once: all is read before any is written
+  } else {
+    // Any order, an index more than once: all is read before any is written. The rows lie in local memory: falling
+    // paths take 10.6 us where rising ones take 6.9 (512 sequences of up to 17 rows), 47.5 against 22.8 (of 64).
     uint4 x[kTreeMaxNodes];
     for (int k = 0; k < count; ++k) x[k] = c[s_from[k] * pieces];
     for (int k = 0; k < count; ++k) c[s_to[k] * pieces] = x[k];
@@ -353,7 +355,6 @@ cudaError_t launch_cache_append_rope(const jfa_cache_append_rope_args& a, int32_
   p.hq = a.q_heads;
   p.hkv = a.kv_heads;
   p.rot = a.rot_dim;
-  p.interleaved = a.interleaved;
   p.table_rows = a.table_rows;
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;
@@ -391,7 +392,6 @@ cudaError_t launch_cache_accept(const jfa_cache_accept_args& a, int32_t* status,
   p.accepted = a.accepted;
   p.counts = a.counts;
   p.batch = a.batch;
-  p.hkv = a.kv_heads;
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;
   p.width = a.width;
