@@ -30,7 +30,8 @@
 // Drafts are the last tokens, so only a line's last one or two tiles have a
 // mask. In those V rows that some row may not see are checked first: what is
 // not finite there becomes 0 for the product, since 0 * NaN would reach every
-// row, and is added to the rows that do see it at the end.
+// row, and is added to the rows that do see it at the end. Where partial results are joined a weight that has
+// underflowed to 0 still multiplies, so that NaN and infinities are kept wherever the line was cut.
 //
 // Roles (384 threads): warps 0-3 and 4-7 the streams' softmax and epilogue, warp
 // 8 K loads, warp 9 Q and V loads, warp 10 MMA issuer, warp 11 the scheduler,
@@ -39,11 +40,11 @@
 // from DRAM again and again, past the stream of K and V in L2: an item cost 7.7 us.)
 //
 // Measured, 8 KV heads of 128, pages of 16, device time with the join: 32 x 1k-32k tokens,
-// 4 rows a head 328-338 us by the card (98-100% of the copy rate), 64 rows 339-348 (96-98%), 256
-// rows 406-411 (80%). Where rows are many the chain of one stream is the bound (softmax 1860
+// 4 rows a head 328-339 us by the card (98-100% of the copy rate), 64 rows 338-348 (96-98%), 256
+// rows 406-427 (79-83%). Where rows are many the chain of one stream is the bound (softmax 1860
 // cycles, then its products behind the other stream's, 1024 each, and barriers between): 16 x
 // 0.5k-8k with 512 rows on 4 heads 74 us, tensor cores busy 46% of the cycles. Where lines are
-// short it is the chain at a line's end: 512 x 1-300 tokens 159 us, 31% of the copy rate.
+// short it is the chain at a line's end: 512 x 1-300 tokens 144-147 us, 33% of the copy rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -125,8 +126,8 @@ __device__ __forceinline__ int row_tiles(const TreeParams& p, int n) {
   return static_cast<int>((static_cast<uint32_t>(n + p.nodes_per_tile - 1) * p.node_tile_mul) >> 16);
 }
 // A line's end (its mask, the last products, the results, the next line's Q) takes about as long as this many
-// tiles, so it counts like them when the work is split. (16 x 0.5k-8k tokens with 512 rows a head: 84 us if it
-// counts 1, 78 for 2, 75 for 3, 79 for 4; 512 x 1-300 tokens of one row tile 150, 153, 155, 161.)
+// tiles, so it counts like them when the work is split. (16 x 0.5k-8k tokens with 512 rows a head: 81 us if it
+// counts 1, 77 for 2, 74 for 3, 78 for 4; 512 x 1-300 tokens of one row tile 138, 140, 144, 149.)
 constexpr int kLineCost = 3;
 // What all the sequence's lines cost, in tiles (below 2^31: the entry point sees to that).
 __device__ __forceinline__ uint32_t seq_work(const TreeParams& p, int n, int L) {
